@@ -16,6 +16,7 @@ HYMBA_OK, HYMBA_ERR_INVALID_ARG, HYMBA_ERR_UNSUPPORTED, HYMBA_ERR_WORKSPACE, HYM
     HYMBA_ERR_TIMEOUT = range(6)
 HYMBA_F32, HYMBA_BF16 = 0, 1
 HYMBA_KV_OWN, HYMBA_KV_PRODUCE, HYMBA_KV_CONSUME = 0, 1, 2
+HYMBA_CACHE_F32, HYMBA_CACHE_BF16, HYMBA_CACHE_E4M3 = 0, 1, 2
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libhymba.so")
 
@@ -27,6 +28,8 @@ ENTRY_POINTS = (
     "hymba_attention", "hymba_branch_norm", "hymba_rmsnorm", "hymba_layer_fwd_noalloc", "hymba_layer_fuses_dt_proj",
     "hymba_check_wait_timeout", "hymba_decode_workspace_size", "hymba_layer_prefill", "hymba_layer_decode",
     "hymba_meta_prefix_size", "hymba_meta_prefix", "hymba_layer_fwd_prefixed",
+    "hymba_paged_kv_append", "hymba_paged_kv_read", "hymba_paged_attention_workspace_size", "hymba_paged_attention",
+    "hymba_quantize_w4", "hymba_dequantize_w4", "hymba_gemm_w4",
 )
 
 # size of the library-owned scratch block behind hymba_layer_fwd_noalloc (HYMBA_NOALLOC_SCRATCH_BYTES)
@@ -52,6 +55,11 @@ class hymba_weights_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "w_in", "w_x", "w_dt", "w_out", "a_log", "b_dt", "beta1", "beta2", "w_gate_up", "w_down",
         "norm1", "norm2", "w_conv", "b_conv", "d_skip")]
+
+
+class hymba_paged_kv_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("pages", "scales", "page_table")] + [(n, ctypes.c_int) for n in (
+        "n_pages", "page_size", "table_ld", "n_kv_heads", "head_dim", "cache_type")]
 
 
 _VP, _SZ, _I, _F = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
@@ -88,6 +96,14 @@ _SIGS = {
                                  _VP, _I, _VP, _VP, _VP, _SZ, _VP]),
     "hymba_layer_decode": (_I, [_VP, ctypes.POINTER(hymba_weights_t), ctypes.POINTER(hymba_cfg_t),
                                 _VP, _I, _I, _VP, _VP, _VP, _SZ, _VP]),
+    "hymba_paged_kv_append": (_I, [ctypes.POINTER(hymba_paged_kv_t), _VP, _VP, _I, _I, _VP, _VP, _I, _I, _VP, _SZ, _VP]),
+    "hymba_paged_kv_read": (_I, [ctypes.POINTER(hymba_paged_kv_t), _VP, _VP, _I, _I, _VP, _VP, _I, _I, _VP, _SZ, _VP]),
+    "hymba_paged_attention_workspace_size": (_SZ, [ctypes.POINTER(hymba_paged_kv_t), _I, _I, _I, _I, _I]),
+    "hymba_paged_attention": (_I, [_VP, _I, ctypes.POINTER(hymba_paged_kv_t), _VP, _I, _I, _VP, _VP, _I, _I, _I, _I, _I,
+                                   _I, _VP, _SZ, _VP]),
+    "hymba_quantize_w4": (_I, [_VP, _VP, _VP, _I, _I, _I, _I, _VP]),
+    "hymba_dequantize_w4": (_I, [_VP, _VP, _VP, _I, _I, _I, _I, _VP]),
+    "hymba_gemm_w4": (_I, [_VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP]),
 }
 
 _lib = None
@@ -153,6 +169,20 @@ def make_weights(p: Dict[str, object]) -> hymba_weights_t:
     for f, _ in hymba_weights_t._fields_:
         setattr(w, f, _ptr(p.get(f)))
     return w
+
+
+def make_paged_kv(pages, page_table, page_size: int, n_kv_heads: int, head_dim: int, cache_type: int,
+                  scales=None) -> hymba_paged_kv_t:
+    """hymba_paged_kv_t over device tensors: `pages` holds [2, n_pages, page_size, Hkv*dh]
+    (any shape of that many elements), `page_table` [batch, table_ld] int32, `scales`
+    [2, n_pages, Hkv, page_size] fp32 for HYMBA_CACHE_E4M3.  The caller keeps the tensors."""
+    kv = hymba_paged_kv_t()
+    kv.pages, kv.scales, kv.page_table = _ptr(pages), _ptr(scales), _ptr(page_table)
+    kv.page_size, kv.n_kv_heads, kv.head_dim, kv.cache_type = page_size, n_kv_heads, head_dim, cache_type
+    row = page_size * n_kv_heads * head_dim
+    kv.n_pages = pages.numel() // (2 * row) if row > 0 else 0
+    kv.table_ld = page_table.shape[-1]
+    return kv
 
 
 # --------------------------------------------------------------------------- entry points
@@ -294,6 +324,46 @@ def hymba_layer_decode(x_t, weights: hymba_weights_t, cfg: hymba_cfg_t, kv_cache
     return load().hymba_layer_decode(_ptr(x_t), ctypes.byref(weights), ctypes.byref(cfg), _ptr(kv_cache),
                                      int(cache_rows), int(pos), _ptr(ssm_state), _ptr(out_t), _ptr(workspace),
                                      _nbytes(workspace), _stream(stream))
+
+
+def hymba_paged_kv_append(kv: hymba_paged_kv_t, k, v, ld: int, batch: int, q_start, kv_len, total_rows: int, dtype: int,
+                          workspace, ws_bytes: Optional[int] = None, stream=None) -> int:
+    wsb = _nbytes(workspace) if ws_bytes is None and workspace is not None else (ws_bytes or 0)
+    return load().hymba_paged_kv_append(ctypes.byref(kv), _ptr(k), _ptr(v), ld, batch, _ptr(q_start), _ptr(kv_len),
+                                        total_rows, dtype, _ptr(workspace), wsb, _stream(stream))
+
+
+def hymba_paged_kv_read(kv: hymba_paged_kv_t, k, v, ld: int, batch: int, q_start, kv_len, total_rows: int, dtype: int,
+                        workspace, ws_bytes: Optional[int] = None, stream=None) -> int:
+    wsb = _nbytes(workspace) if ws_bytes is None and workspace is not None else (ws_bytes or 0)
+    return load().hymba_paged_kv_read(ctypes.byref(kv), _ptr(k), _ptr(v), ld, batch, _ptr(q_start), _ptr(kv_len),
+                                      total_rows, dtype, _ptr(workspace), wsb, _stream(stream))
+
+
+def hymba_paged_attention_workspace_size(kv: hymba_paged_kv_t, batch: int, total_rows: int, max_rows: int,
+                                         n_q_heads: int, dtype: int) -> int:
+    return load().hymba_paged_attention_workspace_size(ctypes.byref(kv), batch, total_rows, max_rows, n_q_heads, dtype)
+
+
+def hymba_paged_attention(q, q_ld: int, kv: hymba_paged_kv_t, out, out_ld: int, batch: int, q_start, kv_len,
+                          total_rows: int, max_rows: int, n_q_heads: int, n_meta: int, window: int, dtype: int,
+                          workspace, ws_bytes: Optional[int] = None, stream=None) -> int:
+    wsb = _nbytes(workspace) if ws_bytes is None and workspace is not None else (ws_bytes or 0)
+    return load().hymba_paged_attention(_ptr(q), q_ld, ctypes.byref(kv), _ptr(out), out_ld, batch, _ptr(q_start),
+                                        _ptr(kv_len), total_rows, max_rows, n_q_heads, n_meta, window, dtype,
+                                        _ptr(workspace), wsb, _stream(stream))
+
+
+def hymba_quantize_w4(w, w_q4, scales, N: int, K: int, group: int, dtype: int, stream=None) -> int:
+    return load().hymba_quantize_w4(_ptr(w), _ptr(w_q4), _ptr(scales), N, K, group, dtype, _stream(stream))
+
+
+def hymba_dequantize_w4(w_q4, scales, w, N: int, K: int, group: int, dtype: int, stream=None) -> int:
+    return load().hymba_dequantize_w4(_ptr(w_q4), _ptr(scales), _ptr(w), N, K, group, dtype, _stream(stream))
+
+
+def hymba_gemm_w4(a, w_q4, scales, c, M: int, N: int, K: int, group: int, dtype: int, stream=None) -> int:
+    return load().hymba_gemm_w4(_ptr(a), _ptr(w_q4), _ptr(scales), _ptr(c), M, N, K, group, dtype, _stream(stream))
 
 
 def hymba_check_wait_timeout(workspace, limit_us: int, stream=None) -> int:

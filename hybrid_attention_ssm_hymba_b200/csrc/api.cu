@@ -1087,7 +1087,8 @@ hymba_status_t hymba_workspace_status(void* workspace, void* stream) {
   if (v != 0) {
     if (cudaMemsetAsync(workspace, 0, sizeof(unsigned), st) != cudaSuccess) return HYMBA_ERR_CUDA;
     if (cudaStreamSynchronize(st) != cudaSuccess) return HYMBA_ERR_CUDA;
-    return v == HYMBA_ERR_TIMEOUT ? HYMBA_ERR_TIMEOUT : HYMBA_ERR_CUDA;
+    if (v == HYMBA_ERR_TIMEOUT) return HYMBA_ERR_TIMEOUT;
+    return v == HYMBA_ERR_INVALID_ARG ? HYMBA_ERR_INVALID_ARG : HYMBA_ERR_CUDA;
   }
   return HYMBA_OK;
 }

@@ -1,0 +1,211 @@
+// paged.cu -- the paged K/V cache of the attention heads (blog.outta.ai Hymba review,
+// "Efficiency and KV cache optimization"): new rows written into the pages (quantised to
+// e4m3 with one scale per row and head, or as they are), cache rows read back, and the
+// attention of the new rows over the cache on the CUDA cores (fp32).
+//
+//   paged_copy_kernel   a CTA takes ROWS rows of the batch: one thread per row finds its
+//                       sequence and page, then groups of lanes (eight elements each) move
+//                       one (row, K or V, head) vector, with the maximum over the group by
+//                       shuffles when it is quantised.
+#include "paged.cuh"
+
+namespace hy {
+namespace {
+
+constexpr int kCopyThreads = 256;
+
+// WRITE: x (the batch's rows) -> cache; else cache -> x.  T: element type of x, C: of the cache.
+template <typename T, typename C, bool WRITE, int ROWS>
+__global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const PagedKv kv, const RaggedBatch rb, T* xk, T* xv,
+                                                                  long long ld, int lpu, unsigned* status) {
+  constexpr bool kQuant = sizeof(C) == 1;
+  __shared__ int s_page[ROWS], s_row[ROWS];
+  pdl_trigger();
+  pdl_wait();
+  const int r0 = blockIdx.x * ROWS;
+  if (blockIdx.x == 0) check_batch(rb, kv, status);
+  for (int i = threadIdx.x; i < ROWS; i += kCopyThreads) {
+    int page = -1, row = 0;
+    const int r = r0 + i;
+    const int b = r < rb.total_rows ? seq_of_row(rb, r) : -1;
+    if (b >= 0) {
+      Seq s;
+      if (load_seq(rb, kv, b, &s) && r >= s.q0 && r < s.q0 + s.n) {
+        const int at = s.len - s.n + (r - s.q0);
+        page = page_of(kv, b, at);
+        row = at % kv.page_size;
+        if (page < 0) report_invalid(status);
+      }
+    }
+    s_page[i] = page;
+    s_row[i] = row;
+  }
+  __syncthreads();
+  const int e0 = (threadIdx.x & (lpu - 1)) * 8, per_row = 2 * kv.hkv;
+  const int units = ROWS * per_row, step = kCopyThreads / lpu;
+  C* pages = static_cast<C*>(kv.pages);
+  for (int u0 = threadIdx.x / lpu; u0 < units; u0 += 4 * step) {
+    // four vectors in flight before any is used
+    Vec8<T> vx[4];
+    Vec8<C> vc[4];
+    float sc[4];
+    bool ok[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int u = u0 + k * step, i = u / per_row, w = (u - i * per_row) / kv.hkv, h = u - i * per_row - w * kv.hkv;
+      ok[k] = u < units && s_page[min(i, ROWS - 1)] >= 0 && e0 < kv.dh;
+      sc[k] = 0.f;
+      if (!ok[k]) continue;
+      if (WRITE) {
+        vx[k].load((w ? xv : xk) + (r0 + i) * ld + h * kv.dh + e0);
+      } else {
+        vc[k].load(pages + page_elem(kv, w, s_page[i], s_row[i], h) + e0);
+        if (kQuant) sc[k] = kv.scales[page_scale(kv, w, s_page[i], s_row[i], h)];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int u = u0 + k * step, i = u / per_row, w = (u - i * per_row) / kv.hkv, h = u - i * per_row - w * kv.hkv;
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = 0.f;
+      if (ok[k]) {
+        if (WRITE) vx[k].to_f32(f);
+        else vc[k].to_f32(f);
+      }
+      if (WRITE && kQuant) {
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+        for (int o = lpu >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        // the floor keeps 1 / scale finite for rows of zeros and of subnormal values
+        sc[k] = fmaxf(__fdiv_rn(m, 448.f), 1.17549435e-38f);
+        const float inv = __frcp_rn(sc[k]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= inv;
+      } else if (kQuant) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= sc[k];
+      }
+      if (!ok[k]) continue;
+      if (WRITE) {
+        vc[k].from_f32(f);
+        vc[k].store(pages + page_elem(kv, w, s_page[i], s_row[i], h) + e0);
+        if (kQuant && e0 == 0) kv.scales[page_scale(kv, w, s_page[i], s_row[i], h)] = sc[k];
+      } else {
+        vx[k].from_f32(f);
+        vx[k].store((w ? xv : xk) + (r0 + i) * ld + h * kv.dh + e0);
+      }
+    }
+  }
+}
+
+template <typename T, typename C, bool WRITE>
+cudaError_t launch_copy_t(const PagedKv& kv, const RaggedBatch& rb, void* k, void* v, long long ld, unsigned* status,
+                          cudaStream_t st) {
+  int lpu = 2;
+  while (lpu * 8 < kv.dh) lpu *= 2;
+  constexpr int kRows = 8;
+  return launch(paged_copy_kernel<T, C, WRITE, kRows>, dim3((rb.total_rows + kRows - 1) / kRows), dim3(kCopyThreads),
+                0, st, kv, rb, static_cast<T*>(k), static_cast<T*>(v), ld, lpu, status);
+}
+
+template <bool WRITE>
+cudaError_t launch_copy(const PagedKv& kv, const RaggedBatch& rb, void* k, void* v, long long ld, bool bf16,
+                        unsigned* status, cudaStream_t st) {
+  if (rb.total_rows <= 0) return cudaSuccess;
+  if (kv.type == CACHE_E4M3)
+    return bf16 ? launch_copy_t<__nv_bfloat16, __nv_fp8_e4m3, WRITE>(kv, rb, k, v, ld, status, st)
+                : launch_copy_t<float, __nv_fp8_e4m3, WRITE>(kv, rb, k, v, ld, status, st);
+  return bf16 ? launch_copy_t<__nv_bfloat16, __nv_bfloat16, WRITE>(kv, rb, k, v, ld, status, st)
+              : launch_copy_t<float, float, WRITE>(kv, rb, k, v, ld, status, st);
+}
+
+// Attention, one warp per (new row, query head): online softmax in fp32 over the visible
+// keys (meta rows below the window, then the window up to the row itself).
+template <typename T, typename C>
+__global__ void __launch_bounds__(128) paged_attn_simt(const PagedAttnDesc p, float scale) {
+  pdl_trigger();
+  pdl_wait();
+  const PagedKv& kv = p.kv;
+  const long long wid = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, dh = kv.dh;
+  if (blockIdx.x == 0) check_batch(p.rb, kv, p.status);
+  if (wid >= static_cast<long long>(p.rb.total_rows) * p.n_q_heads) return;
+  const int r = static_cast<int>(wid / p.n_q_heads), h = static_cast<int>(wid % p.n_q_heads);
+  const int kvh = h / (p.n_q_heads / kv.hkv);
+  const int b = seq_of_row(p.rb, r);
+  if (b < 0) return;
+  Seq s;
+  if (!load_seq(p.rb, kv, b, &s) || r < s.q0 || r >= s.q0 + s.n) return;
+  const int i = s.len - s.n + (r - s.q0);
+  float qv[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
+  const T* q = static_cast<const T*>(p.q) + r * p.q_ld + h * dh;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) qv[e] = lane + 32 * e < dh ? to_f<T>(q[lane + 32 * e]) : 0.f;
+  const int w_lo = p.window < 0 ? 0 : max(0, i - p.window), m_cnt = min(p.n_meta, w_lo);
+  const int n = m_cnt + (i - w_lo + 1);
+  const C* pages = static_cast<const C*>(kv.pages);
+  float m = -INFINITY, l = 0.f;
+  for (int x = 0; x < n; ++x) {
+    const int j = x < m_cnt ? x : w_lo + (x - m_cnt);
+    const int page = page_of(kv, b, j), row = j % kv.page_size;
+    if (page < 0) {
+      if (lane == 0) report_invalid(p.status);
+      continue;
+    }
+    const C* k = pages + page_elem(kv, 0, page, row, kvh);
+    const C* v = pages + page_elem(kv, 1, page, row, kvh);
+    float sk = 1.f, sv = 1.f;
+    if (kv.type == CACHE_E4M3) {
+      sk = kv.scales[page_scale(kv, 0, page, row, kvh)];
+      sv = kv.scales[page_scale(kv, 1, page, row, kvh)];
+    }
+    float t = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (lane + 32 * e < dh) t = fmaf(qv[e], static_cast<float>(k[lane + 32 * e]), t);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    t *= scale * sk;
+    const float mn = fmaxf(m, t);
+    const float corr = expf(m - mn), pj = expf(t - mn);
+    l = l * corr + pj;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (lane + 32 * e < dh) acc[e] = acc[e] * corr + pj * sv * static_cast<float>(v[lane + 32 * e]);
+    m = mn;
+  }
+  T* out = static_cast<T*>(p.out) + r * p.out_ld + h * dh;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (lane + 32 * e < dh) out[lane + 32 * e] = from_f<T>(l != 0.f ? acc[e] / l : 0.f);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedKv& kv, const RaggedBatch& rb, const void* k, const void* v, long long ld,
+                                bool bf16, unsigned* status, cudaStream_t st) {
+  return launch_copy<true>(kv, rb, const_cast<void*>(k), const_cast<void*>(v), ld, bf16, status, st);
+}
+
+cudaError_t launch_paged_read(const PagedKv& kv, const RaggedBatch& rb, void* k, void* v, long long ld, bool bf16,
+                              unsigned* status, cudaStream_t st) {
+  return launch_copy<false>(kv, rb, k, v, ld, bf16, status, st);
+}
+
+size_t paged_attention_scratch(const PagedKv&, const RaggedBatch&, int, bool) { return 0; }
+
+cudaError_t launch_paged_attention(const PagedAttnDesc& a, cudaStream_t st) {
+  const long long warps = static_cast<long long>(a.rb.total_rows) * a.n_q_heads;
+  if (warps <= 0) return cudaSuccess;
+  const dim3 grid(static_cast<unsigned>((warps + 3) / 4));
+  const float scale = 1.f / sqrtf(static_cast<float>(a.kv.dh));
+  if (a.kv.type == CACHE_E4M3)
+    return a.bf16 ? launch(paged_attn_simt<__nv_bfloat16, __nv_fp8_e4m3>, grid, dim3(128), 0, st, a, scale)
+                  : launch(paged_attn_simt<float, __nv_fp8_e4m3>, grid, dim3(128), 0, st, a, scale);
+  return a.bf16 ? launch(paged_attn_simt<__nv_bfloat16, __nv_bfloat16>, grid, dim3(128), 0, st, a, scale)
+                : launch(paged_attn_simt<float, float>, grid, dim3(128), 0, st, a, scale);
+}
+
+}  // namespace hy

@@ -235,7 +235,8 @@ HYMBA_API hymba_status_t hymba_layer_fwd_noalloc(const void* x, const void* meta
                                void* out, void* stream);
 
 /* Synchronises `stream`, reads and clears the status word at the start of
- * `workspace`: HYMBA_OK, or HYMBA_ERR_TIMEOUT if a kernel's bounded wait ran out. */
+ * `workspace`: HYMBA_OK, HYMBA_ERR_TIMEOUT if a kernel's bounded wait ran out, or
+ * HYMBA_ERR_INVALID_ARG if a paged call found a bad length or page number on the device. */
 HYMBA_API hymba_status_t hymba_workspace_status(void* workspace, void* stream);
 
 /* ---------------- generation: prefill with state, then one token per step ----------------
@@ -407,6 +408,102 @@ HYMBA_API hymba_status_t hymba_branch_norm(void* z, const float* beta1, const fl
 /* y[rows, d] = x / sqrt(mean(x^2) + eps) row-wise (unit gain); x and y may alias. */
 HYMBA_API hymba_status_t hymba_rmsnorm(const void* x, void* y, int rows, int d, float eps,
                              hymba_dtype_t dtype, void* stream);
+
+/* ---------------- serving: a paged K/V cache, its attention, 4-bit weights ----------------
+ * A generation step reads two things: the K/V cache and the weights (the blog.outta.ai
+ * review, "Efficiency and KV cache optimization").  The calls below keep the cache in pages
+ * shared by sequences of different lengths, optionally in 8 bits, attend over it with the
+ * layer's own mask, and multiply a few rows with weights held in 4 bits.  They are stage
+ * calls, like hymba_attention and hymba_gemm: the status word of `workspace` is not reset.
+ *
+ * Pages: cache row r of sequence b is row r % page_size of page
+ * page_table[b * table_ld + r / page_size].  A contiguous cache [2, B, cache_rows, Hkv*dh]
+ * with cache_rows a multiple of 128 is the paged cache with n_pages = B, page_size =
+ * cache_rows and page_table = 0 .. B-1.  Several sequences may name the same page (the meta
+ * rows, a shared prompt) as long as no call writes rows of it for two of them.
+ * HYMBA_CACHE_E4M3 holds, per (row, K/V head), e4m3 codes and one fp32 scale over the head's
+ * dh elements:
+ *   scale = max(amax / 448, 2^-126);  code = e4m3(x * (1 / scale)), nearest even;  value = code * scale
+ * (a NaN keeps its own place; a row with an infinity reads back as NaN).
+ */
+typedef enum { HYMBA_CACHE_F32 = 0, HYMBA_CACHE_BF16 = 1, HYMBA_CACHE_E4M3 = 2 } hymba_cache_type_t;
+
+typedef struct {
+  void* pages;             /* [2, n_pages, page_size, Hkv*dh] cache_type: K pages, then V pages; 16-byte aligned */
+  float* scales;           /* [2, n_pages, Hkv, page_size] fp32, 16-byte aligned (HYMBA_CACHE_E4M3), else NULL */
+  const int* page_table;   /* [batch, table_ld] int32 on the device */
+  int n_pages;
+  int page_size;           /* 8, 16, 32, 64 or a multiple of 128 */
+  int table_ld;            /* entries per sequence */
+  int n_kv_heads;          /* Hkv */
+  int head_dim;            /* dh: a multiple of 16 up to 256 (attention: see there) */
+  int cache_type;          /* hymba_cache_type_t: the calls' dtype, or HYMBA_CACHE_E4M3 */
+} hymba_paged_kv_t;
+
+/*
+ * The batch of all three paged calls: sequence b's n_b = q_start[b+1] - q_start[b] rows of
+ * the ragged tensors are rows [q_start[b], q_start[b+1]) there and cache rows
+ * [kv_len[b] - n_b, kv_len[b]).  q_start [batch + 1] and kv_len [batch] are int32 on the
+ * device; n_b may be 0, and rows of the tensors outside [q_start[0], q_start[batch]) are
+ * neither read nor written.  total_rows bounds q_start[batch].  What only the device can
+ * check is checked there and recorded as HYMBA_ERR_INVALID_ARG in the status word: a
+ * sequence with n_b < 0, n_b > kv_len[b], kv_len[b] beyond its table, or rows beyond
+ * total_rows is skipped (attention: n_b > max_rows too); a row whose page number is outside
+ * [0, n_pages) is not written, not read (its output row stays as it was), and as a key not
+ * attended to.  Page numbers of rows that a call does not reach (behind kv_len, or outside
+ * the window) may be anything.
+ *   workspace  >= 256 bytes (status word), 256-byte aligned, unless a size call says otherwise
+ *
+ * hymba_paged_kv_append writes k, v [total_rows, Hkv*dh] dtype (row stride ld) into the cache,
+ * quantising for HYMBA_CACHE_E4M3; hymba_paged_kv_read writes the cache rows back into
+ * k, v.  Pointers 16-byte aligned, row strides a multiple of 16 bytes.
+ */
+HYMBA_API hymba_status_t hymba_paged_kv_append(const hymba_paged_kv_t* kv, const void* k, const void* v, int ld,
+                                     int batch, const int* q_start, const int* kv_len, int total_rows,
+                                     hymba_dtype_t dtype, void* workspace, size_t ws_bytes, void* stream);
+HYMBA_API hymba_status_t hymba_paged_kv_read(const hymba_paged_kv_t* kv, void* k, void* v, int ld, int batch,
+                                   const int* q_start, const int* kv_len, int total_rows, hymba_dtype_t dtype,
+                                   void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Attention of the new rows of each sequence (their K/V already appended) over its cache:
+ * the query at cache row i sees key j iff j <= i and (window < 0 or i - j <= window or
+ * j < n_meta), query head h reads K/V head h / (Hq / Hkv), as in hymba_attention.
+ *   q [total_rows, Hq*dh] dtype, row stride q_ld; out likewise, row stride out_ld
+ *   max_rows  bounds every n_b (1: a generation step)
+ *   bf16: dh 128 and at most 128 query heads per K/V head; f32: dh a multiple of 16 up to
+ *   128; pointers 16-byte aligned, row strides a multiple of 16 bytes
+ * Cache rows no query of the call sees may hold anything, NaN included.  A visible K or V
+ * that is not finite reaches the rows that see it and, where several queries are handled
+ * together, may reach others of the same sequence.  A row that sees no key (every page
+ * number it needs was invalid) gives 0.
+ * Workspace: hymba_paged_attention_workspace_size bytes, 256-byte aligned.  Calls that share
+ * one (also through captured graphs) must be ordered.
+ */
+HYMBA_API size_t hymba_paged_attention_workspace_size(const hymba_paged_kv_t* kv, int batch, int total_rows,
+                                                      int max_rows, int n_q_heads, hymba_dtype_t dtype);
+HYMBA_API hymba_status_t hymba_paged_attention(const void* q, int q_ld, const hymba_paged_kv_t* kv, void* out,
+                                     int out_ld, int batch, const int* q_start, const int* kv_len,
+                                     int total_rows, int max_rows, int n_q_heads, int n_meta, int window,
+                                     hymba_dtype_t dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Weights in 4 bits with group scales: per row n and group of `group` (32, 64 or 128)
+ * consecutive k, with q in [-8, 7]:  w[n, k] = q[n, k] * scales[n, k / group].
+ *   w_q4    [N, K/2] bytes: byte i of a row holds q[2i] + 8 in its low, q[2i + 1] + 8 in its high nibble
+ *   scales  [N, K/group] fp32
+ * K a multiple of group; w, a and w_q4 16-byte aligned.
+ * hymba_quantize_w4:   scale = max(amax / 7, 2^-126), q = 7 w / amax to the nearest integer (ties to
+ *                      even); a group's weights must be finite
+ * hymba_dequantize_w4: w = q * scale rounded to dtype (the weights of a product with many rows)
+ * hymba_gemm_w4:       C[M, N] = A[M, K] W^T for M <= 16, A and C dtype, fp32 sums
+ */
+HYMBA_API hymba_status_t hymba_quantize_w4(const void* w, void* w_q4, float* scales, int N, int K, int group,
+                                 hymba_dtype_t dtype, void* stream);
+HYMBA_API hymba_status_t hymba_dequantize_w4(const void* w_q4, const float* scales, void* w, int N, int K, int group,
+                                   hymba_dtype_t dtype, void* stream);
+HYMBA_API hymba_status_t hymba_gemm_w4(const void* a, const void* w_q4, const float* scales, void* c, int M, int N,
+                             int K, int group, hymba_dtype_t dtype, void* stream);
 
 #ifdef __cplusplus
 }
