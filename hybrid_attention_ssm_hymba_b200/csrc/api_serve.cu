@@ -36,9 +36,10 @@ hymba_status_t check_cache(const hymba_paged_kv_t* kv, hymba_dtype_t dtype) {
   const int ps = kv->page_size;
   if (!(ps == 8 || ps == 16 || ps == 32 || ps == 64 || ps % 128 == 0)) return HYMBA_ERR_UNSUPPORTED;
   if (kv->head_dim % 16 || kv->head_dim > 256) return HYMBA_ERR_UNSUPPORTED;
-  // row numbers, in the cache and in a sequence, and row widths are 32-bit
-  const long long lim = (1ll << 31) - 1;
-  if (static_cast<long long>(kv->n_pages) * ps > lim || static_cast<long long>(kv->table_ld) * ps > lim ||
+  // row numbers, in the cache and in a sequence, and row widths are 32-bit, with room for the
+  // difference of two places in a sequence and a window
+  if (static_cast<long long>(kv->n_pages) * ps > (1ll << 31) - 1 ||
+      static_cast<long long>(kv->table_ld) * ps > (1ll << 30) ||
       static_cast<long long>(kv->n_kv_heads) * kv->head_dim > (1 << 20))
     return HYMBA_ERR_UNSUPPORTED;
   if (!aligned16(kv->pages) || (kv->cache_type == HYMBA_CACHE_E4M3 && !aligned16(kv->scales)))
@@ -151,7 +152,8 @@ hymba_status_t hymba_paged_attention(const void* q, int q_ld, const hymba_paged_
   a.out_ld = out_ld;
   a.n_q_heads = n_q_heads;
   a.n_meta = n_meta;
-  a.window = window;
+  // a window that no sequence can outgrow is none
+  a.window = window >= static_cast<long long>(kv->table_ld) * kv->page_size ? -1 : window;
   a.bf16 = dtype == HYMBA_BF16;
   a.status = static_cast<unsigned*>(workspace);
   a.scratch = static_cast<uint8_t*>(workspace) + 256;

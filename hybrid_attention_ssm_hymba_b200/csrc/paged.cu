@@ -194,9 +194,16 @@ cudaError_t launch_paged_read(const PagedKv& kv, const RaggedBatch& rb, void* k,
   return launch_copy<false>(kv, rb, k, v, ld, bf16, status, st);
 }
 
-size_t paged_attention_scratch(const PagedKv&, const RaggedBatch&, int, bool) { return 0; }
+// paged_attn_tc.cu
+size_t paged_attention_tc_scratch(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads);
+cudaError_t launch_paged_attention_tc(const PagedAttnDesc& a, cudaStream_t st);
+
+size_t paged_attention_scratch(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads, bool bf16) {
+  return bf16 && kv.type == CACHE_BF16 ? paged_attention_tc_scratch(kv, rb, n_q_heads) : 0;
+}
 
 cudaError_t launch_paged_attention(const PagedAttnDesc& a, cudaStream_t st) {
+  if (a.bf16 && a.kv.type == CACHE_BF16) return launch_paged_attention_tc(a, st);
   const long long warps = static_cast<long long>(a.rb.total_rows) * a.n_q_heads;
   if (warps <= 0) return cudaSuccess;
   const dim3 grid(static_cast<unsigned>((warps + 3) / 4));

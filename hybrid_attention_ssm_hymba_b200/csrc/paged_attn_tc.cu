@@ -1,0 +1,613 @@
+// paged_attn_tc.cu -- attention of new rows over the paged K/V cache on the sm_100a tensor
+// cores (the layer's attention heads, blog.outta.ai Hymba review, "Design formulation" and
+// "Combine global and local attention"; meta rows always visible).
+//
+//   out_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = 2^(s_ij - m_i),   s_ij = log2(e) q_i.k_j / sqrt(dh)
+//
+// in one pass over the keys with a running m_i.  The G query heads that share a K/V head are
+// packed into the rows of a tile, so every K/V row is read once for all of them; two row
+// groups of up to 128 rows (TQ tokens x G heads) share each 128-key block.  The work is one
+// line of key blocks, cut evenly over a persistent CTA per SM (paged_plan.cuh); parts of a cut
+// tile leave their unnormalised output, m and sum in scratch, and paged_join_kernel joins them.
+//
+//   warp 0      producer: Q of both groups by TMA; K and V block by block, one TMA per page
+//               piece and 64-column half, through the page table (two 2-deep rings)
+//   warp 1      UMMA issuer, per block: P_a V, S_a of the next block, P_b V, S_b of the next
+//   warps 2..9  softmax of group a, warps 10..17 of group b: two threads per row, each over 64
+//               of the block's keys and 64 of O's columns
+// TMEM (512 columns): S_a | S_b | O_a | O_b; P in bf16 over the consumed S columns.
+//
+// Rows of V that no query of the tile sees (behind the sequence, between the meta rows and
+// the window) may hold NaN, and 0 x NaN would reach every output: page pieces of such rows
+// are loaded from beyond the tensor map (zeros), and in a partly visible piece the softmax
+// threads zero them before P V.
+#include "paged_plan.cuh"
+
+namespace hy {
+namespace {
+
+constexpr int DH = 128, TILE_BYTES = 128 * DH * 2, HALF = 128 * 64 * 2;
+constexpr uint32_t IDESC_QK = idesc_bf16(128, 128, false, false), IDESC_PV = idesc_bf16(128, DH, false, true);
+constexpr int kMaskSlots = 8;   // the producer is at most four blocks ahead of the softmax
+constexpr int SMEM_BYTES = 6 * TILE_BYTES + 1024 + 256 + kMaskSlots * 16 + 2 * 2 * 2 * 128 * 4 + 2 * 2 * 128 * 4;
+
+struct TcParams {
+  PagedKv kv;
+  RaggedBatch rb;
+  PagedGeo g;
+  const long long* prefix;
+  __nv_bfloat16* out;
+  long long out_ld;
+  float* part;          // [CTA][2][part_rows][DH]: 0 = the CTA's first tile continued, 1 = its last tile begun
+  float2* part_ml;      // [CTA][2][part_rows] (m in log2 units, sum)
+  int part_rows;        // 128 or 256
+  int Hq, piece;        // piece: rows of one K/V load, min(page_size, 128)
+  float scale_log2;
+  unsigned* status;
+};
+
+// What every role of the CTA knows of the tile in hand.
+struct Piece {
+  TileSpan ts;
+  int b, kvh, row0;     // row0: ragged row of the tile's first token
+  int blk0, blk1;       // blocks of the tile to do here
+  int groups;           // row groups with tokens (1 or 2)
+  bool whole;
+};
+
+struct PieceWalk {
+  Walk w;
+  long long left;
+  bool first = true;
+  HY_DEV bool init(const TcParams& p) {
+    const PieceLine line(p.prefix[p.rb.batch], gridDim.x);
+    const int cta = blockIdx.x;
+    left = 0;
+    if (cta >= line.n) return false;
+    const long long w0 = line.start(cta);
+    left = line.start(cta + 1) - w0;
+    w.seek(p.rb, p.kv, p.g, p.prefix, w0);
+    return true;
+  }
+  HY_DEV bool next(const TcParams& p, Piece* o) {
+    if (left <= 0) return false;
+    if (!first && !w.advance(p.rb, p.kv, p.g)) return false;
+    first = false;
+    o->ts = tile_span(p.g, w.s, w.t);
+    o->b = w.b;
+    o->kvh = w.kvh;
+    o->row0 = w.s.q0 + o->ts.tok0;
+    o->blk0 = w.off;
+    o->blk1 = static_cast<int>(min(static_cast<long long>(o->ts.n), w.off + left));
+    o->groups = o->ts.toks > p.g.TQ ? 2 : 1;
+    o->whole = o->blk0 == 0 && o->blk1 == o->ts.n;
+    left -= o->blk1 - o->blk0;
+    return true;
+  }
+};
+
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Maximum of 64 values in eight independent chains of three-input maxima.
+__device__ __forceinline__ float row_max64(const uint32_t (&sv)[64]) {
+  float m[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m[i] = fmaxf(__uint_as_float(sv[i]), __uint_as_float(sv[i + 8]));
+#pragma unroll
+  for (int e = 16; e < 64; e += 16)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = max3f(m[i], __uint_as_float(sv[e + i]), __uint_as_float(sv[e + 8 + i]));
+  return max3f(max3f(m[0], m[1], m[2]), max3f(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
+}
+// P = 2^(S scale - m_ref), packed in place as bf16 pairs (sv[q] <- p[2q], p[2q + 1]); returns
+// the sum of the fp32 values.  P is rounded to bf16 once, as the P V operand.
+__device__ __forceinline__ float row_exp64(uint32_t (&sv)[64], float scale_log2, float m_ref) {
+  const float2 sc = make_float2(scale_log2, scale_log2), nm = make_float2(-m_ref, -m_ref);
+  float2 acc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int q = 0; q < 32; ++q) {
+    const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[2 * q]), __uint_as_float(sv[2 * q + 1])), sc, nm);
+    const float2 pq = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+    acc[q & 3] = __fadd2_rn(acc[q & 3], pq);
+    sv[q] = pack_bf16(pq.x, pq.y);
+  }
+  const float2 t = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+  return t.x + t.y;
+}
+
+__global__ void __launch_bounds__(576, 1)
+    paged_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TcParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  uint8_t* sQ = smem_raw + pad;       // 2 groups
+  uint8_t* sK = sQ + 2 * TILE_BYTES;  // 2 stages
+  uint8_t* sV = sK + 2 * TILE_BYTES;  // 2 stages
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + 2 * TILE_BYTES);
+  uint64_t* q_full = bars + 0;
+  uint64_t* q_empty = bars + 1;
+  uint64_t* k_full = bars + 2;    // [2]
+  uint64_t* k_empty = bars + 4;   // [2]
+  uint64_t* v_full = bars + 6;    // [2]
+  uint64_t* v_empty = bars + 8;   // [2]
+  uint64_t* s_full = bars + 10;   // [group]
+  uint64_t* p_full = bars + 12;   // [group]
+  uint64_t* o_done = bars + 14;   // [group], completes once per P V
+  uint64_t* mma_done = bars + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 17);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // rows of a block whose page number is valid, one bit each: [slot][4]
+  volatile uint32_t* s_valid = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(bars) + 256);
+  float* smax = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 256 + kMaskSlots * 16);  // [2][group][half][row]
+  float* slsum = smax + 2 * 2 * 2 * 128;                                                             // [group][half][row]
+
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 256);
+      mbar_init(&o_done[s], 1);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch(&tmQ);
+    tma_prefetch(&tmK);
+    tma_prefetch(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
+
+  PieceWalk walk;
+  Piece pc;
+  const bool any = walk.init(p);
+  if (any && warp == 0) {
+    // ---------------------------------------------------------------- producer (whole warp)
+    const int npc = 128 / p.piece;   // K/V loads per block and half: lane i < npc issues piece i's
+    const int none = p.kv.n_pages * p.kv.page_size;   // a row beyond the map: zeros
+    uint32_t jb = 0, seg = 0;        // blocks and tiles so far
+    uint32_t k_iss = 0, v_iss = 0, k_par = 0, v_par = 0;
+    bool ok = true;
+    while (ok && walk.next(p, &pc)) {
+      ok = mbar_wait(q_empty, (seg & 1) ^ 1u, p.status, abort_flag);
+      if (ok && lane == 0) {
+        const int bytes = p.g.TQ * p.g.G * 128;
+        mbar_arrive_expect_tx(q_full, 2 * pc.groups * bytes);
+        for (int x = 0; x < pc.groups; ++x) {
+          tma_load_3d(sQ + x * TILE_BYTES, &tmQ, q_full, 0, pc.kvh * p.g.G, pc.row0 + x * p.g.TQ);
+          tma_load_3d(sQ + x * TILE_BYTES + HALF, &tmQ, q_full, 64, pc.kvh * p.g.G, pc.row0 + x * p.g.TQ);
+        }
+      }
+      __syncwarp();
+      const int lo = p.g.window < 0 ? 0 : pc.ts.p0 - p.g.window;   // first key of the window of any query
+      for (int x = pc.blk0; ok && x < pc.blk1; ++x, ++jb) {
+        const int k0 = pc.ts.block(x) * kKeyBlock, s = jb & 1;
+        const uint32_t par = (jb >> 1) & 1;
+        int row = none;
+        bool bad = false;
+        if (lane < npc) {
+          const int r0 = k0 + lane * p.piece, r1 = r0 + p.piece - 1;
+          if (r0 <= pc.ts.p1 && (r0 < p.g.n_meta || r1 >= lo)) {
+            const int page = page_of(p.kv, pc.b, r0);
+            bad = page < 0;
+            if (!bad) row = page * p.kv.page_size + r0 % p.kv.page_size;
+          }
+        }
+        const unsigned bads = __ballot_sync(0xffffffffu, bad);
+        if (bads && lane == 0) report_invalid(p.status);
+        if (lane < 4) {   // 32 rows per word
+          uint32_t m = 0xffffffffu;
+          if (bads)
+            for (int r = 0; r < 32; ++r)
+              if ((bads >> ((lane * 32 + r) / p.piece)) & 1u) m &= ~(1u << r);
+          s_valid[(jb & (kMaskSlots - 1)) * 4 + lane] = m;
+        }
+        __syncwarp();
+        ok = mbar_wait(&k_empty[s], par ^ 1u, p.status, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&k_full[s], TILE_BYTES);
+        __syncwarp();
+        if (lane < npc) {
+          uint8_t* dst = sK + s * TILE_BYTES + lane * p.piece * 128;
+          tma_load_2d(dst, &tmK, &k_full[s], pc.kvh * DH, row);
+          tma_load_2d(dst + HALF, &tmK, &k_full[s], pc.kvh * DH + 64, row);
+        }
+        k_iss |= 1u << s;
+        k_par = (k_par & ~(1u << s)) | (par << s);
+        ok = mbar_wait(&v_empty[s], par ^ 1u, p.status, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&v_full[s], TILE_BYTES);
+        __syncwarp();
+        if (lane < npc) {
+          uint8_t* dst = sV + s * TILE_BYTES + lane * p.piece * 128;
+          tma_load_2d(dst, &tmV, &v_full[s], pc.kvh * DH, row);
+          tma_load_2d(dst + HALF, &tmV, &v_full[s], pc.kvh * DH + 64, row);
+        }
+        v_iss |= 1u << s;
+        v_par = (v_par & ~(1u << s)) | (par << s);
+      }
+      ++seg;
+    }
+    // every issued copy lands before the CTA may exit
+    int never = 0;
+    for (int s = 0; s < 2; ++s) {
+      if (k_iss & (1u << s)) mbar_wait(&k_full[s], (k_par >> s) & 1u, nullptr, &never, 100000000ull);
+      if (v_iss & (1u << s)) mbar_wait(&v_full[s], (v_par >> s) & 1u, nullptr, &never, 100000000ull);
+    }
+    if (seg) mbar_wait(q_full, (seg - 1) & 1u, nullptr, &never, 100000000ull);
+  } else if (any && warp == 1) {
+    // ---------------------------------------------------------------- UMMA issuer (lane 0)
+    const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(sK), 16, 1024),
+                   dV = sdesc_sw128(smem_u32(sV), HALF, 1024);
+    auto issue_s = [&](int x, int s) {  // S_x = Q_x K^T into TMEM columns [128 x, 128 x + 128)
+      const uint64_t qd = sdesc_add(dQ, x * TILE_BYTES), kd = sdesc_add(dK, s * TILE_BYTES);
+#pragma unroll
+      for (int k = 0; k < DH / 16; ++k) {
+        const uint32_t off = (k >> 2) * HALF + (k & 3) * 32;
+        umma_bf16_ss(tmem_base + x * 128, sdesc_add(qd, off), sdesc_add(kd, off), IDESC_QK, k != 0 ? 1u : 0u);
+      }
+      umma_commit(&s_full[x]);
+    };
+    auto issue_pv = [&](int x, int s, bool acc) {  // O_x (+)= P_x V, P_x from TMEM over S_x
+      const uint64_t vd = sdesc_add(dV, s * TILE_BYTES);
+#pragma unroll
+      for (int k = 0; k < 128 / 16; ++k)
+        umma_bf16_ts(tmem_base + 256 + x * 128, tmem_base + x * 128 + k * 8, sdesc_add(vd, k * 16 * 128), IDESC_PV,
+                     (acc || k != 0) ? 1u : 0u);
+      umma_commit(&o_done[x]);
+    };
+    uint32_t jb = 0, seg = 0, cnt[2] = {0, 0};   // blocks so far: all, and per group
+    bool ok = true;
+    while (walk.next(p, &pc)) {
+      if (lane == 0 && ok) {
+        const int n = pc.blk1 - pc.blk0, gr = pc.groups;
+        ok = mbar_wait(q_full, seg & 1, p.status, abort_flag) &&
+             mbar_wait(&k_full[jb & 1], (jb >> 1) & 1, p.status, abort_flag);
+        // S_x goes over the TMEM columns that the last P V of the previous tile reads
+        for (int x = 0; ok && x < gr; ++x)
+          if (cnt[x] > 0) ok = mbar_wait(&o_done[x], (cnt[x] - 1) & 1, p.status, abort_flag);
+        if (ok) {
+          tc_fence_after();
+          for (int x = 0; x < gr; ++x) issue_s(x, jb & 1);
+          umma_commit(&k_empty[jb & 1]);
+          if (n == 1) umma_commit(q_empty);
+        }
+        for (int j = 0; ok && j < n; ++j, ++jb) {
+          for (int x = 0; ok && x < gr; ++x) {
+            const uint32_t par = cnt[x] & 1;
+            if (!mbar_wait(&p_full[x], par, p.status, abort_flag)) { ok = false; break; }
+            if (x == 0 && !mbar_wait(&v_full[jb & 1], (jb >> 1) & 1, p.status, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            issue_pv(x, jb & 1, j > 0);
+            ++cnt[x];
+            if (x == gr - 1) umma_commit(&v_empty[jb & 1]);
+            if (j + 1 < n) {
+              // S_x of the next block overwrites the TMEM columns this P V reads: wait for it
+              if (!mbar_wait(&o_done[x], par, p.status, abort_flag)) { ok = false; break; }
+              if (x == 0 && !mbar_wait(&k_full[(jb + 1) & 1], ((jb + 1) >> 1) & 1, p.status, abort_flag)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              issue_s(x, (jb + 1) & 1);
+              if (x == gr - 1) {
+                umma_commit(&k_empty[(jb + 1) & 1]);
+                if (j + 2 == n) umma_commit(q_empty);
+              }
+            }
+          }
+        }
+        ++seg;
+      }
+      __syncwarp();
+    }
+    if (lane == 0) {
+      umma_commit(mma_done);
+      int never = 0;
+      mbar_wait(mma_done, 0, nullptr, &never, 100000000ull);
+    }
+    __syncwarp();
+  } else if (any) {
+    // ------------------------------------------------------------------ softmax (two groups of 8 warps)
+    const int x = (warp - 2) >> 3;         // row group
+    const int kh = ((warp - 2) >> 2) & 1;  // half of the keys and of O's columns
+    const int r = (warp & 3) * 32 + lane;
+    const int tid = (warp - 2 - 8 * x) * 32 + lane;   // of the group's 256
+    const int rtok = r / p.g.G, rg = r - rtok * p.g.G;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tSx = tmem_base + x * 128 + lane_off, tOx = tmem_base + 256 + x * 128 + lane_off + kh * 64;
+    constexpr float kRescaleLog2 = 8.0f;
+    uint32_t jb = 0, cnt = 0;
+    bool ok = true;
+    while (walk.next(p, &pc)) {
+      const int n = pc.blk1 - pc.blk0;
+      if (x >= pc.groups) {
+        jb += n;
+        continue;
+      }
+      const int i = pc.ts.p0 + x * p.g.TQ + rtok;   // this row's place in the sequence
+      const int pa = pc.ts.p0 + x * p.g.TQ, pb = min(pc.ts.p1, pa + p.g.TQ - 1);   // places of the group's rows
+      const int lo_all = p.g.window < 0 ? 0 : pc.ts.p0 - p.g.window;
+      float m_used = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j, ++jb, ++cnt) {
+        const int k0 = pc.ts.block(pc.blk0 + j) * kKeyBlock;
+        // every thread of the group takes the same steps, so the group barrier below is
+        // reached by all of them (a failed wait only skips the work)
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&s_full[x], cnt & 1, p.status, abort_flag));
+        uint32_t sv[64];
+        float m_half = -INFINITY;
+        if (ok) {
+          tc_fence_after();
+          tmem_ld32(tSx + kh * 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+          tmem_ld32(tSx + kh * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+          const volatile uint32_t* vm = s_valid + (jb & (kMaskSlots - 1)) * 4 + kh * 2;
+          const uint32_t v0 = vm[0], v1 = vm[1];
+          const bool need_mask = !(k0 + kKeyBlock - 1 <= pa &&
+                                   (p.g.window < 0 || pb - k0 <= p.g.window || k0 + kKeyBlock - 1 < p.g.n_meta)) ||
+                                 (v0 & v1) != 0xffffffffu;
+          tmem_wait_ld();
+          if (need_mask) {
+            // e is visible iff e <= hi and (e >= lo or e < me)
+            const int base = k0 + kh * 64, hi = i - base, me = p.g.n_meta - base;
+            const int lo = p.g.window < 0 ? 0 : i - p.g.window - base;
+#pragma unroll
+            for (int e = 0; e < 64; ++e) {
+              const bool vis = e <= hi && (e >= lo || e < me) && (((e < 32 ? v0 : v1) >> (e & 31)) & 1u);
+              if (!vis) sv[e] = __float_as_uint(-INFINITY);
+            }
+          }
+          m_half = row_max64(sv) * p.scale_log2;
+        }
+        // the row maximum over both halves; the barrier also orders this half's reads of
+        // S before the other half's P stores (P of keys 64..127 lands in S columns 32..63)
+        float* sm_j = smax + (cnt & 1) * 512 + x * 256;
+        sm_j[kh * 128 + r] = m_half;
+        tc_fence_before();
+        bar_sync_n(1 + x, 256);
+        tc_fence_after();
+        const float m_cand = fmaxf(sm_j[r], sm_j[128 + r]);
+        if (ok) {
+          const bool need = m_cand > m_used + kRescaleLog2;
+          float alpha = 1.f;
+          if (need) {
+            alpha = ex2_approx(m_used - m_cand);  // 0 when m_used is -inf
+            m_used = m_cand;
+          }
+          const float m_ref = (m_used == -INFINITY) ? 0.f : m_used;
+          const float sum = row_exp64(sv, p.scale_log2, m_ref);
+          tmem_st32(tSx + kh * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+          if (j > 0 && __any_sync(0xffffffffu, need)) {
+            // rescale this half of O (every earlier P V of this group has completed: S_x(j)
+            // was issued after it, and P_x V_j cannot start before p_full below)
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[16];
+              tmem_ld16(tOx + c * 16, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st16(tOx + c * 16, o);
+            }
+          }
+          // rows of V that no query of the tile sees: [a0, a1) between the meta rows and the
+          // window, [b0, 128) behind the last query
+          const int a0 = max(0, p.g.n_meta - k0), a1 = min(kKeyBlock, lo_all - k0);
+          const int b0 = max(0, pc.ts.p1 + 1 - k0);
+          if (a0 < a1 || b0 < kKeyBlock) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&v_full[jb & 1], (jb >> 1) & 1, p.status, abort_flag));
+            if (ok) {
+              uint8_t* v = sV + (jb & 1) * TILE_BYTES;
+              const int na = max(0, a1 - a0), rows = na + max(0, kKeyBlock - b0);
+              for (int c = tid; c < rows * 16; c += 256) {
+                const int q = c >> 4, row = q < na ? a0 + q : b0 + (q - na);
+                *reinterpret_cast<uint4*>(v + ((c >> 3) & 1) * HALF + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+            }
+          }
+          tmem_wait_st();
+          l = fmaf(l, alpha, sum);
+        }
+        tc_fence_before();
+        mbar_arrive(&p_full[x]);
+      }
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&o_done[x], (cnt - 1) & 1, p.status, abort_flag));
+      // the row sum over both halves (every thread of the group reaches these barriers)
+      slsum[x * 256 + kh * 128 + r] = l;
+      bar_sync_n(1 + x, 256);
+      const float lsum = slsum[x * 256 + r] + slsum[x * 256 + 128 + r];
+      bar_sync_n(1 + x, 256);
+      const bool mine = rtok < p.g.TQ && x * p.g.TQ + rtok < pc.ts.toks;
+      if (ok) {
+        tc_fence_after();
+        const float inv = lsum != 0.f ? 1.f / lsum : 0.f;
+        __nv_bfloat16* orow = p.out + static_cast<long long>(pc.row0 + x * p.g.TQ + rtok) * p.out_ld +
+                              (pc.kvh * p.g.G + rg) * DH + kh * 64;
+        const long long prow = (static_cast<long long>(blockIdx.x) * 2 + (pc.blk0 == 0 ? 1 : 0)) * p.part_rows + x * 128 + r;
+        float* part = p.part + prow * DH + kh * 64;
+        if (!pc.whole && kh == 0) p.part_ml[prow] = make_float2(m_used, lsum);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tOx + c * 32, o);
+          tmem_wait_ld();
+          if (!pc.whole) {
+            uint4* dst = reinterpret_cast<uint4*>(part + c * 32);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          } else if (mine) {
+            uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              dst[q] = make_uint4(pack_bf16(__uint_as_float(o[8 * q]) * inv, __uint_as_float(o[8 * q + 1]) * inv),
+                                  pack_bf16(__uint_as_float(o[8 * q + 2]) * inv, __uint_as_float(o[8 * q + 3]) * inv),
+                                  pack_bf16(__uint_as_float(o[8 * q + 4]) * inv, __uint_as_float(o[8 * q + 5]) * inv),
+                                  pack_bf16(__uint_as_float(o[8 * q + 6]) * inv, __uint_as_float(o[8 * q + 7]) * inv));
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+// Joins the parts of each tile that a boundary cut: CTA (i, y) looks at the boundary between
+// CTAs i and i + 1 of the attention and takes every gridDim.y-th group of eight rows (a warp
+// each) of the tile, if this is its first boundary.  A row's parts are weighted by 2^(m - max).
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ TcParams p, int ctas) {
+  pdl_trigger();
+  pdl_wait();
+  const PieceLine line(p.prefix[p.rb.batch], ctas);
+  const int i = blockIdx.x;
+  if (i + 1 >= line.n) return;
+  Walk w;
+  const long long at = line.start(i + 1);
+  w.seek(p.rb, p.kv, p.g, p.prefix, at);
+  if (w.off == 0 || line.start(i) > at - w.off) return;   // not cut here, or cut before
+  const TileSpan ts = tile_span(p.g, w.s, w.t);
+  const long long end = at - w.off + ts.n;
+  int last = i + 1;                                      // the last CTA with a part
+  while (last + 1 < line.n && line.start(last + 1) < end) ++last;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group_rows = p.g.TQ * p.g.G;
+  for (int rr = blockIdx.y * 8 + warp; rr < ts.toks * p.g.G; rr += gridDim.y * 8) {
+    const int x = rr / group_rows, r = rr - x * group_rows, tok = x * p.g.TQ + r / p.g.G, rg = r % p.g.G;
+    float m = -INFINITY;
+    for (int c = i + lane; c <= last; c += 32)
+      m = fmaxf(m, p.part_ml[(2LL * c + (c == i ? 1 : 0)) * p.part_rows + x * 128 + r].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    for (int c = i; c <= last; ++c) {
+      const long long row = (2LL * c + (c == i ? 1 : 0)) * p.part_rows + x * 128 + r;
+      const float2 ml = p.part_ml[row];
+      const float4 v = reinterpret_cast<const float4*>(p.part + row * DH)[lane];
+      if (ml.x == -INFINITY) continue;
+      const float f = ex2_approx(ml.x - m);
+      l = fmaf(ml.y, f, l);
+      acc = make_float4(fmaf(v.x, f, acc.x), fmaf(v.y, f, acc.y), fmaf(v.z, f, acc.z), fmaf(v.w, f, acc.w));
+    }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    __nv_bfloat16* o = p.out + static_cast<long long>(w.s.q0 + ts.tok0 + tok) * p.out_ld + (w.kvh * p.g.G + rg) * DH;
+    reinterpret_cast<uint2*>(o)[lane] = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static const EncodeTiledFn fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<EncodeTiledFn>(ptr)
+               : nullptr;
+  }();
+  return fn;
+}
+
+bool encode(CUtensorMap* m, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+  const cuuint32_t es[3] = {1, 1, 1};
+  const EncodeTiledFn fn = encode_fn();
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Scratch {
+  size_t prefix, part, ml, total;
+  int part_rows;
+};
+Scratch scratch_layout(const RaggedBatch& rb, int G, int ctas) {
+  auto al = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  Scratch s;
+  s.part_rows = rb.max_rows > 128 / G ? 256 : 128;
+  size_t o = 0;
+  s.prefix = o; o = al(o + (static_cast<size_t>(rb.batch) + 1) * 8);
+  s.part = o; o = al(o + static_cast<size_t>(ctas) * 2 * s.part_rows * DH * 4);
+  s.ml = o; o = al(o + static_cast<size_t>(ctas) * 2 * s.part_rows * 8);
+  s.total = o;
+  return s;
+}
+
+}  // namespace
+
+// The scratch is sized for the B200's 148 SMs; a launch uses at most that many CTAs.
+constexpr int kMaxCtas = 148;
+
+size_t paged_attention_tc_scratch(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads) {
+  return scratch_layout(rb, n_q_heads / kv.hkv, kMaxCtas).total;
+}
+
+cudaError_t launch_paged_attention_tc(const PagedAttnDesc& a, cudaStream_t st) {
+  static std::atomic<uint64_t> attr_done{0};
+  if (cudaError_t e = smem_attr_once(paged_attn_tc, SMEM_BYTES, attr_done)) return e;
+  const int ctas = num_sms() < kMaxCtas ? num_sms() : kMaxCtas;
+  TcParams p{};
+  p.kv = a.kv;
+  p.rb = a.rb;
+  p.Hq = a.n_q_heads;
+  p.g.G = a.n_q_heads / a.kv.hkv;
+  p.g.TQ = 128 / p.g.G;
+  p.g.tile_tok = 2 * p.g.TQ;
+  p.g.n_meta = a.n_meta;
+  p.g.window = a.window;
+  const Scratch L = scratch_layout(a.rb, p.g.G, kMaxCtas);
+  uint8_t* sc = static_cast<uint8_t*>(a.scratch);
+  p.prefix = reinterpret_cast<const long long*>(sc + L.prefix);
+  p.part = reinterpret_cast<float*>(sc + L.part);
+  p.part_ml = reinterpret_cast<float2*>(sc + L.ml);
+  p.part_rows = L.part_rows;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.out_ld = a.out_ld;
+  p.piece = a.kv.page_size < 128 ? a.kv.page_size : 128;
+  p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(DH));
+  p.status = a.status;
+  CUtensorMap tq, tk, tv;
+  const cuuint64_t qd[3] = {DH, static_cast<cuuint64_t>(a.n_q_heads), static_cast<cuuint64_t>(a.rb.total_rows)};
+  const cuuint64_t qs[2] = {DH * 2, static_cast<cuuint64_t>(a.q_ld) * 2};
+  const cuuint32_t qb[3] = {64, static_cast<cuuint32_t>(p.g.G), static_cast<cuuint32_t>(p.g.TQ)};
+  const cuuint64_t rows = static_cast<cuuint64_t>(a.kv.n_pages) * a.kv.page_size, cols = static_cast<cuuint64_t>(a.kv.hkv) * DH;
+  const cuuint64_t kd[2] = {cols, rows}, ks[1] = {cols * 2};
+  const cuuint32_t kb[2] = {64, static_cast<cuuint32_t>(p.piece)};
+  if (!encode(&tq, 3, a.q, qd, qs, qb) || !encode(&tk, 2, a.kv.pages, kd, ks, kb) ||
+      !encode(&tv, 2, static_cast<const uint8_t*>(a.kv.pages) + rows * cols * 2, kd, ks, kb))
+    return cudaErrorInvalidValue;
+  if (cudaError_t e = launch(paged_plan_kernel, dim3(1), dim3(1024), 0, st, a.kv, a.rb, p.g,
+                             const_cast<long long*>(p.prefix), a.status))
+    return e;
+  if (cudaError_t e = launch(paged_attn_tc, dim3(ctas), dim3(576), SMEM_BYTES, st, tq, tk, tv, p)) return e;
+  return launch(paged_join_kernel, dim3(ctas - 1, 8), dim3(256), 0, st, p, ctas);
+}
+
+}  // namespace hy

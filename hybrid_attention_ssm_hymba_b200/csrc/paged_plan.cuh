@@ -1,0 +1,167 @@
+// paged_plan.cuh -- how the attention over a paged cache is cut into equal pieces on the
+// device (the host knows no length).  The queries of one sequence and K/V head are packed
+// (token-major, the G query heads of a token next to one another) into row groups of TQ
+// tokens (TQ * G <= 128 rows); a tile is `groups` row groups that share every K/V block, and
+// visits 128-key blocks: those of the meta rows, then those of the window up to its last row.
+// All blocks of all tiles, in the order (sequence, K/V head, tile, block), form one line of W
+// blocks; CTA i of n takes [i W / n, (i + 1) W / n) of it.  A tile cut by such a boundary is
+// computed in parts, which a second kernel joins in the order of the CTAs.
+#pragma once
+
+#include "paged.cuh"
+
+namespace hy {
+
+constexpr int kKeyBlock = 128;
+constexpr int kMinBlocks = 2;   // fewer blocks than this are not worth a CTA of their own
+
+struct PagedGeo {
+  int G, TQ, tile_tok;   // query heads per K/V head; tokens per row group; tokens per tile
+  int n_meta, window;
+};
+
+// One tile's visit: block x of [0, n) starts at key 128 * block(x).
+struct TileSpan {
+  int tok0, toks;       // first token (of the sequence's new ones) and their number
+  int p0, p1;           // cache rows of the first and last token
+  int first, wlo, n;    // blocks [0, first), then [wlo, wlo + n - first)
+  HY_DEV int block(int x) const { return x < first ? x : wlo + (x - first); }
+};
+
+HY_DEV TileSpan tile_span(const PagedGeo& g, const Seq& s, int t) {
+  TileSpan r;
+  r.tok0 = t * g.tile_tok;
+  r.toks = min(g.tile_tok, s.n - r.tok0);
+  r.p0 = s.len - s.n + r.tok0;
+  r.p1 = r.p0 + r.toks - 1;
+  r.first = r.wlo = 0;
+  if (g.window >= 0) {
+    r.wlo = max(0, r.p0 - g.window) / kKeyBlock;
+    r.first = min((min(g.n_meta, r.p1 + 1) + kKeyBlock - 1) / kKeyBlock, r.wlo);
+  }
+  r.n = r.first + r.p1 / kKeyBlock - r.wlo + 1;
+  return r;
+}
+
+HY_DEV bool key_visible(const PagedGeo& g, int i, int j) {
+  return j <= i && (g.window < 0 || i - j <= g.window || j < g.n_meta);
+}
+
+// Blocks of all tiles of a sequence and one K/V head (every lane of the warp gets the sum).
+HY_DEV long long seq_blocks(const PagedGeo& g, const Seq& s) {
+  const int tiles = (s.n + g.tile_tok - 1) / g.tile_tok;
+  long long sum = 0;
+  for (int t = threadIdx.x & 31; t < tiles; t += 32) sum += tile_span(g, s, t).n;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// Writes prefix[b] = blocks of all sequences before b (every K/V head), prefix[batch] = W; one
+// CTA of 1024 threads.  Sequences whose lengths do not fit are recorded and have no blocks.
+static __global__ void __launch_bounds__(1024) paged_plan_kernel(const PagedKv kv, const RaggedBatch rb, const PagedGeo g,
+                                                                 long long* prefix, unsigned* status) {
+  __shared__ long long cnt[1024], wsum[32];
+  pdl_trigger();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long carry = 0;
+  for (int b0 = 0; b0 < rb.batch; b0 += 1024) {
+    for (int i = warp; i < 1024; i += 32) {
+      Seq s;
+      long long c = 0;
+      if (b0 + i < rb.batch) {
+        if (load_seq(rb, kv, b0 + i, &s)) c = seq_blocks(g, s) * kv.hkv;
+        else if (lane == 0) report_invalid(status);
+      }
+      if (lane == 0) cnt[i] = c;
+    }
+    __syncthreads();
+    long long v = cnt[threadIdx.x];
+    const long long own = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (lane == 31) wsum[warp] = v;
+    __syncthreads();
+    long long before = carry;
+    for (int w = 0; w < warp; ++w) before += wsum[w];
+    if (b0 + static_cast<int>(threadIdx.x) < rb.batch) prefix[b0 + threadIdx.x] = before + v - own;
+    long long all = 0;
+    for (int w = 0; w < 32; ++w) all += wsum[w];
+    carry += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) prefix[rb.batch] = carry;
+}
+
+// CTA i's piece of the line of W blocks, over at most n CTAs.
+struct PieceLine {
+  long long W;
+  int n;
+  HY_DEV PieceLine(long long w, int ctas) : W(w) {
+    const long long most = (w + kMinBlocks - 1) / kMinBlocks;
+    n = static_cast<int>(most < ctas ? most : ctas);
+  }
+  HY_DEV long long start(int i) const { return i * W / n; }   // i <= n
+};
+
+// A walk along the line from block `w`; every lane of a warp holds the same state.
+struct Walk {
+  int b, kvh, t, off;   // sequence, K/V head, tile, first block of the tile still to do
+  int tiles;
+  Seq s;
+
+  HY_DEV void load(const RaggedBatch& rb, const PagedKv& kv, const PagedGeo& g) {
+    tiles = load_seq(rb, kv, b, &s) ? (s.n + g.tile_tok - 1) / g.tile_tok : 0;
+  }
+  HY_DEV void seek(const RaggedBatch& rb, const PagedKv& kv, const PagedGeo& g, const long long* prefix, long long w) {
+    int lo = 0, hi = rb.batch;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (prefix[mid] <= w) lo = mid;
+      else hi = mid;
+    }
+    b = lo;
+    load(rb, kv, g);
+    long long rem = w - prefix[b];
+    const long long per = (prefix[b + 1] - prefix[b]) / kv.hkv;
+    kvh = static_cast<int>(rem / per);
+    rem -= kvh * per;
+    const int lane = threadIdx.x & 31;
+    for (int t0 = 0;; t0 += 32) {   // ends: rem < per = the sum over the tiles
+      const long long c = t0 + lane < tiles ? tile_span(g, s, t0 + lane).n : 0;
+      long long inc = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, inc > rem);
+      if (hit || t0 + 32 >= tiles) {
+        const int l = hit ? __ffs(hit) - 1 : 31;
+        t = t0 + l;
+        off = static_cast<int>(rem - __shfl_sync(0xffffffffu, inc - c, l));
+        return;
+      }
+      rem -= __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
+  // To the next tile that has work (false: behind the last sequence).
+  HY_DEV bool advance(const RaggedBatch& rb, const PagedKv& kv, const PagedGeo& g) {
+    off = 0;
+    if (++t < tiles) return true;
+    t = 0;
+    if (++kvh < kv.hkv) return true;
+    kvh = 0;
+    do {
+      if (++b >= rb.batch) return false;
+      load(rb, kv, g);
+    } while (tiles == 0);
+    return true;
+  }
+};
+
+}  // namespace hy
