@@ -28,8 +28,37 @@ namespace {
 
 constexpr int DH = 128, TILE_BYTES = 128 * DH * 2, HALF = 128 * 64 * 2;
 constexpr uint32_t IDESC_QK = idesc_bf16(128, 128, false, false), IDESC_PV = idesc_bf16(128, DH, false, true);
-constexpr int kMaskSlots = 8;   // the producer is at most four blocks ahead of the softmax
-constexpr int SMEM_BYTES = 6 * TILE_BYTES + 1024 + 256 + kMaskSlots * 16 + 2 * 2 * 2 * 128 * 4 + 2 * 2 * 128 * 4;
+
+// What the producer tells the softmax threads of each tile and of each key block.  It is at
+// most one tile and four blocks ahead of them, so rings of 4 and 8 are never overwritten early.
+constexpr int kTileSlots = 4, kBlockSlots = 8;
+struct TileInfo {
+  int p0, p1, toks;   // places of the first and last token; their number (0: no more tiles)
+  int n;              // key blocks to do
+  int row0, kvh;
+  int part;           // -1: the whole tile is done here; else 1 its first part, 0 a later one
+  int groups;
+};
+struct BlockInfo {
+  int k0;
+  uint32_t flags;     // bit x: group x masks; bit 2: some rows of V are to be zeroed
+  uint32_t pad[2];
+  uint32_t valid[4];  // rows whose page number is valid, one bit each
+};
+constexpr uint32_t kZeroV = 4u;
+
+struct Smem {   // behind the six tiles
+  uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2], p_full[2], o_done[2];   // per group; o_done completes once per P V
+  uint64_t tile_full[kTileSlots], mma_done;
+  uint32_t tmem_slot;
+  int abort_flag;
+  alignas(16) TileInfo tile[kTileSlots];
+  alignas(16) BlockInfo block[kBlockSlots];
+  float smax[2][2][2][128];   // [block parity][group][half][row]
+  float slsum[2][2][128];     // [group][half][row]
+};
+constexpr int SMEM_BYTES = 6 * TILE_BYTES + 1024 + sizeof(Smem);
 
 struct TcParams {
   PagedKv kv;
@@ -46,7 +75,7 @@ struct TcParams {
   unsigned* status;
 };
 
-// What every role of the CTA knows of the tile in hand.
+// The producer's view of the tile in hand.
 struct Piece {
   TileSpan ts;
   int b, kvh, row0;     // row0: ragged row of the tile's first token
@@ -59,15 +88,14 @@ struct PieceWalk {
   Walk w;
   long long left;
   bool first = true;
-  HY_DEV bool init(const TcParams& p) {
+  HY_DEV void init(const TcParams& p) {
     const PieceLine line(p.prefix[p.rb.batch], gridDim.x);
     const int cta = blockIdx.x;
     left = 0;
-    if (cta >= line.n) return false;
+    if (cta >= line.n) return;
     const long long w0 = line.start(cta);
     left = line.start(cta + 1) - w0;
     w.seek(p.rb, p.kv, p.g, p.prefix, w0);
-    return true;
   }
   HY_DEV bool next(const TcParams& p, Piece* o) {
     if (left <= 0) return false;
@@ -128,39 +156,25 @@ __global__ void __launch_bounds__(576, 1)
   uint8_t* sQ = smem_raw + pad;       // 2 groups
   uint8_t* sK = sQ + 2 * TILE_BYTES;  // 2 stages
   uint8_t* sV = sK + 2 * TILE_BYTES;  // 2 stages
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + 2 * TILE_BYTES);
-  uint64_t* q_full = bars + 0;
-  uint64_t* q_empty = bars + 1;
-  uint64_t* k_full = bars + 2;    // [2]
-  uint64_t* k_empty = bars + 4;   // [2]
-  uint64_t* v_full = bars + 6;    // [2]
-  uint64_t* v_empty = bars + 8;   // [2]
-  uint64_t* s_full = bars + 10;   // [group]
-  uint64_t* p_full = bars + 12;   // [group]
-  uint64_t* o_done = bars + 14;   // [group], completes once per P V
-  uint64_t* mma_done = bars + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 17);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  // rows of a block whose page number is valid, one bit each: [slot][4]
-  volatile uint32_t* s_valid = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(bars) + 256);
-  float* smax = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 256 + kMaskSlots * 16);  // [2][group][half][row]
-  float* slsum = smax + 2 * 2 * 2 * 128;                                                             // [group][half][row]
+  Smem& sm = *reinterpret_cast<Smem*>(sV + 2 * TILE_BYTES);
+  volatile int* abort_flag = &sm.abort_flag;
 
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], 1);
-      mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], 1);
-      mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 256);
-      mbar_init(&o_done[s], 1);
+      mbar_init(&sm.k_full[s], 1);
+      mbar_init(&sm.k_empty[s], 1);
+      mbar_init(&sm.v_full[s], 1);
+      mbar_init(&sm.v_empty[s], 1);
+      mbar_init(&sm.s_full[s], 1);
+      mbar_init(&sm.p_full[s], 256);
+      mbar_init(&sm.o_done[s], 1);
     }
-    mbar_init(mma_done, 1);
+    for (int s = 0; s < kTileSlots; ++s) mbar_init(&sm.tile_full[s], 1);
+    mbar_init(&sm.mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch(&tmQ);
@@ -168,38 +182,57 @@ __global__ void __launch_bounds__(576, 1)
     tma_prefetch(&tmV);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
+    tmem_alloc(&sm.tmem_slot, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = sm.tmem_slot;
   pdl_wait();
 
-  PieceWalk walk;
-  Piece pc;
-  const bool any = walk.init(p);
-  if (any && warp == 0) {
+  if (warp == 0) {
     // ---------------------------------------------------------------- producer (whole warp)
+    PieceWalk walk;
+    Piece pc;
     const int npc = 128 / p.piece;   // K/V loads per block and half: lane i < npc issues piece i's
     const int none = p.kv.n_pages * p.kv.page_size;   // a row beyond the map: zeros
     uint32_t jb = 0, seg = 0;        // blocks and tiles so far
     uint32_t k_iss = 0, v_iss = 0, k_par = 0, v_par = 0;
     bool ok = true;
-    while (ok && walk.next(p, &pc)) {
-      ok = mbar_wait(q_empty, (seg & 1) ^ 1u, p.status, abort_flag);
-      if (ok && lane == 0) {
+    walk.init(p);
+    for (;;) {
+      const bool more = walk.next(p, &pc);
+      // the slot was last read before this tile's predecessor's Q was done with (ring of 4)
+      ok = mbar_wait(&sm.q_empty, (seg & 1) ^ 1u, p.status, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (lane == 0) {
+        TileInfo& ti = sm.tile[seg & (kTileSlots - 1)];
+        ti.toks = more && ok ? pc.ts.toks : 0;
+        if (more) {
+          ti.p0 = pc.ts.p0;
+          ti.p1 = pc.ts.p1;
+          ti.n = pc.blk1 - pc.blk0;
+          ti.row0 = pc.row0;
+          ti.kvh = pc.kvh;
+          ti.part = pc.whole ? -1 : (pc.blk0 == 0 ? 1 : 0);
+          ti.groups = pc.groups;
+        }
+        mbar_arrive(&sm.tile_full[seg & (kTileSlots - 1)]);
+      }
+      if (!more || !ok) break;
+      if (lane == 0) {
         const int bytes = p.g.TQ * p.g.G * 128;
-        mbar_arrive_expect_tx(q_full, 2 * pc.groups * bytes);
+        mbar_arrive_expect_tx(&sm.q_full, 2 * pc.groups * bytes);
         for (int x = 0; x < pc.groups; ++x) {
-          tma_load_3d(sQ + x * TILE_BYTES, &tmQ, q_full, 0, pc.kvh * p.g.G, pc.row0 + x * p.g.TQ);
-          tma_load_3d(sQ + x * TILE_BYTES + HALF, &tmQ, q_full, 64, pc.kvh * p.g.G, pc.row0 + x * p.g.TQ);
+          tma_load_3d(sQ + x * TILE_BYTES, &tmQ, &sm.q_full, 0, pc.kvh * p.g.G, pc.row0 + x * p.g.TQ);
+          tma_load_3d(sQ + x * TILE_BYTES + HALF, &tmQ, &sm.q_full, 64, pc.kvh * p.g.G, pc.row0 + x * p.g.TQ);
         }
       }
+      ++seg;
       __syncwarp();
-      const int lo = p.g.window < 0 ? 0 : pc.ts.p0 - p.g.window;   // first key of the window of any query
-      for (int x = pc.blk0; ok && x < pc.blk1; ++x, ++jb) {
+      const int lo = p.g.window < 0 ? 0 : pc.ts.p0 - p.g.window;   // first key of any query's window
+      for (int x = pc.blk0; x < pc.blk1; ++x, ++jb) {
         const int k0 = pc.ts.block(x) * kKeyBlock, s = jb & 1;
         const uint32_t par = (jb >> 1) & 1;
         int row = none;
@@ -214,163 +247,168 @@ __global__ void __launch_bounds__(576, 1)
         }
         const unsigned bads = __ballot_sync(0xffffffffu, bad);
         if (bads && lane == 0) report_invalid(p.status);
+        BlockInfo& bi = sm.block[jb & (kBlockSlots - 1)];
         if (lane < 4) {   // 32 rows per word
           uint32_t m = 0xffffffffu;
           if (bads)
             for (int r = 0; r < 32; ++r)
               if ((bads >> ((lane * 32 + r) / p.piece)) & 1u) m &= ~(1u << r);
-          s_valid[(jb & (kMaskSlots - 1)) * 4 + lane] = m;
+          bi.valid[lane] = m;
+        }
+        if (lane == 0) {
+          uint32_t f = 0;
+          const int k1 = k0 + kKeyBlock - 1;
+          for (int gx = 0; gx < 2; ++gx) {   // places of the group's rows: pa .. pb
+            const int pa = pc.ts.p0 + gx * p.g.TQ, pb = min(pc.ts.p1, pa + p.g.TQ - 1);
+            if (bads || k1 > pa || (p.g.window >= 0 && pb - k0 > p.g.window && k1 >= p.g.n_meta)) f |= 1u << gx;
+          }
+          if (k1 > pc.ts.p1 || max(k0, p.g.n_meta) < min(k0 + kKeyBlock, lo)) f |= kZeroV;
+          bi.k0 = k0;
+          bi.flags = f;
         }
         __syncwarp();
-        ok = mbar_wait(&k_empty[s], par ^ 1u, p.status, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.k_empty[s], par ^ 1u, p.status, abort_flag));
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&k_full[s], TILE_BYTES);
+        if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[s], TILE_BYTES);
         __syncwarp();
         if (lane < npc) {
           uint8_t* dst = sK + s * TILE_BYTES + lane * p.piece * 128;
-          tma_load_2d(dst, &tmK, &k_full[s], pc.kvh * DH, row);
-          tma_load_2d(dst + HALF, &tmK, &k_full[s], pc.kvh * DH + 64, row);
+          tma_load_2d(dst, &tmK, &sm.k_full[s], pc.kvh * DH, row);
+          tma_load_2d(dst + HALF, &tmK, &sm.k_full[s], pc.kvh * DH + 64, row);
         }
         k_iss |= 1u << s;
         k_par = (k_par & ~(1u << s)) | (par << s);
-        ok = mbar_wait(&v_empty[s], par ^ 1u, p.status, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.v_empty[s], par ^ 1u, p.status, abort_flag));
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&v_full[s], TILE_BYTES);
+        if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[s], TILE_BYTES);
         __syncwarp();
         if (lane < npc) {
           uint8_t* dst = sV + s * TILE_BYTES + lane * p.piece * 128;
-          tma_load_2d(dst, &tmV, &v_full[s], pc.kvh * DH, row);
-          tma_load_2d(dst + HALF, &tmV, &v_full[s], pc.kvh * DH + 64, row);
+          tma_load_2d(dst, &tmV, &sm.v_full[s], pc.kvh * DH, row);
+          tma_load_2d(dst + HALF, &tmV, &sm.v_full[s], pc.kvh * DH + 64, row);
         }
         v_iss |= 1u << s;
         v_par = (v_par & ~(1u << s)) | (par << s);
       }
-      ++seg;
+      if (!ok) break;   // the others leave by the abort flag
     }
     // every issued copy lands before the CTA may exit
     int never = 0;
     for (int s = 0; s < 2; ++s) {
-      if (k_iss & (1u << s)) mbar_wait(&k_full[s], (k_par >> s) & 1u, nullptr, &never, 100000000ull);
-      if (v_iss & (1u << s)) mbar_wait(&v_full[s], (v_par >> s) & 1u, nullptr, &never, 100000000ull);
+      if (k_iss & (1u << s)) mbar_wait(&sm.k_full[s], (k_par >> s) & 1u, nullptr, &never, 100000000ull);
+      if (v_iss & (1u << s)) mbar_wait(&sm.v_full[s], (v_par >> s) & 1u, nullptr, &never, 100000000ull);
     }
-    if (seg) mbar_wait(q_full, (seg - 1) & 1u, nullptr, &never, 100000000ull);
-  } else if (any && warp == 1) {
+    if (seg) mbar_wait(&sm.q_full, (seg - 1) & 1u, nullptr, &never, 100000000ull);
+  } else if (warp == 1) {
     // ---------------------------------------------------------------- UMMA issuer (lane 0)
-    const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(sK), 16, 1024),
-                   dV = sdesc_sw128(smem_u32(sV), HALF, 1024);
-    auto issue_s = [&](int x, int s) {  // S_x = Q_x K^T into TMEM columns [128 x, 128 x + 128)
-      const uint64_t qd = sdesc_add(dQ, x * TILE_BYTES), kd = sdesc_add(dK, s * TILE_BYTES);
+    if (lane == 0) {
+      const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(sK), 16, 1024),
+                     dV = sdesc_sw128(smem_u32(sV), HALF, 1024);
+      auto issue_s = [&](int x, int s) {  // S_x = Q_x K^T into TMEM columns [128 x, 128 x + 128)
+        const uint64_t qd = sdesc_add(dQ, x * TILE_BYTES), kd = sdesc_add(dK, s * TILE_BYTES);
 #pragma unroll
-      for (int k = 0; k < DH / 16; ++k) {
-        const uint32_t off = (k >> 2) * HALF + (k & 3) * 32;
-        umma_bf16_ss(tmem_base + x * 128, sdesc_add(qd, off), sdesc_add(kd, off), IDESC_QK, k != 0 ? 1u : 0u);
-      }
-      umma_commit(&s_full[x]);
-    };
-    auto issue_pv = [&](int x, int s, bool acc) {  // O_x (+)= P_x V, P_x from TMEM over S_x
-      const uint64_t vd = sdesc_add(dV, s * TILE_BYTES);
+        for (int k = 0; k < DH / 16; ++k) {
+          const uint32_t off = (k >> 2) * HALF + (k & 3) * 32;
+          umma_bf16_ss(tmem_base + x * 128, sdesc_add(qd, off), sdesc_add(kd, off), IDESC_QK, k != 0 ? 1u : 0u);
+        }
+        umma_commit(&sm.s_full[x]);
+      };
+      auto issue_pv = [&](int x, int s, bool acc) {  // O_x (+)= P_x V, P_x from TMEM over S_x
+        const uint64_t vd = sdesc_add(dV, s * TILE_BYTES);
 #pragma unroll
-      for (int k = 0; k < 128 / 16; ++k)
-        umma_bf16_ts(tmem_base + 256 + x * 128, tmem_base + x * 128 + k * 8, sdesc_add(vd, k * 16 * 128), IDESC_PV,
-                     (acc || k != 0) ? 1u : 0u);
-      umma_commit(&o_done[x]);
-    };
-    uint32_t jb = 0, seg = 0, cnt[2] = {0, 0};   // blocks so far: all, and per group
-    bool ok = true;
-    while (walk.next(p, &pc)) {
-      if (lane == 0 && ok) {
-        const int n = pc.blk1 - pc.blk0, gr = pc.groups;
-        ok = mbar_wait(q_full, seg & 1, p.status, abort_flag) &&
-             mbar_wait(&k_full[jb & 1], (jb >> 1) & 1, p.status, abort_flag);
+        for (int k = 0; k < 128 / 16; ++k)
+          umma_bf16_ts(tmem_base + 256 + x * 128, tmem_base + x * 128 + k * 8, sdesc_add(vd, k * 16 * 128), IDESC_PV,
+                       (acc || k != 0) ? 1u : 0u);
+        umma_commit(&sm.o_done[x]);
+      };
+      uint32_t jb = 0, cnt[2] = {0, 0};   // blocks so far: all, and per group
+      bool ok = true;
+      for (uint32_t seg = 0; ok; ++seg) {
+        const TileInfo& ti = sm.tile[seg & (kTileSlots - 1)];
+        ok = mbar_wait(&sm.tile_full[seg & (kTileSlots - 1)], (seg / kTileSlots) & 1, p.status, abort_flag);
+        if (!ok || ti.toks == 0) break;
+        const int n = ti.n, gr = ti.groups;
+        ok = mbar_wait(&sm.q_full, seg & 1, p.status, abort_flag) &&
+             mbar_wait(&sm.k_full[jb & 1], (jb >> 1) & 1, p.status, abort_flag);
         // S_x goes over the TMEM columns that the last P V of the previous tile reads
         for (int x = 0; ok && x < gr; ++x)
-          if (cnt[x] > 0) ok = mbar_wait(&o_done[x], (cnt[x] - 1) & 1, p.status, abort_flag);
-        if (ok) {
-          tc_fence_after();
-          for (int x = 0; x < gr; ++x) issue_s(x, jb & 1);
-          umma_commit(&k_empty[jb & 1]);
-          if (n == 1) umma_commit(q_empty);
-        }
+          if (cnt[x] > 0) ok = mbar_wait(&sm.o_done[x], (cnt[x] - 1) & 1, p.status, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        for (int x = 0; x < gr; ++x) issue_s(x, jb & 1);
+        umma_commit(&sm.k_empty[jb & 1]);
+        if (n == 1) umma_commit(&sm.q_empty);
         for (int j = 0; ok && j < n; ++j, ++jb) {
           for (int x = 0; ok && x < gr; ++x) {
             const uint32_t par = cnt[x] & 1;
-            if (!mbar_wait(&p_full[x], par, p.status, abort_flag)) { ok = false; break; }
-            if (x == 0 && !mbar_wait(&v_full[jb & 1], (jb >> 1) & 1, p.status, abort_flag)) { ok = false; break; }
+            if (!mbar_wait(&sm.p_full[x], par, p.status, abort_flag)) { ok = false; break; }
+            if (x == 0 && !mbar_wait(&sm.v_full[jb & 1], (jb >> 1) & 1, p.status, abort_flag)) { ok = false; break; }
             tc_fence_after();
             issue_pv(x, jb & 1, j > 0);
             ++cnt[x];
-            if (x == gr - 1) umma_commit(&v_empty[jb & 1]);
+            if (x == gr - 1) umma_commit(&sm.v_empty[jb & 1]);
             if (j + 1 < n) {
               // S_x of the next block overwrites the TMEM columns this P V reads: wait for it
-              if (!mbar_wait(&o_done[x], par, p.status, abort_flag)) { ok = false; break; }
-              if (x == 0 && !mbar_wait(&k_full[(jb + 1) & 1], ((jb + 1) >> 1) & 1, p.status, abort_flag)) {
+              if (!mbar_wait(&sm.o_done[x], par, p.status, abort_flag)) { ok = false; break; }
+              if (x == 0 && !mbar_wait(&sm.k_full[(jb + 1) & 1], ((jb + 1) >> 1) & 1, p.status, abort_flag)) {
                 ok = false;
                 break;
               }
               tc_fence_after();
               issue_s(x, (jb + 1) & 1);
               if (x == gr - 1) {
-                umma_commit(&k_empty[(jb + 1) & 1]);
-                if (j + 2 == n) umma_commit(q_empty);
+                umma_commit(&sm.k_empty[(jb + 1) & 1]);
+                if (j + 2 == n) umma_commit(&sm.q_empty);
               }
             }
           }
         }
-        ++seg;
       }
-      __syncwarp();
-    }
-    if (lane == 0) {
-      umma_commit(mma_done);
+      umma_commit(&sm.mma_done);
       int never = 0;
-      mbar_wait(mma_done, 0, nullptr, &never, 100000000ull);
+      mbar_wait(&sm.mma_done, 0, nullptr, &never, 100000000ull);
     }
-    __syncwarp();
-  } else if (any) {
+  } else {
     // ------------------------------------------------------------------ softmax (two groups of 8 warps)
     const int x = (warp - 2) >> 3;         // row group
     const int kh = ((warp - 2) >> 2) & 1;  // half of the keys and of O's columns
     const int r = (warp & 3) * 32 + lane;
-    const int tid = (warp - 2 - 8 * x) * 32 + lane;   // of the group's 256
-    const int rtok = r / p.g.G, rg = r - rtok * p.g.G;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tSx = tmem_base + x * 128 + lane_off, tOx = tmem_base + 256 + x * 128 + lane_off + kh * 64;
+    const int rtok = x * p.g.TQ + r / p.g.G;   // this row's token of the tile
     constexpr float kRescaleLog2 = 8.0f;
     uint32_t jb = 0, cnt = 0;
     bool ok = true;
-    while (walk.next(p, &pc)) {
-      const int n = pc.blk1 - pc.blk0;
-      if (x >= pc.groups) {
+    for (uint32_t seg = 0;; ++seg) {
+      const volatile TileInfo& ti = sm.tile[seg & (kTileSlots - 1)];
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.tile_full[seg & (kTileSlots - 1)], (seg / kTileSlots) & 1,
+                                                   p.status, abort_flag));
+      // every thread of the group takes the same steps from here on, so the group barriers are
+      // reached by all of them; the group leaves together when any of them gave up
+      ok = !bar_red_or(1 + x, 256, !ok);
+      if (!ok || ti.toks == 0) break;
+      const int n = ti.n;
+      if (x >= ti.groups) {
         jb += n;
         continue;
       }
-      const int i = pc.ts.p0 + x * p.g.TQ + rtok;   // this row's place in the sequence
-      const int pa = pc.ts.p0 + x * p.g.TQ, pb = min(pc.ts.p1, pa + p.g.TQ - 1);   // places of the group's rows
-      const int lo_all = p.g.window < 0 ? 0 : pc.ts.p0 - p.g.window;
       float m_used = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++jb, ++cnt) {
-        const int k0 = pc.ts.block(pc.blk0 + j) * kKeyBlock;
-        // every thread of the group takes the same steps, so the group barrier below is
-        // reached by all of them (a failed wait only skips the work)
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&s_full[x], cnt & 1, p.status, abort_flag));
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.s_full[x], cnt & 1, p.status, abort_flag));
         uint32_t sv[64];
         float m_half = -INFINITY;
+        const volatile BlockInfo& bi = sm.block[jb & (kBlockSlots - 1)];
         if (ok) {
           tc_fence_after();
           tmem_ld32(tSx + kh * 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
           tmem_ld32(tSx + kh * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-          const volatile uint32_t* vm = s_valid + (jb & (kMaskSlots - 1)) * 4 + kh * 2;
-          const uint32_t v0 = vm[0], v1 = vm[1];
-          const bool need_mask = !(k0 + kKeyBlock - 1 <= pa &&
-                                   (p.g.window < 0 || pb - k0 <= p.g.window || k0 + kKeyBlock - 1 < p.g.n_meta)) ||
-                                 (v0 & v1) != 0xffffffffu;
+          const uint32_t flags = bi.flags;
           tmem_wait_ld();
-          if (need_mask) {
-            // e is visible iff e <= hi and (e >= lo or e < me)
-            const int base = k0 + kh * 64, hi = i - base, me = p.g.n_meta - base;
-            const int lo = p.g.window < 0 ? 0 : i - p.g.window - base;
+          if (flags & (1u << x)) {
+            // key e of this half is visible iff e <= hi and (e >= lo or e < me), on a valid page
+            const int base = bi.k0 + kh * 64, hi = ti.p0 + rtok - base, me = p.g.n_meta - base;
+            const int lo = p.g.window < 0 ? 0 : hi - p.g.window;
+            const uint32_t v0 = bi.valid[kh * 2], v1 = bi.valid[kh * 2 + 1];
 #pragma unroll
             for (int e = 0; e < 64; ++e) {
               const bool vis = e <= hi && (e >= lo || e < me) && (((e < 32 ? v0 : v1) >> (e & 31)) & 1u);
@@ -381,12 +419,11 @@ __global__ void __launch_bounds__(576, 1)
         }
         // the row maximum over both halves; the barrier also orders this half's reads of
         // S before the other half's P stores (P of keys 64..127 lands in S columns 32..63)
-        float* sm_j = smax + (cnt & 1) * 512 + x * 256;
-        sm_j[kh * 128 + r] = m_half;
+        sm.smax[cnt & 1][x][kh][r] = m_half;
         tc_fence_before();
         bar_sync_n(1 + x, 256);
         tc_fence_after();
-        const float m_cand = fmaxf(sm_j[r], sm_j[128 + r]);
+        const float m_cand = fmaxf(m_half, sm.smax[cnt & 1][x][kh ^ 1][r]);
         if (ok) {
           const bool need = m_cand > m_used + kRescaleLog2;
           float alpha = 1.f;
@@ -410,12 +447,13 @@ __global__ void __launch_bounds__(576, 1)
               tmem_st16(tOx + c * 16, o);
             }
           }
-          // rows of V that no query of the tile sees: [a0, a1) between the meta rows and the
-          // window, [b0, 128) behind the last query
-          const int a0 = max(0, p.g.n_meta - k0), a1 = min(kKeyBlock, lo_all - k0);
-          const int b0 = max(0, pc.ts.p1 + 1 - k0);
-          if (a0 < a1 || b0 < kKeyBlock) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&v_full[jb & 1], (jb >> 1) & 1, p.status, abort_flag));
+          if (bi.flags & kZeroV) {
+            // rows of V that no query of the tile sees: [a0, a1) between the meta rows and the
+            // window, [b0, 128) behind the last query
+            const int k0 = bi.k0, tid = (warp - 2 - 8 * x) * 32 + lane;
+            const int a0 = max(0, p.g.n_meta - k0);
+            const int a1 = min(kKeyBlock, p.g.window < 0 ? 0 : ti.p0 - p.g.window - k0), b0 = max(0, ti.p1 + 1 - k0);
+            ok = __all_sync(0xffffffffu, mbar_wait(&sm.v_full[jb & 1], (jb >> 1) & 1, p.status, abort_flag));
             if (ok) {
               uint8_t* v = sV + (jb & 1) * TILE_BYTES;
               const int na = max(0, a1 - a0), rows = na + max(0, kKeyBlock - b0);
@@ -430,36 +468,35 @@ __global__ void __launch_bounds__(576, 1)
           l = fmaf(l, alpha, sum);
         }
         tc_fence_before();
-        mbar_arrive(&p_full[x]);
+        mbar_arrive(&sm.p_full[x]);
       }
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(&o_done[x], (cnt - 1) & 1, p.status, abort_flag));
-      // the row sum over both halves (every thread of the group reaches these barriers)
-      slsum[x * 256 + kh * 128 + r] = l;
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.o_done[x], (cnt - 1) & 1, p.status, abort_flag));
+      // the row sum over both halves
+      sm.slsum[x][kh][r] = l;
       bar_sync_n(1 + x, 256);
-      const float lsum = slsum[x * 256 + r] + slsum[x * 256 + 128 + r];
-      bar_sync_n(1 + x, 256);
-      const bool mine = rtok < p.g.TQ && x * p.g.TQ + rtok < pc.ts.toks;
+      const float lsum = l + sm.slsum[x][kh ^ 1][r];
       if (ok) {
         tc_fence_after();
+        const bool mine = rtok < (x + 1) * p.g.TQ && rtok < ti.toks, whole = ti.part < 0;
         const float inv = lsum != 0.f ? 1.f / lsum : 0.f;
-        __nv_bfloat16* orow = p.out + static_cast<long long>(pc.row0 + x * p.g.TQ + rtok) * p.out_ld +
-                              (pc.kvh * p.g.G + rg) * DH + kh * 64;
-        const long long prow = (static_cast<long long>(blockIdx.x) * 2 + (pc.blk0 == 0 ? 1 : 0)) * p.part_rows + x * 128 + r;
+        __nv_bfloat16* orow = p.out + static_cast<long long>(ti.row0 + rtok) * p.out_ld +
+                              (ti.kvh * p.g.G + r % p.g.G) * DH + kh * 64;
+        const long long prow = (static_cast<long long>(blockIdx.x) * 2 + ti.part) * p.part_rows + x * 128 + r;
         float* part = p.part + prow * DH + kh * 64;
-        if (!pc.whole && kh == 0) p.part_ml[prow] = make_float2(m_used, lsum);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tOx + c * 32, o);
+        if (!whole && kh == 0) p.part_ml[prow] = make_float2(m_used, lsum);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[16];
+          tmem_ld16(tOx + c * 16, o);
           tmem_wait_ld();
-          if (!pc.whole) {
-            uint4* dst = reinterpret_cast<uint4*>(part + c * 32);
+          if (!whole) {
+            uint4* dst = reinterpret_cast<uint4*>(part + c * 16);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            for (int q = 0; q < 4; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           } else if (mine) {
-            uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+            uint4* dst = reinterpret_cast<uint4*>(orow + c * 16);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 2; ++q)
               dst[q] = make_uint4(pack_bf16(__uint_as_float(o[8 * q]) * inv, __uint_as_float(o[8 * q + 1]) * inv),
                                   pack_bf16(__uint_as_float(o[8 * q + 2]) * inv, __uint_as_float(o[8 * q + 3]) * inv),
                                   pack_bf16(__uint_as_float(o[8 * q + 4]) * inv, __uint_as_float(o[8 * q + 5]) * inv),
