@@ -74,12 +74,14 @@ __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const PagedKv 
         else vc[k].to_f32(f);
       }
       if (WRITE && kQuant) {
-        float m = 0.f;
+        // the largest magnitude, as bits, so that a NaN is the largest of all
+        uint32_t mb = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
-        for (int o = lpu >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int e = 0; e < 8; ++e) mb = max(mb, __float_as_uint(f[e]) & 0x7fffffffu);
+        for (int o = lpu >> 1; o > 0; o >>= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
         // the floor keeps 1 / scale finite for rows of zeros and of subnormal values
-        sc[k] = fmaxf(__fdiv_rn(m, 448.f), 1.17549435e-38f);
+        const float d = __fdiv_rn(__uint_as_float(mb), 448.f);
+        sc[k] = d < 1.17549435e-38f ? 1.17549435e-38f : d;
         const float inv = __frcp_rn(sc[k]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= inv;
@@ -199,20 +201,17 @@ size_t paged_attention_tc_scratch(const PagedKv& kv, const RaggedBatch& rb, int 
 cudaError_t launch_paged_attention_tc(const PagedAttnDesc& a, cudaStream_t st);
 
 size_t paged_attention_scratch(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads, bool bf16) {
-  return bf16 && kv.type == CACHE_BF16 ? paged_attention_tc_scratch(kv, rb, n_q_heads) : 0;
+  return bf16 ? paged_attention_tc_scratch(kv, rb, n_q_heads) : 0;
 }
 
 cudaError_t launch_paged_attention(const PagedAttnDesc& a, cudaStream_t st) {
-  if (a.bf16 && a.kv.type == CACHE_BF16) return launch_paged_attention_tc(a, st);
+  if (a.bf16) return launch_paged_attention_tc(a, st);
   const long long warps = static_cast<long long>(a.rb.total_rows) * a.n_q_heads;
   if (warps <= 0) return cudaSuccess;
   const dim3 grid(static_cast<unsigned>((warps + 3) / 4));
   const float scale = 1.f / sqrtf(static_cast<float>(a.kv.dh));
-  if (a.kv.type == CACHE_E4M3)
-    return a.bf16 ? launch(paged_attn_simt<__nv_bfloat16, __nv_fp8_e4m3>, grid, dim3(128), 0, st, a, scale)
-                  : launch(paged_attn_simt<float, __nv_fp8_e4m3>, grid, dim3(128), 0, st, a, scale);
-  return a.bf16 ? launch(paged_attn_simt<__nv_bfloat16, __nv_bfloat16>, grid, dim3(128), 0, st, a, scale)
-                : launch(paged_attn_simt<float, float>, grid, dim3(128), 0, st, a, scale);
+  return a.kv.type == CACHE_E4M3 ? launch(paged_attn_simt<float, __nv_fp8_e4m3>, grid, dim3(128), 0, st, a, scale)
+                                 : launch(paged_attn_simt<float, float>, grid, dim3(128), 0, st, a, scale);
 }
 
 }  // namespace hy

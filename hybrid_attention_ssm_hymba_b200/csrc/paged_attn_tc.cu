@@ -15,6 +15,9 @@
 //   warp 1      UMMA issuer, per block: P_a V, S_a of the next block, P_b V, S_b of the next
 //   warps 2..9  softmax of group a, warps 10..17 of group b: two threads per row, each over 64
 //               of the block's keys and 64 of O's columns
+//   warps 18, 19 (e4m3 cache only) turn the 8-bit K and V of a block into the bf16 tiles the
+//               tensor core reads.  An e4m3 code is exact in bf16, so the row scales stay out of
+//               the products: the softmax threads multiply S's columns by K's and P's by V's.
 // TMEM (512 columns): S_a | S_b | O_a | O_b; P in bf16 over the consumed S columns.
 //
 // Rows of V that no query of the tile sees (behind the sequence, between the meta rows and
@@ -29,8 +32,8 @@ namespace {
 constexpr int DH = 128, TILE_BYTES = 128 * DH * 2, HALF = 128 * 64 * 2;
 constexpr uint32_t IDESC_QK = idesc_bf16(128, 128, false, false), IDESC_PV = idesc_bf16(128, DH, false, true);
 
-// What the producer tells the softmax threads of each tile and of each key block.  It is at
-// most one tile and four blocks ahead of them, so rings of 4 and 8 are never overwritten early.
+// What the producer tells the softmax threads of each tile (they give the slot back) and of
+// each key block (it is at most four blocks ahead of them: a ring of 8 needs no giving back).
 constexpr int kTileSlots = 4, kBlockSlots = 8;
 struct TileInfo {
   int p0, p1, toks;   // places of the first and last token; their number (0: no more tiles)
@@ -47,18 +50,29 @@ struct BlockInfo {
 };
 constexpr uint32_t kZeroV = 4u;
 
-struct Smem {   // behind the six tiles
+template <bool FP8> struct Smem;
+template <> struct Smem<true>;   // with the scales and barriers of the 8-bit path, below
+template <> struct Smem<false> {   // behind the six tiles
   uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_full[2], o_done[2];   // per group; o_done completes once per P V
-  uint64_t tile_full[kTileSlots], mma_done;
+  uint64_t tile_full[kTileSlots], tile_empty[kTileSlots], mma_done;
   uint32_t tmem_slot;
   int abort_flag;
   alignas(16) TileInfo tile[kTileSlots];
   alignas(16) BlockInfo block[kBlockSlots];
   float smax[2][2][2][128];   // [block parity][group][half][row]
-  float slsum[2][2][128];     // [group][half][row]
 };
-constexpr int SMEM_BYTES = 6 * TILE_BYTES + 1024 + sizeof(Smem);
+// 8-bit path: raw K and V come in half tiles of 64 rows through a ring of three, their scales
+// through a ring of four blocks (the producer is at most three blocks ahead of the softmax).
+constexpr int kRawStages = 3, kRawBytes = 64 * DH, kScaleSlots = 4;
+template <> struct Smem<true> : Smem<false> {
+  uint64_t raw_full[kRawStages], raw_empty[kRawStages], scale_full[kScaleSlots];
+  alignas(16) float scale[kScaleSlots][2][128];   // [slot][K, V][row]
+};
+template <bool FP8> constexpr int smem_bytes() {
+  return 6 * TILE_BYTES + 1024 + (FP8 ? kRawStages * kRawBytes : 0) + static_cast<int>(sizeof(Smem<FP8>));
+}
+static_assert(smem_bytes<true>() <= 227 * 1024, "shared memory of one CTA");
 
 struct TcParams {
   PagedKv kv;
@@ -70,7 +84,7 @@ struct TcParams {
   float* part;          // [CTA][2][part_rows][DH]: 0 = the CTA's first tile continued, 1 = its last tile begun
   float2* part_ml;      // [CTA][2][part_rows] (m in log2 units, sum)
   int part_rows;        // 128 or 256
-  int Hq, piece;        // piece: rows of one K/V load, min(page_size, 128)
+  int piece;            // rows of one K/V load: min(page_size, 128), 8-bit min(page_size, 64)
   float scale_log2;
   unsigned* status;
 };
@@ -130,6 +144,56 @@ __device__ __forceinline__ float row_max64(const uint32_t (&sv)[64]) {
     for (int i = 0; i < 8; ++i) m[i] = max3f(m[i], __uint_as_float(sv[e + i]), __uint_as_float(sv[e + 8 + i]));
   return max3f(max3f(m[0], m[1], m[2]), max3f(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
 }
+// Four e4m3 codes as two bf16 pairs, exactly: the code's exponent and mantissa go to the top
+// of bf16's mantissa and the low end of its exponent, which is the value times 2^-120 (also
+// for subnormal codes).  The NaN code comes out as 480: a row that holds a NaN has a NaN scale.
+__device__ __forceinline__ uint2 bf16_of_e4m3(uint32_t u) {
+  const __nv_bfloat162 up = __float2bfloat162_rn(1.329227995784916e36f);   // 2^120
+  uint32_t o[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t h = __byte_perm(u, 0, i ? 0x3424 : 0x1404);   // code c in the high byte of a 16-bit half
+    const uint32_t b = (h & 0x80008000u) | ((h >> 4) & 0x07f007f0u);
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), up);
+    o[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint2(o[0], o[1]);
+}
+// f[2q], f[2q + 1] times a shared vector (the same for every row): 64 values.
+__device__ __forceinline__ void scale64(uint32_t (&sv)[64], uint32_t vec) {
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    const float4 k = lds_f4(vec + 16 * q);
+    const float2 a = __fmul2_rn(make_float2(__uint_as_float(sv[4 * q]), __uint_as_float(sv[4 * q + 1])), make_float2(k.x, k.y));
+    const float2 b = __fmul2_rn(make_float2(__uint_as_float(sv[4 * q + 2]), __uint_as_float(sv[4 * q + 3])), make_float2(k.z, k.w));
+    sv[4 * q] = __float_as_uint(a.x);
+    sv[4 * q + 1] = __float_as_uint(a.y);
+    sv[4 * q + 2] = __float_as_uint(b.x);
+    sv[4 * q + 3] = __float_as_uint(b.y);
+  }
+}
+// row_exp64 with P's columns times V's scales before their rounding (the sum is without them).
+// Where a mask may have hidden a key its scale may be anything, and 0 stays 0.
+__device__ __forceinline__ float row_exp64_scaled(uint32_t (&sv)[64], float scale_log2, float m_ref, uint32_t vec, bool masked) {
+  const float2 sc = make_float2(scale_log2, scale_log2), nm = make_float2(-m_ref, -m_ref);
+  float2 acc[2];
+  acc[0] = acc[1] = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    const float4 k = lds_f4(vec + 16 * q);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[4 * q + 2 * h]), __uint_as_float(sv[4 * q + 2 * h + 1])), sc, nm);
+      const float2 pq = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+      acc[h] = __fadd2_rn(acc[h], pq);
+      float2 w = __fmul2_rn(pq, h ? make_float2(k.z, k.w) : make_float2(k.x, k.y));
+      if (masked) w = make_float2(pq.x == 0.f ? 0.f : w.x, pq.y == 0.f ? 0.f : w.y);
+      sv[2 * q + h] = pack_bf16(w.x, w.y);
+    }
+  }
+  const float2 t = __fadd2_rn(acc[0], acc[1]);
+  return t.x + t.y;
+}
 // P = 2^(S scale - m_ref), packed in place as bf16 pairs (sv[q] <- p[2q], p[2q + 1]); returns
 // the sum of the fp32 values.  P is rounded to bf16 once, as the P V operand.
 __device__ __forceinline__ float row_exp64(uint32_t (&sv)[64], float scale_log2, float m_ref) {
@@ -148,7 +212,10 @@ __device__ __forceinline__ float row_exp64(uint32_t (&sv)[64], float scale_log2,
   return t.x + t.y;
 }
 
-__global__ void __launch_bounds__(576, 1)
+constexpr int kThreads = 576, kThreadsFp8 = 640;
+
+template <bool FP8>
+__global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
     paged_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TcParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -156,7 +223,8 @@ __global__ void __launch_bounds__(576, 1)
   uint8_t* sQ = smem_raw + pad;       // 2 groups
   uint8_t* sK = sQ + 2 * TILE_BYTES;  // 2 stages
   uint8_t* sV = sK + 2 * TILE_BYTES;  // 2 stages
-  Smem& sm = *reinterpret_cast<Smem*>(sV + 2 * TILE_BYTES);
+  uint8_t* sRaw = sV + 2 * TILE_BYTES;   // FP8: kRawStages half tiles
+  Smem<FP8>& sm = *reinterpret_cast<Smem<FP8>*>(sRaw + (FP8 ? kRawStages * kRawBytes : 0));
   volatile int* abort_flag = &sm.abort_flag;
 
   pdl_trigger();
@@ -165,16 +233,26 @@ __global__ void __launch_bounds__(576, 1)
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&sm.k_full[s], 1);
+      mbar_init(&sm.k_full[s], FP8 ? 128 : 1);
       mbar_init(&sm.k_empty[s], 1);
-      mbar_init(&sm.v_full[s], 1);
+      mbar_init(&sm.v_full[s], FP8 ? 128 : 1);
       mbar_init(&sm.v_empty[s], 1);
       mbar_init(&sm.s_full[s], 1);
       mbar_init(&sm.p_full[s], 256);
       mbar_init(&sm.o_done[s], 1);
     }
-    for (int s = 0; s < kTileSlots; ++s) mbar_init(&sm.tile_full[s], 1);
+    for (int s = 0; s < kTileSlots; ++s) {
+      mbar_init(&sm.tile_full[s], 1);
+      mbar_init(&sm.tile_empty[s], 16);
+    }
     mbar_init(&sm.mma_done, 1);
+    if constexpr (FP8) {
+      for (int s = 0; s < kRawStages; ++s) {
+        mbar_init(&sm.raw_full[s], 1);
+        mbar_init(&sm.raw_empty[s], 64);
+      }
+      for (int s = 0; s < kScaleSlots; ++s) mbar_init(&sm.scale_full[s], 1);
+    }
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch(&tmQ);
@@ -199,12 +277,13 @@ __global__ void __launch_bounds__(576, 1)
     const int none = p.kv.n_pages * p.kv.page_size;   // a row beyond the map: zeros
     uint32_t jb = 0, seg = 0;        // blocks and tiles so far
     uint32_t k_iss = 0, v_iss = 0, k_par = 0, v_par = 0;
+    uint32_t raw = 0, scales_issued = 0;   // FP8: half tiles, and blocks whose scales are under way
     bool ok = true;
     walk.init(p);
     for (;;) {
       const bool more = walk.next(p, &pc);
-      // the slot was last read before this tile's predecessor's Q was done with (ring of 4)
-      ok = mbar_wait(&sm.q_empty, (seg & 1) ^ 1u, p.status, abort_flag);
+      ok = mbar_wait(&sm.q_empty, (seg & 1) ^ 1u, p.status, abort_flag) &&
+           mbar_wait(&sm.tile_empty[seg & (kTileSlots - 1)], ((seg / kTileSlots) & 1) ^ 1u, p.status, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (lane == 0) {
         TileInfo& ti = sm.tile[seg & (kTileSlots - 1)];
@@ -267,6 +346,35 @@ __global__ void __launch_bounds__(576, 1)
           bi.flags = f;
         }
         __syncwarp();
+        if constexpr (FP8) {
+          // the scales of the pieces that are there, then K and V in half tiles
+          const int page = row / p.kv.page_size, at = row - page * p.kv.page_size;
+          const bool have = lane < npc && row != none;
+          const unsigned haves = __ballot_sync(0xffffffffu, have);
+          uint64_t* sf = &sm.scale_full[jb % kScaleSlots];
+          if (lane == 0) mbar_arrive_expect_tx(sf, 2 * __popc(haves) * p.piece * 4);
+          __syncwarp();
+          if (have) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+              bulk_load_1d(&sm.scale[jb % kScaleSlots][w][lane * p.piece], p.kv.scales + page_scale(p.kv, w, page, at, pc.kvh),
+                           p.piece * 4, sf);
+          }
+          scales_issued = jb + 1;
+#pragma unroll 1
+          for (int u = 0; ok && u < 4; ++u, ++raw) {   // K rows 0.., K rows 64.., V rows 0.., V rows 64..
+            const uint32_t rs = raw % kRawStages;
+            ok = __all_sync(0xffffffffu, mbar_wait(&sm.raw_empty[rs], ((raw / kRawStages) & 1) ^ 1u, p.status, abort_flag));
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[rs], kRawBytes);
+            __syncwarp();
+            const int r0 = lane * p.piece;
+            if (lane < npc && (r0 >> 6) == (u & 1))
+              tma_load_2d(sRaw + rs * kRawBytes + (r0 & 63) * DH, u < 2 ? &tmK : &tmV, &sm.raw_full[rs], pc.kvh * DH, row);
+          }
+          if (!ok) break;
+          continue;
+        }
         ok = __all_sync(0xffffffffu, mbar_wait(&sm.k_empty[s], par ^ 1u, p.status, abort_flag));
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[s], TILE_BYTES);
@@ -297,6 +405,12 @@ __global__ void __launch_bounds__(576, 1)
     for (int s = 0; s < 2; ++s) {
       if (k_iss & (1u << s)) mbar_wait(&sm.k_full[s], (k_par >> s) & 1u, nullptr, &never, 100000000ull);
       if (v_iss & (1u << s)) mbar_wait(&sm.v_full[s], (v_par >> s) & 1u, nullptr, &never, 100000000ull);
+    }
+    if constexpr (FP8) {
+      for (uint32_t u = raw > kRawStages ? raw - kRawStages : 0; u < raw; ++u)
+        mbar_wait(&sm.raw_full[u % kRawStages], (u / kRawStages) & 1, nullptr, &never, 100000000ull);
+      for (uint32_t u = scales_issued > kScaleSlots ? scales_issued - kScaleSlots : 0; u < scales_issued; ++u)
+        mbar_wait(&sm.scale_full[u % kScaleSlots], (u / kScaleSlots) & 1, nullptr, &never, 100000000ull);
     }
     if (seg) mbar_wait(&sm.q_full, (seg - 1) & 1u, nullptr, &never, 100000000ull);
   } else if (warp == 1) {
@@ -368,6 +482,51 @@ __global__ void __launch_bounds__(576, 1)
       int never = 0;
       mbar_wait(&sm.mma_done, 0, nullptr, &never, 100000000ull);
     }
+  } else if (FP8 && warp >= 18) {
+    // ---------------------------------------------------------------- e4m3 -> bf16 (two warps)
+    if constexpr (FP8) {
+      const int t = threadIdx.x - 18 * 32;   // of 64
+      uint32_t jb = 0, raw = 0;
+      bool ok = true;
+      for (uint32_t seg = 0; ok; ++seg) {
+        const volatile TileInfo& ti = sm.tile[seg & (kTileSlots - 1)];
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.tile_full[seg & (kTileSlots - 1)], (seg / kTileSlots) & 1, p.status,
+                                               abort_flag));
+        if (!ok || ti.toks == 0) break;
+        const int n = ti.n;
+        for (int j = 0; ok && j < n; ++j, ++jb) {
+          const uint32_t s = jb & 1, par = (jb >> 1) & 1;
+#pragma unroll 1
+          for (int u = 0; u < 4; ++u, ++raw) {
+            const uint32_t rs = raw % kRawStages;
+            if ((u & 1) == 0) ok = __all_sync(0xffffffffu, mbar_wait(u ? &sm.v_empty[s] : &sm.k_empty[s], par ^ 1u, p.status, abort_flag));
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.raw_full[rs], (raw / kRawStages) & 1, p.status, abort_flag));
+            if (!ok) break;
+            const uint32_t src = smem_u32(sRaw + rs * kRawBytes) + t * 16;
+            uint8_t* dst = (u < 2 ? sK : sV) + s * TILE_BYTES + ((t & 4) ? HALF : 0);
+            // 16 codes (one of a row's eight chunks) at a time, to two 16-byte chunks of the
+            // swizzled tile; the four lanes of the upper half store theirs in the other order,
+            // so that the eight lanes of a row meet no bank twice
+            const int c = (t & 3) * 2, flip = (t >> 2) & 1;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int row = (u & 1) * 64 + i * 8 + (t >> 3);
+              const float4 raw4 = lds_f4(src + i * 1024);
+              const uint2 a = bf16_of_e4m3(__float_as_uint(raw4.x)), b = bf16_of_e4m3(__float_as_uint(raw4.y)),
+                          d = bf16_of_e4m3(__float_as_uint(raw4.z)), e = bf16_of_e4m3(__float_as_uint(raw4.w));
+              const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, e.x, e.y);
+              const uint32_t at = smem_u32(dst) + row * 128, sw = row & 7;
+              const uint4 v0 = flip ? hi : lo, v1 = flip ? lo : hi;
+              sts_u32x4(at + (((c + flip) ^ sw) << 4), v0.x, v0.y, v0.z, v0.w);
+              sts_u32x4(at + (((c + (flip ^ 1)) ^ sw) << 4), v1.x, v1.y, v1.z, v1.w);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&sm.raw_empty[rs]);
+            mbar_arrive(u < 2 ? &sm.k_full[s] : &sm.v_full[s]);
+          }
+        }
+      }
+    }
   } else {
     // ------------------------------------------------------------------ softmax (two groups of 8 warps)
     const int x = (warp - 2) >> 3;         // row group
@@ -390,6 +549,8 @@ __global__ void __launch_bounds__(576, 1)
       const int n = ti.n;
       if (x >= ti.groups) {
         jb += n;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.tile_empty[seg & (kTileSlots - 1)]);
         continue;
       }
       float m_used = -INFINITY, l = 0.f;
@@ -404,6 +565,10 @@ __global__ void __launch_bounds__(576, 1)
           tmem_ld32(tSx + kh * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
           const uint32_t flags = bi.flags;
           tmem_wait_ld();
+          if constexpr (FP8) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&sm.scale_full[jb % kScaleSlots], (jb / kScaleSlots) & 1, p.status, abort_flag));
+            scale64(sv, smem_u32(&sm.scale[jb % kScaleSlots][0][kh * 64]));
+          }
           if (flags & (1u << x)) {
             // key e of this half is visible iff e <= hi and (e >= lo or e < me), on a valid page
             const int base = bi.k0 + kh * 64, hi = ti.p0 + rtok - base, me = p.g.n_meta - base;
@@ -432,7 +597,12 @@ __global__ void __launch_bounds__(576, 1)
             m_used = m_cand;
           }
           const float m_ref = (m_used == -INFINITY) ? 0.f : m_used;
-          const float sum = row_exp64(sv, p.scale_log2, m_ref);
+          float sum;
+          if constexpr (FP8)
+            sum = row_exp64_scaled(sv, p.scale_log2, m_ref, smem_u32(&sm.scale[jb % kScaleSlots][1][kh * 64]),
+                                   (bi.flags & (1u << x)) != 0);
+          else
+            sum = row_exp64(sv, p.scale_log2, m_ref);
           tmem_st32(tSx + kh * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
           if (j > 0 && __any_sync(0xffffffffu, need)) {
             // rescale this half of O (every earlier P V of this group has completed: S_x(j)
@@ -447,7 +617,7 @@ __global__ void __launch_bounds__(576, 1)
               tmem_st16(tOx + c * 16, o);
             }
           }
-          if (bi.flags & kZeroV) {
+          if (!FP8 && (bi.flags & kZeroV)) {
             // rows of V that no query of the tile sees: [a0, a1) between the meta rows and the
             // window, [b0, 128) behind the last query
             const int k0 = bi.k0, tid = (warp - 2 - 8 * x) * 32 + lane;
@@ -472,9 +642,9 @@ __global__ void __launch_bounds__(576, 1)
       }
       ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.o_done[x], (cnt - 1) & 1, p.status, abort_flag));
       // the row sum over both halves
-      sm.slsum[x][kh][r] = l;
+      sm.smax[cnt & 1][x][kh][r] = l;
       bar_sync_n(1 + x, 256);
-      const float lsum = l + sm.slsum[x][kh ^ 1][r];
+      const float lsum = l + sm.smax[cnt & 1][x][kh ^ 1][r];
       if (ok) {
         tc_fence_after();
         const bool mine = rtok < (x + 1) * p.g.TQ && rtok < ti.toks, whole = ti.part < 0;
@@ -504,6 +674,8 @@ __global__ void __launch_bounds__(576, 1)
           }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.tile_empty[seg & (kTileSlots - 1)]);
     }
   }
   tc_fence_before();
@@ -572,12 +744,14 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-bool encode(CUtensorMap* m, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+// A map of bf16 (128-byte swizzled boxes of 64 columns) or of bytes (plain boxes of 128).
+bool encode(CUtensorMap* m, bool bytes, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
             const cuuint32_t* box) {
   const cuuint32_t es[3] = {1, 1, 1};
   const EncodeTiledFn fn = encode_fn();
-  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return fn && fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+                  const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -607,13 +781,15 @@ size_t paged_attention_tc_scratch(const PagedKv& kv, const RaggedBatch& rb, int 
 }
 
 cudaError_t launch_paged_attention_tc(const PagedAttnDesc& a, cudaStream_t st) {
-  static std::atomic<uint64_t> attr_done{0};
-  if (cudaError_t e = smem_attr_once(paged_attn_tc, SMEM_BYTES, attr_done)) return e;
+  static std::atomic<uint64_t> attr_done{0}, attr8_done{0};
+  const bool fp8 = a.kv.type == CACHE_E4M3;
+  if (cudaError_t e = fp8 ? smem_attr_once(paged_attn_tc<true>, smem_bytes<true>(), attr8_done)
+                          : smem_attr_once(paged_attn_tc<false>, smem_bytes<false>(), attr_done))
+    return e;
   const int ctas = num_sms() < kMaxCtas ? num_sms() : kMaxCtas;
   TcParams p{};
   p.kv = a.kv;
   p.rb = a.rb;
-  p.Hq = a.n_q_heads;
   p.g.G = a.n_q_heads / a.kv.hkv;
   p.g.TQ = 128 / p.g.G;
   p.g.tile_tok = 2 * p.g.TQ;
@@ -627,23 +803,27 @@ cudaError_t launch_paged_attention_tc(const PagedAttnDesc& a, cudaStream_t st) {
   p.part_rows = L.part_rows;
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.out_ld = a.out_ld;
-  p.piece = a.kv.page_size < 128 ? a.kv.page_size : 128;
+  const int most = fp8 ? 64 : 128;
+  p.piece = a.kv.page_size < most ? a.kv.page_size : most;
   p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(DH));
   p.status = a.status;
   CUtensorMap tq, tk, tv;
   const cuuint64_t qd[3] = {DH, static_cast<cuuint64_t>(a.n_q_heads), static_cast<cuuint64_t>(a.rb.total_rows)};
   const cuuint64_t qs[2] = {DH * 2, static_cast<cuuint64_t>(a.q_ld) * 2};
   const cuuint32_t qb[3] = {64, static_cast<cuuint32_t>(p.g.G), static_cast<cuuint32_t>(p.g.TQ)};
-  const cuuint64_t rows = static_cast<cuuint64_t>(a.kv.n_pages) * a.kv.page_size, cols = static_cast<cuuint64_t>(a.kv.hkv) * DH;
-  const cuuint64_t kd[2] = {cols, rows}, ks[1] = {cols * 2};
-  const cuuint32_t kb[2] = {64, static_cast<cuuint32_t>(p.piece)};
-  if (!encode(&tq, 3, a.q, qd, qs, qb) || !encode(&tk, 2, a.kv.pages, kd, ks, kb) ||
-      !encode(&tv, 2, static_cast<const uint8_t*>(a.kv.pages) + rows * cols * 2, kd, ks, kb))
+  const cuuint64_t rows = static_cast<cuuint64_t>(a.kv.n_pages) * a.kv.page_size;
+  const cuuint64_t row_bytes = static_cast<cuuint64_t>(a.kv.hkv) * DH * (fp8 ? 1 : 2);
+  const cuuint64_t kd[2] = {static_cast<cuuint64_t>(a.kv.hkv) * DH, rows}, ks[1] = {row_bytes};
+  const cuuint32_t kb[2] = {fp8 ? 128u : 64u, static_cast<cuuint32_t>(p.piece)};
+  if (!encode(&tq, false, 3, a.q, qd, qs, qb) || !encode(&tk, fp8, 2, a.kv.pages, kd, ks, kb) ||
+      !encode(&tv, fp8, 2, static_cast<const uint8_t*>(a.kv.pages) + rows * row_bytes, kd, ks, kb))
     return cudaErrorInvalidValue;
   if (cudaError_t e = launch(paged_plan_kernel, dim3(1), dim3(1024), 0, st, a.kv, a.rb, p.g,
                              const_cast<long long*>(p.prefix), a.status))
     return e;
-  if (cudaError_t e = launch(paged_attn_tc, dim3(ctas), dim3(576), SMEM_BYTES, st, tq, tk, tv, p)) return e;
+  if (cudaError_t e = fp8 ? launch(paged_attn_tc<true>, dim3(ctas), dim3(kThreadsFp8), smem_bytes<true>(), st, tq, tk, tv, p)
+                          : launch(paged_attn_tc<false>, dim3(ctas), dim3(kThreads), smem_bytes<false>(), st, tq, tk, tv, p))
+    return e;
   return launch(paged_join_kernel, dim3(ctas - 1, 8), dim3(256), 0, st, p, ctas);
 }
 

@@ -424,7 +424,8 @@ HYMBA_API hymba_status_t hymba_rmsnorm(const void* x, void* y, int rows, int d, 
  * HYMBA_CACHE_E4M3 holds, per (row, K/V head), e4m3 codes and one fp32 scale over the head's
  * dh elements:
  *   scale = max(amax / 448, 2^-126);  code = e4m3(x * (1 / scale)), nearest even;  value = code * scale
- * (a NaN keeps its own place; a row with an infinity reads back as NaN).
+ * (a row with a NaN or an infinity has a NaN or infinite scale and reads back as NaN throughout;
+ * codes written by other means hold no NaN code, 0x7f or 0xff).
  */
 typedef enum { HYMBA_CACHE_F32 = 0, HYMBA_CACHE_BF16 = 1, HYMBA_CACHE_E4M3 = 2 } hymba_cache_type_t;
 

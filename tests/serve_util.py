@@ -22,7 +22,7 @@ def quantise_e4m3(x):
     """x [..., dh] fp32 -> (codes as a float8 tensor, scales): the documented fp32 steps, each
     of which IEEE arithmetic fixes to the last bit."""
     x = np.asarray(x, np.float32)
-    amax = np.nanmax(np.abs(x), axis=-1)
+    amax = np.abs(x).max(axis=-1)
     scale = np.maximum(amax / np.float32(448), TINY).astype(np.float32)
     with np.errstate(invalid="ignore"):
         y = x * (np.float32(1) / scale)[..., None]

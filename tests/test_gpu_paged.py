@@ -86,7 +86,7 @@ def test_attention_ignores_rows_outside_every_window(cache, n):
             pg, at = c.slots(b, j, j + 1)
             for w in range(2):
                 if cache == "e4m3":
-                    c.pages[w].view(torch.uint8)[pg, at] = 0x7f
+                    c.pages[w].view(torch.uint8)[pg, at] = 0x7f     # (codes and scales as they come)
                     c.scales[w][pg, :, at] = float("nan")
                 else:
                     c.pages[w][pg, at] = float("nan")
@@ -241,7 +241,7 @@ def test_append_and_read(batch, dtype, cache, hkv, dh, page):
 
 
 def test_append_special_values():
-    """Infinities and NaN: a NaN keeps its place, a row with an infinity reads back as NaN."""
+    """A row with a NaN or an infinity reads back as NaN throughout, and only that row."""
     c = Paged("bf16", "e4m3", 2, 128, 64, [4], [0], pad=0).upload()
     x = torch.randn(4, 2, 2, 128, dtype=torch.bfloat16, device="cuda")
     x[1, 0, 1, 7] = float("nan")
@@ -251,7 +251,7 @@ def test_append_special_values():
     status_ok(c.read(back[0], back[1], 256))
     nan = torch.isnan(back)
     want = torch.zeros_like(nan)
-    want[0, 1, 1, 7] = True
+    want[0, 1, 1] = True
     want[1, 2, 0] = True
     assert torch.equal(nan, want)
 
