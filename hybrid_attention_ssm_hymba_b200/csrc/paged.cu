@@ -196,16 +196,20 @@ cudaError_t launch_paged_read(const PagedKv& kv, const RaggedBatch& rb, void* k,
   return launch_copy<false>(kv, rb, k, v, ld, bf16, status, st);
 }
 
-// paged_attn_tc.cu
+// paged_decode.cu (at most 16 rows per K/V head) and paged_attn_tc.cu
+bool paged_decode_takes(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads);
+size_t paged_decode_scratch(const RaggedBatch& rb);
+cudaError_t launch_paged_decode(const PagedAttnDesc& a, cudaStream_t st);
 size_t paged_attention_tc_scratch(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads);
 cudaError_t launch_paged_attention_tc(const PagedAttnDesc& a, cudaStream_t st);
 
 size_t paged_attention_scratch(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads, bool bf16) {
-  return bf16 ? paged_attention_tc_scratch(kv, rb, n_q_heads) : 0;
+  if (!bf16) return 0;
+  return paged_decode_takes(kv, rb, n_q_heads) ? paged_decode_scratch(rb) : paged_attention_tc_scratch(kv, rb, n_q_heads);
 }
 
 cudaError_t launch_paged_attention(const PagedAttnDesc& a, cudaStream_t st) {
-  if (a.bf16) return launch_paged_attention_tc(a, st);
+  if (a.bf16) return paged_decode_takes(a.kv, a.rb, a.n_q_heads) ? launch_paged_decode(a, st) : launch_paged_attention_tc(a, st);
   const long long warps = static_cast<long long>(a.rb.total_rows) * a.n_q_heads;
   if (warps <= 0) return cudaSuccess;
   const dim3 grid(static_cast<unsigned>((warps + 3) / 4));

@@ -74,60 +74,6 @@ template <bool FP8> constexpr int smem_bytes() {
 }
 static_assert(smem_bytes<true>() <= 227 * 1024, "shared memory of one CTA");
 
-struct TcParams {
-  PagedKv kv;
-  RaggedBatch rb;
-  PagedGeo g;
-  const long long* prefix;
-  __nv_bfloat16* out;
-  long long out_ld;
-  float* part;          // [CTA][2][part_rows][DH]: 0 = the CTA's first tile continued, 1 = its last tile begun
-  float2* part_ml;      // [CTA][2][part_rows] (m in log2 units, sum)
-  int part_rows;        // 128 or 256
-  int piece;            // rows of one K/V load: min(page_size, 128), 8-bit min(page_size, 64)
-  float scale_log2;
-  unsigned* status;
-};
-
-// The producer's view of the tile in hand.
-struct Piece {
-  TileSpan ts;
-  int b, kvh, row0;     // row0: ragged row of the tile's first token
-  int blk0, blk1;       // blocks of the tile to do here
-  int groups;           // row groups with tokens (1 or 2)
-  bool whole;
-};
-
-struct PieceWalk {
-  Walk w;
-  long long left;
-  bool first = true;
-  HY_DEV void init(const TcParams& p) {
-    const PieceLine line(p.prefix[p.rb.batch], gridDim.x);
-    const int cta = blockIdx.x;
-    left = 0;
-    if (cta >= line.n) return;
-    const long long w0 = line.start(cta);
-    left = line.start(cta + 1) - w0;
-    w.seek(p.rb, p.kv, p.g, p.prefix, w0);
-  }
-  HY_DEV bool next(const TcParams& p, Piece* o) {
-    if (left <= 0) return false;
-    if (!first && !w.advance(p.rb, p.kv, p.g)) return false;
-    first = false;
-    o->ts = tile_span(p.g, w.s, w.t);
-    o->b = w.b;
-    o->kvh = w.kvh;
-    o->row0 = w.s.q0 + o->ts.tok0;
-    o->blk0 = w.off;
-    o->blk1 = static_cast<int>(min(static_cast<long long>(o->ts.n), w.off + left));
-    o->groups = o->ts.toks > p.g.TQ ? 2 : 1;
-    o->whole = o->blk0 == 0 && o->blk1 == o->ts.n;
-    left -= o->blk1 - o->blk0;
-    return true;
-  }
-};
-
 __device__ __forceinline__ float max3f(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -143,21 +89,6 @@ __device__ __forceinline__ float row_max64(const uint32_t (&sv)[64]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) m[i] = max3f(m[i], __uint_as_float(sv[e + i]), __uint_as_float(sv[e + 8 + i]));
   return max3f(max3f(m[0], m[1], m[2]), max3f(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
-}
-// Four e4m3 codes as two bf16 pairs, exactly: the code's exponent and mantissa go to the top
-// of bf16's mantissa and the low end of its exponent, which is the value times 2^-120 (also
-// for subnormal codes).  The NaN code comes out as 480: a row that holds a NaN has a NaN scale.
-__device__ __forceinline__ uint2 bf16_of_e4m3(uint32_t u) {
-  const __nv_bfloat162 up = __float2bfloat162_rn(1.329227995784916e36f);   // 2^120
-  uint32_t o[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t h = __byte_perm(u, 0, i ? 0x3424 : 0x1404);   // code c in the high byte of a 16-bit half
-    const uint32_t b = (h & 0x80008000u) | ((h >> 4) & 0x07f007f0u);
-    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), up);
-    o[i] = *reinterpret_cast<const uint32_t*>(&v);
-  }
-  return make_uint2(o[0], o[1]);
 }
 // f[2q], f[2q + 1] times a shared vector (the same for every row): 64 values.
 __device__ __forceinline__ void scale64(uint32_t (&sv)[64], uint32_t vec) {
@@ -217,7 +148,7 @@ constexpr int kThreads = 576, kThreadsFp8 = 640;
 template <bool FP8>
 __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
     paged_attn_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TcParams p) {
+                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedAttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* sQ = smem_raw + pad;       // 2 groups
@@ -279,9 +210,10 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
     uint32_t k_iss = 0, v_iss = 0, k_par = 0, v_par = 0;
     uint32_t raw = 0, scales_issued = 0;   // FP8: half tiles, and blocks whose scales are under way
     bool ok = true;
-    walk.init(p);
+    walk.init(p, p.prefix);
     for (;;) {
       const bool more = walk.next(p, &pc);
+      const int groups = pc.ts.toks > p.g.TQ ? 2 : 1;   // row groups with tokens
       ok = mbar_wait(&sm.q_empty, (seg & 1) ^ 1u, p.status, abort_flag) &&
            mbar_wait(&sm.tile_empty[seg & (kTileSlots - 1)], ((seg / kTileSlots) & 1) ^ 1u, p.status, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
@@ -295,15 +227,15 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
           ti.row0 = pc.row0;
           ti.kvh = pc.kvh;
           ti.part = pc.whole ? -1 : (pc.blk0 == 0 ? 1 : 0);
-          ti.groups = pc.groups;
+          ti.groups = groups;
         }
         mbar_arrive(&sm.tile_full[seg & (kTileSlots - 1)]);
       }
       if (!more || !ok) break;
       if (lane == 0) {
         const int bytes = p.g.TQ * p.g.G * 128;
-        mbar_arrive_expect_tx(&sm.q_full, 2 * pc.groups * bytes);
-        for (int x = 0; x < pc.groups; ++x) {
+        mbar_arrive_expect_tx(&sm.q_full, 2 * groups * bytes);
+        for (int x = 0; x < groups; ++x) {
           tma_load_3d(sQ + x * TILE_BYTES, &tmQ, &sm.q_full, 0, pc.kvh * p.g.G, pc.row0 + x * p.g.TQ);
           tma_load_3d(sQ + x * TILE_BYTES + HALF, &tmQ, &sm.q_full, 64, pc.kvh * p.g.G, pc.row0 + x * p.g.TQ);
         }
@@ -689,10 +621,10 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
 // Joins the parts of each tile that a boundary cut: CTA (i, y) looks at the boundary between
 // CTAs i and i + 1 of the attention and takes every gridDim.y-th group of eight rows (a warp
 // each) of the tile, if this is its first boundary.  A row's parts are weighted by 2^(m - max).
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ TcParams p, int ctas) {
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedAttnParams p, int ctas) {
   pdl_trigger();
   pdl_wait();
-  const PieceLine line(p.prefix[p.rb.batch], ctas);
+  const PieceLine line(p.prefix[p.rb.batch], ctas, p.min_blocks);
   const int i = blockIdx.x;
   if (i + 1 >= line.n) return;
   Walk w;
@@ -755,29 +687,22 @@ bool encode(CUtensorMap* m, bool bytes, int rank, const void* base, const cuuint
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-struct Scratch {
-  size_t prefix, part, ml, total;
-  int part_rows;
-};
-Scratch scratch_layout(const RaggedBatch& rb, int G, int ctas) {
-  auto al = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-  Scratch s;
-  s.part_rows = rb.max_rows > 128 / G ? 256 : 128;
-  size_t o = 0;
-  s.prefix = o; o = al(o + (static_cast<size_t>(rb.batch) + 1) * 8);
-  s.part = o; o = al(o + static_cast<size_t>(ctas) * 2 * s.part_rows * DH * 4);
-  s.ml = o; o = al(o + static_cast<size_t>(ctas) * 2 * s.part_rows * 8);
-  s.total = o;
-  return s;
-}
-
 }  // namespace
+
+cudaError_t launch_paged_join(const PagedAttnParams& p, int ctas, cudaStream_t st) {
+  if (ctas < 2) return cudaSuccess;
+  return launch(paged_join_kernel, dim3(ctas - 1, (p.part_rows + 31) / 32), dim3(256), 0, st, p, ctas);
+}
 
 // The scratch is sized for the B200's 148 SMs; a launch uses at most that many CTAs.
 constexpr int kMaxCtas = 148;
 
+namespace {
+int tc_part_rows(const RaggedBatch& rb, int G) { return rb.max_rows > 128 / G ? 256 : 128; }
+}  // namespace
+
 size_t paged_attention_tc_scratch(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads) {
-  return scratch_layout(rb, n_q_heads / kv.hkv, kMaxCtas).total;
+  return paged_scratch_layout(rb.batch, kMaxCtas, tc_part_rows(rb, n_q_heads / kv.hkv), DH).total;
 }
 
 cudaError_t launch_paged_attention_tc(const PagedAttnDesc& a, cudaStream_t st) {
@@ -787,7 +712,7 @@ cudaError_t launch_paged_attention_tc(const PagedAttnDesc& a, cudaStream_t st) {
                           : smem_attr_once(paged_attn_tc<false>, smem_bytes<false>(), attr_done))
     return e;
   const int ctas = num_sms() < kMaxCtas ? num_sms() : kMaxCtas;
-  TcParams p{};
+  PagedAttnParams p{};
   p.kv = a.kv;
   p.rb = a.rb;
   p.g.G = a.n_q_heads / a.kv.hkv;
@@ -795,12 +720,13 @@ cudaError_t launch_paged_attention_tc(const PagedAttnDesc& a, cudaStream_t st) {
   p.g.tile_tok = 2 * p.g.TQ;
   p.g.n_meta = a.n_meta;
   p.g.window = a.window;
-  const Scratch L = scratch_layout(a.rb, p.g.G, kMaxCtas);
+  p.part_rows = tc_part_rows(a.rb, p.g.G);
+  p.min_blocks = 2;
+  const PagedScratch L = paged_scratch_layout(a.rb.batch, kMaxCtas, p.part_rows, DH);
   uint8_t* sc = static_cast<uint8_t*>(a.scratch);
-  p.prefix = reinterpret_cast<const long long*>(sc + L.prefix);
+  p.prefix = reinterpret_cast<long long*>(sc + L.prefix);
   p.part = reinterpret_cast<float*>(sc + L.part);
   p.part_ml = reinterpret_cast<float2*>(sc + L.ml);
-  p.part_rows = L.part_rows;
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.out_ld = a.out_ld;
   const int most = fp8 ? 64 : 128;
@@ -818,13 +744,13 @@ cudaError_t launch_paged_attention_tc(const PagedAttnDesc& a, cudaStream_t st) {
   if (!encode(&tq, false, 3, a.q, qd, qs, qb) || !encode(&tk, fp8, 2, a.kv.pages, kd, ks, kb) ||
       !encode(&tv, fp8, 2, static_cast<const uint8_t*>(a.kv.pages) + rows * row_bytes, kd, ks, kb))
     return cudaErrorInvalidValue;
-  if (cudaError_t e = launch(paged_plan_kernel, dim3(1), dim3(1024), 0, st, a.kv, a.rb, p.g,
-                             const_cast<long long*>(p.prefix), a.status))
+  if (cudaError_t e = launch(paged_plan_kernel, dim3(1), dim3(1024), 0, st, a.kv, a.rb, p.g, p.prefix,
+                             a.status))
     return e;
   if (cudaError_t e = fp8 ? launch(paged_attn_tc<true>, dim3(ctas), dim3(kThreadsFp8), smem_bytes<true>(), st, tq, tk, tv, p)
                           : launch(paged_attn_tc<false>, dim3(ctas), dim3(kThreads), smem_bytes<false>(), st, tq, tk, tv, p))
     return e;
-  return launch(paged_join_kernel, dim3(ctas - 1, 8), dim3(256), 0, st, p, ctas);
+  return launch_paged_join(p, ctas, st);
 }
 
 }  // namespace hy

@@ -13,12 +13,45 @@
 namespace hy {
 
 constexpr int kKeyBlock = 128;
-constexpr int kMinBlocks = 2;   // fewer blocks than this are not worth a CTA of their own
 
 struct PagedGeo {
   int G, TQ, tile_tok;   // query heads per K/V head; tokens per row group; tokens per tile
   int n_meta, window;
 };
+
+// What the attention kernels and the join share.
+struct PagedAttnParams {
+  PagedKv kv;
+  RaggedBatch rb;
+  PagedGeo g;
+  long long* prefix;    // [batch + 1], see paged_plan_kernel
+  int min_blocks;       // fewer blocks than this are not worth a CTA of their own
+  const __nv_bfloat16* q;
+  long long q_ld;
+  __nv_bfloat16* out;
+  long long out_ld;
+  float* part;          // [CTA][2][part_rows][dh]: 0 = the CTA's first tile continued, 1 = its last tile begun
+  float2* part_ml;      // [CTA][2][part_rows] (m in log2 units, sum)
+  int part_rows;
+  int piece;            // tensor-core kernel: rows of one K/V load
+  float scale_log2;     // log2(e) / sqrt(dh)
+  unsigned* status;
+};
+struct PagedScratch {
+  size_t prefix, part, ml, total;
+};
+inline PagedScratch paged_scratch_layout(int batch, int ctas, int part_rows, int dh) {
+  auto al = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  PagedScratch s;
+  size_t o = 0;
+  s.prefix = o; o = al(o + (static_cast<size_t>(batch) + 1) * 8);
+  s.part = o; o = al(o + static_cast<size_t>(ctas) * 2 * part_rows * dh * 4);
+  s.ml = o; o = al(o + static_cast<size_t>(ctas) * 2 * part_rows * 8);
+  s.total = o;
+  return s;
+}
+// Joins the cut tiles of a launch of `ctas` CTAs (paged_attn_tc.cu).
+cudaError_t launch_paged_join(const PagedAttnParams& p, int ctas, cudaStream_t st);
 
 // One tile's visit: block x of [0, n) starts at key 128 * block(x).
 struct TileSpan {
@@ -101,8 +134,8 @@ static __global__ void __launch_bounds__(1024) paged_plan_kernel(const PagedKv k
 struct PieceLine {
   long long W;
   int n;
-  HY_DEV PieceLine(long long w, int ctas) : W(w) {
-    const long long most = (w + kMinBlocks - 1) / kMinBlocks;
+  HY_DEV PieceLine(long long w, int ctas, int min_blocks) : W(w) {
+    const long long most = (w + min_blocks - 1) / min_blocks;
     n = static_cast<int>(most < ctas ? most : ctas);
   }
   HY_DEV long long start(int i) const { return i * W / n; }   // i <= n
@@ -163,5 +196,56 @@ struct Walk {
     return true;
   }
 };
+
+// A CTA's piece of the line, tile by tile (every lane of a warp holds the same state).
+struct Piece {
+  TileSpan ts;
+  int b, kvh, row0;     // row0: ragged row of the tile's first token
+  int blk0, blk1;       // blocks of the tile to do here
+  bool whole;
+};
+struct PieceWalk {
+  Walk w;
+  long long left;
+  bool first = true;
+  HY_DEV void init(const PagedAttnParams& p, const long long* prefix) {
+    const PieceLine line(prefix[p.rb.batch], gridDim.x, p.min_blocks);
+    const int cta = blockIdx.x;
+    left = 0;
+    if (cta >= line.n) return;
+    const long long w0 = line.start(cta);
+    left = line.start(cta + 1) - w0;
+    w.seek(p.rb, p.kv, p.g, prefix, w0);
+  }
+  HY_DEV bool next(const PagedAttnParams& p, Piece* o) {
+    if (left <= 0) return false;
+    if (!first && !w.advance(p.rb, p.kv, p.g)) return false;
+    first = false;
+    o->ts = tile_span(p.g, w.s, w.t);
+    o->b = w.b;
+    o->kvh = w.kvh;
+    o->row0 = w.s.q0 + o->ts.tok0;
+    o->blk0 = w.off;
+    o->blk1 = static_cast<int>(min(static_cast<long long>(o->ts.n), w.off + left));
+    o->whole = o->blk0 == 0 && o->blk1 == o->ts.n;
+    left -= o->blk1 - o->blk0;
+    return true;
+  }
+};
+
+// Two e4m3 codes in the high bytes of 16-bit halves (the low bytes may be anything) as bf16,
+// exactly: a code's exponent and mantissa go to the low end of bf16's exponent and the top of
+// its mantissa, which is the value times 2^-120 (also for subnormal codes).  The NaN code
+// comes out as 480: a row that holds a NaN has a NaN scale.
+HY_DEV uint32_t bf16_of_e4m3_high(uint32_t h) {
+  const __nv_bfloat162 up = __float2bfloat162_rn(1.329227995784916e36f);   // 2^120
+  const uint32_t b = (h & 0x80008000u) | ((h >> 4) & 0x07f007f0u);
+  const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), up);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Four consecutive codes as two bf16 pairs.
+HY_DEV uint2 bf16_of_e4m3(uint32_t u) {
+  return make_uint2(bf16_of_e4m3_high(__byte_perm(u, u, 0x1100)), bf16_of_e4m3_high(__byte_perm(u, u, 0x3322)));
+}
 
 }  // namespace hy
