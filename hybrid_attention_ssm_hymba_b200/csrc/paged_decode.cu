@@ -16,7 +16,13 @@
 //          the dims of piece g (eight lanes read 128 consecutive bytes); the two keys of a
 //          register are put together by one byte permutation.
 // A CTA of four warps takes 32 keys of each 128-key block per warp and walks its part of the
-// line of blocks (paged_plan.cuh); K of the next step is loaded before the softmax of this one.
+// line of blocks (paged_plan.cuh).  K of the next step is loaded as soon as Q K^T has read this
+// one's, V as soon as P V has, page numbers two steps and scales one step earlier.
+//
+// e4m3 codes are exact in fp16, one conversion for two of them, so the 8-bit products run in
+// fp16 with their ranges kept by powers of two: a row of Q is scaled to at most 2^8 (its bf16
+// values stay exact down to 2^-32 of the largest), and P V sums n_j = 2^(s_j + log2 sv_j - m' + 8)
+// times the codes, with a running maximum m' of its own, while sum_j 2^(s_j - m) is kept apart.
 #include "paged_plan.cuh"
 
 namespace hy {
@@ -24,13 +30,23 @@ namespace {
 
 constexpr int DH = 128, kWarps = 4, kRows = 16;
 constexpr int kPlanBatch = 1024;   // batches up to this are planned by every CTA itself
+constexpr float kLazy = 7.f;       // a maximum moves when it is exceeded by 2^7: n_j stays below 2^15
+constexpr float kUp = 8.f;         // the exponent added to n_j
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint4 ldg_once(const void* p) {
   uint4 v;
@@ -40,9 +56,27 @@ __device__ __forceinline__ uint4 ldg_once(const void* p) {
   return v;
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+// Two e4m3 codes (the low or the high half of u) as fp16.
+__device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t u, int half) {
+  uint32_t v;
+  if (half) asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, hi;}" : "=r"(v) : "r"(u));
+  else asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, lo;}" : "=r"(v) : "r"(u));
+  return v;
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Two bf16 values times f as fp16.
+__device__ __forceinline__ uint32_t f16_of_bf16(uint32_t u, float f) { return pack_f16(bf16lo(u) * f, bf16hi(u) * f); }
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // One key of a step, held by the lane of its number: its row of the pool (-1: not to be read)
-// and its scales.
+// and its scales, V's as its logarithm.
 struct Key {
   int row;
   float sk, sv;
@@ -51,6 +85,7 @@ struct Key {
 struct Shared {
   float m[kWarps][kRows], l[kWarps][kRows];
   float o[kWarps][kRows][DH + 4];
+  float scale[kWarps][2][2][32];   // [warp][step parity][K, log2 V][key]
   long long prefix[kPlanBatch + 1];
   long long warp_sum[kWarps];
 };
@@ -99,6 +134,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_decode_kernel(const __gr
   constexpr int kSub = 32 / kStep;           // steps per block and warp
   constexpr int kNt = kStep / 8, kKt = kStep / 16;
   constexpr int es = FP8 ? 1 : 2;
+  constexpr unsigned kAll = kStep == 32 ? 0xffffffffu : 0xffffu;
   __shared__ Shared sm;
   pdl_trigger();
   pdl_wait();
@@ -117,86 +153,120 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_decode_kernel(const __gr
   walk.init(p, prefix);
   while (walk.next(p, &pc)) {
     const int rows = pc.ts.toks * p.g.G;
-    // Q of rows g and g + 8 in the dims' order
+    // Q of rows g and g + 8 in the dims' order; qs turns a product into log2 units
     uint32_t qa[8][4];
+    float qs[2];
     {
       const __nv_bfloat16* q0 = p.q + pc.row0 * p.q_ld + static_cast<long long>(pc.kvh) * p.g.G * DH;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int r = g + 8 * half;
         const uint4* q = reinterpret_cast<const uint4*>(q0 + (r / p.g.G) * p.q_ld + (r % p.g.G) * DH);
+        uint4 v[4];
+        uint32_t mx = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           // bf16: piece t of 32 dims j; e4m3: dims 64 (j / 2) + 16 t + 8 (j % 2)
-          const int at = FP8 ? (j >> 1) * 8 + t * 2 + (j & 1) : j * 4 + t;
-          const uint4 v = r < rows ? q[at] : make_uint4(0, 0, 0, 0);
-          qa[2 * j][half] = v.x;
-          qa[2 * j][2 + half] = v.y;
-          qa[2 * j + 1][half] = v.z;
-          qa[2 * j + 1][2 + half] = v.w;
+          v[j] = r < rows ? q[FP8 ? (j >> 1) * 8 + t * 2 + (j & 1) : j * 4 + t] : make_uint4(0, 0, 0, 0);
+          if (FP8) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) mx = max(mx, max(word(v[j], w) & 0x7fffu, (word(v[j], w) >> 16) & 0x7fffu));
+          }
+        }
+        float up = 1.f;
+        qs[half] = p.scale_log2;
+        if (FP8) {   // the row times 2^(f - 127), so that its largest value is in [2^7, 2^8)
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const int f = min(261 - static_cast<int>(mx >> 7), 253);
+          up = __uint_as_float(static_cast<uint32_t>(f) << 23);
+          qs[half] *= __uint_as_float(static_cast<uint32_t>(254 - f) << 23);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          qa[2 * j][half] = FP8 ? f16_of_bf16(v[j].x, up) : v[j].x;
+          qa[2 * j][2 + half] = FP8 ? f16_of_bf16(v[j].y, up) : v[j].y;
+          qa[2 * j + 1][half] = FP8 ? f16_of_bf16(v[j].z, up) : v[j].z;
+          qa[2 * j + 1][2 + half] = FP8 ? f16_of_bf16(v[j].w, up) : v[j].w;
         }
       }
     }
     const int i0 = pc.ts.p0 + g / p.g.G, i1 = pc.ts.p0 + (g + 8) / p.g.G;   // places of the two rows
     const int lo = p.g.window < 0 ? 0 : pc.ts.p0 - p.g.window;             // first key of any row's window
-    const uint8_t* kh = kbase + pc.kvh * (DH * es);
-    const uint8_t* vh = vbase + pc.kvh * (DH * es);
+    const uint8_t* kh = kbase + pc.kvh * (DH * es) + t * 16;
+    const uint8_t* vh = vbase + pc.kvh * (DH * es) + g * 16;
+    const int* table = p.kv.table + static_cast<long long>(pc.b) * p.kv.table_ld;
 
     const int steps = (pc.blk1 - pc.blk0) * kSub;
     auto key0 = [&](int s) { return pc.ts.block(pc.blk0 + s / kSub) * kKeyBlock + warp * 32 + (s % kSub) * kStep; };
-    auto lookup = [&](int s) -> Key {
+    // this lane's key of step s: its page number (kNoKey: nobody sees it), then its row and scales
+    constexpr int kNoKey = -2147483647 - 1;
+    auto lookup = [&](int s) {
+      const int j = key0(s) + lane;
+      if (s >= steps || lane >= kStep || j > pc.ts.p1 || (j < lo && j >= p.g.n_meta)) return kNoKey;
+      const int page = table[p.page_shift >= 0 ? j >> p.page_shift : j / p.kv.page_size];
+      return page == kNoKey ? -1 : page;
+    };
+    auto find = [&](int s, int page) -> Key {
       Key k{-1, 0.f, 0.f};
-      if (s < steps && lane < kStep) {
-        const int j = key0(s) + lane;
-        if (j <= pc.ts.p1 && (j >= lo || j < p.g.n_meta)) {
-          const int page = page_of(p.kv, pc.b, j);
-          if (page < 0) {
-            report_invalid(p.status);
-          } else {
-            const int at = j % p.kv.page_size;
-            k.row = page * p.kv.page_size + at;
-            if (FP8) {
-              k.sk = p.kv.scales[page_scale(p.kv, 0, page, at, pc.kvh)];
-              k.sv = p.kv.scales[page_scale(p.kv, 1, page, at, pc.kvh)];
-            }
-          }
-        }
+      if (page == kNoKey) return k;
+      if (page < 0 || page >= p.kv.n_pages) {
+        report_invalid(p.status);
+        return k;
+      }
+      const int j = key0(s) + lane, at = p.page_shift >= 0 ? j & (p.kv.page_size - 1) : j % p.kv.page_size;
+      k.row = page * p.kv.page_size + at;
+      if (FP8) {
+        k.sk = p.kv.scales[page_scale(p.kv, 0, page, at, pc.kvh)];
+        k.sv = p.kv.scales[page_scale(p.kv, 1, page, at, pc.kvh)];
       }
       return k;
     };
-    // rows that are not read count as zeros
-    constexpr int kLoadsK = FP8 ? 2 : 4;   // 16-byte pieces of a key per lane
-    uint4 kr[kNt][kLoadsK];
+    // a key that is not there loads the pool's first row (a predicated or branched load costs the
+    // kernel a quarter of its time and more); its scores are hidden and its V is zeroed below
+    constexpr int kLoadsK = FP8 ? 2 : 4, kLoadsV = FP8 ? 1 : 2;   // 16-byte pieces of a key per lane
+    uint4 kr[kNt][kLoadsK], vr[kKt][4][kLoadsV];
     auto load_k = [&](const Key& k) {
 #pragma unroll
       for (int nt = 0; nt < kNt; ++nt) {
         const int row = __shfl_sync(0xffffffffu, k.row, nt * 8 + g);
-        const uint8_t* a = kh + row * row_bytes + t * 16;
+        const uint8_t* a = kh + max(row, 0) * row_bytes;
 #pragma unroll
-        for (int j = 0; j < kLoadsK; ++j) kr[nt][j] = row >= 0 ? ldg_once(a + j * 64) : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < kLoadsK; ++j) kr[nt][j] = ldg_once(a + j * 64);
       }
     };
-
-    float o[16][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    Key cur = lookup(0), nxt = lookup(1);
-    load_k(cur);
-    for (int s = 0; s < steps; ++s) {
-      // V of this step
-      uint4 vr[kKt][4][FP8 ? 1 : 2];
+    auto load_v = [&](const Key& k) {
 #pragma unroll
       for (int kt = 0; kt < kKt; ++kt)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int row = __shfl_sync(0xffffffffu, cur.row, kt * 16 + 2 * t + (c & 1) + (c >> 1) * 8);
-          const uint8_t* a = vh + row * row_bytes + g * 16;
+          const int row = __shfl_sync(0xffffffffu, k.row, kt * 16 + 2 * t + (c & 1) + (c >> 1) * 8);
+          const uint8_t* a = vh + max(row, 0) * row_bytes;
 #pragma unroll
-          for (int h = 0; h < (FP8 ? 1 : 2); ++h) vr[kt][c][h] = row >= 0 ? ldg_once(a + h * 128) : make_uint4(0, 0, 0, 0);
+          for (int h = 0; h < kLoadsV; ++h) vr[kt][c][h] = ldg_once(a + h * 128);
         }
-      const Key aft = lookup(s + 2);
+    };
+
+    // mp: the running maxima of what P V sums (e4m3); m, l: of the softmax itself
+    float o[16][4], m[2] = {-INFINITY, -INFINITY}, mp[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+    const int pg1 = lookup(1);
+    int pg2 = lookup(2);
+    Key cur = find(0, lookup(0)), nxt = find(1, pg1);
+    load_k(cur);
+    load_v(cur);
+    for (int s = 0; s < steps; ++s) {
+      const Key aft = find(s + 2, pg2);
+      pg2 = lookup(s + 3);
+      float (&sc_k)[32] = sm.scale[warp][s & 1][0], (&sc_v)[32] = sm.scale[warp][s & 1][1];
+      if (FP8) {
+        sc_k[lane] = cur.sk;
+        sc_v[lane] = cur.row >= 0 ? lg2_approx(cur.sv) : 0.f;
+        __syncwarp();
+      }
       // S = Q K^T
       float sc[kNt][4];
 #pragma unroll
@@ -207,116 +277,152 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_decode_kernel(const __gr
         for (int j = 0; j < kLoadsK; ++j) {
           if constexpr (FP8) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const uint2 b = bf16_of_e4m3(word(kr[nt][j], w));
-              mma_bf16(sc[nt], qa[4 * j + w], b.x, b.y);
-            }
+            for (int w = 0; w < 4; ++w)
+              mma16<true>(sc[nt], qa[4 * j + w], f16_of_e4m3(word(kr[nt][j], w), 0), f16_of_e4m3(word(kr[nt][j], w), 1));
           } else {
-            mma_bf16(sc[nt], qa[2 * j], kr[nt][j].x, kr[nt][j].y);
-            mma_bf16(sc[nt], qa[2 * j + 1], kr[nt][j].z, kr[nt][j].w);
+            mma16<false>(sc[nt], qa[2 * j], kr[nt][j].x, kr[nt][j].y);
+            mma16<false>(sc[nt], qa[2 * j + 1], kr[nt][j].z, kr[nt][j].w);
           }
         }
       }
       if (s + 1 < steps) load_k(nxt);
-      // scores in log2 units, hidden keys -inf
-      const int k0 = key0(s);
+      if (FP8) {
+#pragma unroll
+        for (int nt = 0; nt < kNt; ++nt) {
+          const float2 k = *reinterpret_cast<const float2*>(&sc_k[nt * 8 + 2 * t]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[nt][e] *= e & 1 ? k.y : k.x;
+        }
+      }
+      // hidden keys -inf (most steps have none)
+      const int k0 = key0(s), k1 = k0 + kStep - 1;
       const unsigned there = __ballot_sync(0xffffffffu, cur.row >= 0);
-      float mx0 = -INFINITY, mx1 = -INFINITY;
+      if (there != kAll || k1 > pc.ts.p0 ||
+          (p.g.window >= 0 && pc.ts.p1 - k0 > p.g.window && k1 >= p.g.n_meta)) {
+#pragma unroll
+        for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int c = nt * 8 + 2 * t + e;
+            const bool in = (there >> c) & 1u;
+            if (!in || !key_visible(p.g, i0, k0 + c)) sc[nt][e] = -INFINITY;
+            if (!in || !key_visible(p.g, i1, k0 + c)) sc[nt][2 + e] = -INFINITY;
+          }
+      }
+      // the maxima of both rows: of the scores and (e4m3) of the scores with log2 sv in them
+      float mx[2] = {-INFINITY, -INFINITY}, mxp[2] = {-INFINITY, -INFINITY};
+      float2 lv[kNt];
 #pragma unroll
       for (int nt = 0; nt < kNt; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int c = nt * 8 + 2 * t + e, j = k0 + c;
-          float f = p.scale_log2;
-          if (FP8) f *= __shfl_sync(0xffffffffu, cur.sk, c);
-          const bool in = (there >> c) & 1u;
-          sc[nt][e] = in && key_visible(p.g, i0, j) ? sc[nt][e] * f : -INFINITY;
-          sc[nt][2 + e] = in && key_visible(p.g, i1, j) ? sc[nt][2 + e] * f : -INFINITY;
-          mx0 = fmaxf(mx0, sc[nt][e]);
-          mx1 = fmaxf(mx1, sc[nt][2 + e]);
-        }
-      }
-#pragma unroll
-      for (int d = 1; d < 4; d <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
-      }
-      if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1)) {
-        const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-        const float a0 = n0 == -INFINITY ? 1.f : ex2_approx(m0 - n0), a1 = n1 == -INFINITY ? 1.f : ex2_approx(m1 - n1);
-        m0 = n0;
-        m1 = n1;
-        l0 *= a0;
-        l1 *= a1;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          o[i][0] *= a0;
-          o[i][1] *= a0;
-          o[i][2] *= a1;
-          o[i][3] *= a1;
-        }
-      }
-      const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
-      uint32_t pa[kKt][4];   // P, rounded to bf16 once, with V's scales in it
-#pragma unroll
-      for (int kt = 0; kt < kKt; ++kt)
+        if (FP8) lv[nt] = *reinterpret_cast<const float2*>(&sc_v[nt * 8 + 2 * t]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float (&x)[4] = sc[2 * kt + h];
-          x[0] = ex2_approx(x[0] - r0);
-          x[1] = ex2_approx(x[1] - r0);
-          x[2] = ex2_approx(x[2] - r1);
-          x[3] = ex2_approx(x[3] - r1);
-          l0 += x[0] + x[1];
-          l1 += x[2] + x[3];
-          if (FP8) {   // (a key that is not there has scale 0)
-            const int c = (2 * kt + h) * 8 + 2 * t;
-            const float s0 = __shfl_sync(0xffffffffu, cur.sv, c), s1 = __shfl_sync(0xffffffffu, cur.sv, c + 1);
-            x[0] *= s0;
-            x[1] *= s1;
-            x[2] *= s0;
-            x[3] *= s1;
-          }
-          pa[kt][2 * h] = pack_bf16(x[0], x[1]);
-          pa[kt][2 * h + 1] = pack_bf16(x[2], x[3]);
+          mx[h] = fmaxf(mx[h], fmaxf(sc[nt][2 * h], sc[nt][2 * h + 1]));
+          if (FP8)
+            mxp[h] = fmaxf(mxp[h], fmaxf(fmaf(sc[nt][2 * h], qs[h], lv[nt].x), fmaf(sc[nt][2 * h + 1], qs[h], lv[nt].y)));
         }
+      }
+      bool move = false;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mx[h] *= qs[h];
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], d));
+          if (FP8) mxp[h] = fmaxf(mxp[h], __shfl_xor_sync(0xffffffffu, mxp[h], d));
+        }
+        move |= mx[h] > m[h] + kLazy || (FP8 && mxp[h] > mp[h] + kLazy);
+      }
+      if (__any_sync(0xffffffffu, move)) {
+        float ao[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float n = fmaxf(m[h], mx[h]), np = FP8 ? fmaxf(mp[h], mxp[h]) : n;
+          const float a = n == -INFINITY ? 1.f : ex2_approx(m[h] - n);
+          l[h] *= a;
+          ao[h] = FP8 ? (np == -INFINITY ? 1.f : ex2_approx(mp[h] - np)) : a;
+          m[h] = n;
+          mp[h] = np;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][e] *= ao[e >> 1];
+      }
+      uint32_t pa[kKt][4];   // the rows of P V, rounded once to the products' 16 bits
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float r = m[h] == -INFINITY ? 0.f : m[h], rp = mp[h] == -INFINITY ? 0.f : mp[h] - kUp;
+#pragma unroll
+        for (int nt = 0; nt < kNt; ++nt) {
+          const float x0 = ex2_approx(fmaf(sc[nt][2 * h], qs[h], -r)), x1 = ex2_approx(fmaf(sc[nt][2 * h + 1], qs[h], -r));
+          l[h] += x0 + x1;
+          pa[nt >> 1][2 * (nt & 1) + h] =
+              FP8 ? pack_f16(ex2_approx(fmaf(sc[nt][2 * h], qs[h], lv[nt].x - rp)),
+                             ex2_approx(fmaf(sc[nt][2 * h + 1], qs[h], lv[nt].y - rp)))
+                  : pack_bf16(x0, x1);
+        }
+      }
       // O += P V
+      if (there != kAll) {
+#pragma unroll
+        for (int kt = 0; kt < kKt; ++kt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int h = 0; h < kLoadsV; ++h)
+              if (!((there >> (kt * 16 + 2 * t + (c & 1) + (c >> 1) * 8)) & 1u)) vr[kt][c][h] = make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
       for (int kt = 0; kt < kKt; ++kt) {
         if constexpr (FP8) {
 #pragma unroll
           for (int w = 0; w < 4; ++w)
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const uint32_t sel = (b | (b << 4)) | ((4 + b) << 8) | ((4 + b) << 12);
-              mma_bf16(o[4 * w + b], pa[kt], bf16_of_e4m3_high(__byte_perm(word(vr[kt][0][0], w), word(vr[kt][1][0], w), sel)),
-                       bf16_of_e4m3_high(__byte_perm(word(vr[kt][2][0], w), word(vr[kt][3][0], w), sel)));
+            for (int b = 0; b < 2; ++b) {   // dims 2b, 2b + 1 of the word: (key, next key) of each
+              const uint32_t sel = b ? 0x7362 : 0x5140;
+              const uint32_t x = __byte_perm(word(vr[kt][0][0], w), word(vr[kt][1][0], w), sel),
+                             y = __byte_perm(word(vr[kt][2][0], w), word(vr[kt][3][0], w), sel);
+              mma16<true>(o[4 * w + 2 * b], pa[kt], f16_of_e4m3(x, 0), f16_of_e4m3(y, 0));
+              mma16<true>(o[4 * w + 2 * b + 1], pa[kt], f16_of_e4m3(x, 1), f16_of_e4m3(y, 1));
             }
         } else {
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < kLoadsV; ++h)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const uint32_t sel = e & 1 ? 0x7632 : 0x5410;
-              mma_bf16(o[8 * h + e], pa[kt], __byte_perm(word(vr[kt][0][h], e >> 1), word(vr[kt][1][h], e >> 1), sel),
-                       __byte_perm(word(vr[kt][2][h], e >> 1), word(vr[kt][3][h], e >> 1), sel));
+              mma16<false>(o[8 * h + e], pa[kt], __byte_perm(word(vr[kt][0][h], e >> 1), word(vr[kt][1][h], e >> 1), sel),
+                           __byte_perm(word(vr[kt][2][h], e >> 1), word(vr[kt][3][h], e >> 1), sel));
             }
         }
       }
+      if (s + 1 < steps) load_v(nxt);
       cur = nxt;
       nxt = aft;
+    }
+    if (FP8) {   // O relative to m, like l
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float f = m[h] == -INFINITY ? 0.f : ex2_approx(mp[h] - kUp - m[h]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          o[i][2 * h] *= f;
+          o[i][2 * h + 1] *= f;
+        }
+      }
     }
     // the four lanes of a row, then the four warps
 #pragma unroll
     for (int d = 1; d < 4; d <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+      l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
+      l[1] += __shfl_xor_sync(0xffffffffu, l[1], d);
     }
     if (t == 0) {
-      sm.m[warp][g] = m0;
-      sm.m[warp][g + 8] = m1;
-      sm.l[warp][g] = l0;
-      sm.l[warp][g + 8] = l1;
+      sm.m[warp][g] = m[0];
+      sm.m[warp][g + 8] = m[1];
+      sm.l[warp][g] = l[0];
+      sm.l[warp][g + 8] = l[1];
     }
     // output column n = 2t + e of product i is dim 16 n + i (e4m3) or 64 (i / 8) + 8 n + i % 8 (bf16)
 #pragma unroll
@@ -390,6 +496,7 @@ cudaError_t launch_paged_decode(const PagedAttnDesc& a, cudaStream_t st) {
   p.g.window = a.window;
   p.part_rows = kRows;
   p.min_blocks = 1;
+  p.page_shift = page_shift(a.kv.page_size);
   const PagedScratch L = paged_scratch_layout(a.rb.batch, kDecodeCtas, kRows, DH);
   uint8_t* sc = static_cast<uint8_t*>(a.scratch);
   p.prefix = reinterpret_cast<long long*>(sc + L.prefix);

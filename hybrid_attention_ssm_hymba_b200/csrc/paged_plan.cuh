@@ -33,10 +33,16 @@ struct PagedAttnParams {
   float* part;          // [CTA][2][part_rows][dh]: 0 = the CTA's first tile continued, 1 = its last tile begun
   float2* part_ml;      // [CTA][2][part_rows] (m in log2 units, sum)
   int part_rows;
+  int page_shift;       // log2(page_size) where that is a power of two, else -1
   int piece;            // tensor-core kernel: rows of one K/V load
   float scale_log2;     // log2(e) / sqrt(dh)
   unsigned* status;
 };
+inline int page_shift(int page_size) {
+  int s = 0;
+  while ((1 << s) < page_size) ++s;
+  return (1 << s) == page_size ? s : -1;
+}
 struct PagedScratch {
   size_t prefix, part, ml, total;
 };
