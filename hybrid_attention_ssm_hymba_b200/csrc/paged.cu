@@ -198,14 +198,14 @@ cudaError_t launch_paged_read(const PagedKv& kv, const RaggedBatch& rb, void* k,
 
 // paged_decode.cu (at most 16 rows per K/V head) and paged_attn_tc.cu
 bool paged_decode_takes(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads);
-size_t paged_decode_scratch(const RaggedBatch& rb);
+size_t paged_decode_scratch(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads);
 cudaError_t launch_paged_decode(const PagedAttnDesc& a, cudaStream_t st);
 size_t paged_attention_tc_scratch(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads);
 cudaError_t launch_paged_attention_tc(const PagedAttnDesc& a, cudaStream_t st);
 
 size_t paged_attention_scratch(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads, bool bf16) {
   if (!bf16) return 0;
-  return paged_decode_takes(kv, rb, n_q_heads) ? paged_decode_scratch(rb) : paged_attention_tc_scratch(kv, rb, n_q_heads);
+  return paged_decode_takes(kv, rb, n_q_heads) ? paged_decode_scratch(kv, rb, n_q_heads) : paged_attention_tc_scratch(kv, rb, n_q_heads);
 }
 
 cudaError_t launch_paged_attention(const PagedAttnDesc& a, cudaStream_t st) {

@@ -5,19 +5,20 @@
 //   out = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m),  s_j = log2(e) q.k_j / sqrt(dh)
 //
 // Every K/V row is read once for all query heads that share it, and that reading bounds the
-// call.  The rows are the 16 rows of mma.sync m16n8k16 products (a 128-row tensor-core tile
-// would be mostly empty, and its K and V would have to pass through shared memory); K and V go
-// from global memory straight to the registers that the products read: the order of the
-// summed index (dims for Q K^T, keys for P V) and of the output columns is free, so each lane
-// loads 16 consecutive bytes of a row and the products are told apart by that order alone.
-//   Q K^T  lane (g, t) holds, of key g of eight, the dims of its 16-byte pieces (the four
-//          lanes of a key read 64 consecutive bytes); Q is read in the same order.
-//   P V    lane (g, t) holds keys 2t, 2t+1, 2t+8, 2t+9 of sixteen (as Q K^T left their P) at
-//          the dims of piece g (eight lanes read 128 consecutive bytes); the two keys of a
-//          register are put together by one byte permutation.
+// call.  The products are mma.sync m16n8k16 with the keys (Q K^T) and the dims (P V) as the
+// sixteen rows and the queries as the eight columns, one or two such tiles (a 128-row
+// tensor-core tile would be mostly empty, and its K and V would have to pass through shared
+// memory); K and V go from global memory straight to the registers that the products read: the
+// order of the summed index and of the output's rows is free, so each lane loads 16 consecutive
+// bytes of a row and the products are told apart by that order alone.
+//   K Q^T  lane (g, t) holds, of keys g and g + 8 of sixteen, the dims of its 16-byte pieces
+//          (the four lanes of a key read 64 consecutive bytes); Q is read in the same order.
+//   V^T P^T  lane (g, t) holds keys 2t, 2t+1, 2t+8, 2t+9 of sixteen at the dims of piece g
+//          (eight lanes read 128 consecutive bytes); the two keys of a register are put together
+//          by one byte permutation, and P's 8 x 8 pieces are transposed between the lanes.
 // A CTA of four warps takes 32 keys of each 128-key block per warp and walks its part of the
-// line of blocks (paged_plan.cuh).  K of the next step is loaded as soon as Q K^T has read this
-// one's, V as soon as P V has, page numbers two steps and scales one step earlier.
+// line of blocks (paged_plan.cuh).  K of the next step is loaded as soon as K Q^T has read this
+// one's, V as soon as V^T P^T has, page numbers two steps and scales one step earlier.
 //
 // e4m3 codes are exact in fp16, one conversion for two of them, so the 8-bit products run in
 // fp16 with their ranges kept by powers of two: a row of Q is scaled to at most 2^8 (its bf16
@@ -31,6 +32,7 @@ namespace {
 constexpr int DH = 128, kWarps = 4, kRows = 16;
 constexpr int kPlanBatch = 1024;   // batches up to this are planned by every CTA itself
 constexpr float kLazy = 7.f;       // a maximum moves when it is exceeded by 2^7: n_j stays below 2^15
+constexpr float kLazySum = 60.f;   // the same for a sum in fp32
 constexpr float kUp = 8.f;         // the exponent added to n_j
 
 template <bool F16>
@@ -69,6 +71,12 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
 }
 // Two bf16 values times f as fp16.
 __device__ __forceinline__ uint32_t f16_of_bf16(uint32_t u, float f) { return pack_f16(bf16lo(u) * f, bf16hi(u) * f); }
+// The transpose of an 8 x 8 matrix of 16-bit values, row g's columns 2t, 2t + 1 in lane (g, t).
+__device__ __forceinline__ uint32_t transpose8(uint32_t u) {
+  uint32_t v;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(v) : "r"(u));
+  return v;
+}
 __device__ __forceinline__ float lg2_approx(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -85,7 +93,6 @@ struct Key {
 struct Shared {
   float m[kWarps][kRows], l[kWarps][kRows];
   float o[kWarps][kRows][DH + 4];
-  float scale[kWarps][2][2][32];   // [warp][step parity][K, log2 V][key]
   long long prefix[kPlanBatch + 1];
   long long warp_sum[kWarps];
 };
@@ -128,15 +135,15 @@ __device__ void plan_here(const PagedAttnParams& p, Shared& sm, bool report) {
     for (int b = threadIdx.x; b <= p.rb.batch; b += 32 * kWarps) p.prefix[b] = sm.prefix[b];
 }
 
-template <bool FP8>
-__global__ void __launch_bounds__(32 * kWarps, 2) paged_decode_kernel(const __grid_constant__ PagedAttnParams p) {
+// NT: tiles of eight queries.
+template <bool FP8, int NT>
+__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) paged_decode_kernel(const __grid_constant__ PagedAttnParams p) {
   constexpr int kStep = FP8 ? 32 : 16;       // keys of a warp's step: 4 KB of K and of V either way
   constexpr int kSub = 32 / kStep;           // steps per block and warp
-  constexpr int kNt = kStep / 8, kKt = kStep / 16;
+  constexpr int kKt = kStep / 16;
   constexpr int es = FP8 ? 1 : 2;
   constexpr unsigned kAll = kStep == 32 ? 0xffffffffu : 0xffffu;
   __shared__ Shared sm;
-  pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const long long* prefix = p.prefix;
@@ -153,14 +160,16 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_decode_kernel(const __gr
   walk.init(p, prefix);
   while (walk.next(p, &pc)) {
     const int rows = pc.ts.toks * p.g.G;
-    // Q of rows g and g + 8 in the dims' order; qs turns a product into log2 units
-    uint32_t qa[8][4];
-    float qs[2];
+    // Q of queries 8 n + g in the dims' order; qs turns the products of queries 8 n + 2t + e into
+    // log2 units; at: those queries' places in the sequence
+    uint32_t qb[NT][8][2];
+    float qs[NT][2];
+    int at[NT][2];
     {
       const __nv_bfloat16* q0 = p.q + pc.row0 * p.q_ld + static_cast<long long>(pc.kvh) * p.g.G * DH;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int r = g + 8 * half;
+      for (int n = 0; n < NT; ++n) {
+        const int r = 8 * n + g;
         const uint4* q = reinterpret_cast<const uint4*>(q0 + (r / p.g.G) * p.q_ld + (r % p.g.G) * DH);
         uint4 v[4];
         uint32_t mx = 0;
@@ -173,25 +182,28 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_decode_kernel(const __gr
             for (int w = 0; w < 4; ++w) mx = max(mx, max(word(v[j], w) & 0x7fffu, (word(v[j], w) >> 16) & 0x7fffu));
           }
         }
-        float up = 1.f;
-        qs[half] = p.scale_log2;
+        float up = 1.f, down = p.scale_log2;
         if (FP8) {   // the row times 2^(f - 127), so that its largest value is in [2^7, 2^8)
           mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           const int f = min(261 - static_cast<int>(mx >> 7), 253);
           up = __uint_as_float(static_cast<uint32_t>(f) << 23);
-          qs[half] *= __uint_as_float(static_cast<uint32_t>(254 - f) << 23);
+          down *= __uint_as_float(static_cast<uint32_t>(254 - f) << 23);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          qa[2 * j][half] = FP8 ? f16_of_bf16(v[j].x, up) : v[j].x;
-          qa[2 * j][2 + half] = FP8 ? f16_of_bf16(v[j].y, up) : v[j].y;
-          qa[2 * j + 1][half] = FP8 ? f16_of_bf16(v[j].z, up) : v[j].z;
-          qa[2 * j + 1][2 + half] = FP8 ? f16_of_bf16(v[j].w, up) : v[j].w;
+          qb[n][2 * j][0] = FP8 ? f16_of_bf16(v[j].x, up) : v[j].x;
+          qb[n][2 * j][1] = FP8 ? f16_of_bf16(v[j].y, up) : v[j].y;
+          qb[n][2 * j + 1][0] = FP8 ? f16_of_bf16(v[j].z, up) : v[j].z;
+          qb[n][2 * j + 1][1] = FP8 ? f16_of_bf16(v[j].w, up) : v[j].w;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          qs[n][e] = __shfl_sync(0xffffffffu, down, (2 * t + e) * 4);
+          at[n][e] = pc.ts.p0 + (8 * n + 2 * t + e) / p.g.G;
         }
       }
     }
-    const int i0 = pc.ts.p0 + g / p.g.G, i1 = pc.ts.p0 + (g + 8) / p.g.G;   // places of the two rows
     const int lo = p.g.window < 0 ? 0 : pc.ts.p0 - p.g.window;             // first key of any row's window
     const uint8_t* kh = kbase + pc.kvh * (DH * es) + t * 16;
     const uint8_t* vh = vbase + pc.kvh * (DH * es) + g * 16;
@@ -225,15 +237,17 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_decode_kernel(const __gr
     // a key that is not there loads the pool's first row (a predicated or branched load costs the
     // kernel a quarter of its time and more); its scores are hidden and its V is zeroed below
     constexpr int kLoadsK = FP8 ? 2 : 4, kLoadsV = FP8 ? 1 : 2;   // 16-byte pieces of a key per lane
-    uint4 kr[kNt][kLoadsK], vr[kKt][4][kLoadsV];
+    uint4 kr[kKt][2][kLoadsK], vr[kKt][4][kLoadsV];
     auto load_k = [&](const Key& k) {
 #pragma unroll
-      for (int nt = 0; nt < kNt; ++nt) {
-        const int row = __shfl_sync(0xffffffffu, k.row, nt * 8 + g);
-        const uint8_t* a = kh + max(row, 0) * row_bytes;
+      for (int kt = 0; kt < kKt; ++kt)
 #pragma unroll
-        for (int j = 0; j < kLoadsK; ++j) kr[nt][j] = ldg_once(a + j * 64);
-      }
+        for (int h = 0; h < 2; ++h) {
+          const int row = __shfl_sync(0xffffffffu, k.row, kt * 16 + h * 8 + g);
+          const uint8_t* a = kh + max(row, 0) * row_bytes;
+#pragma unroll
+          for (int j = 0; j < kLoadsK; ++j) kr[kt][h][j] = ldg_once(a + j * 64);
+        }
     };
     auto load_v = [&](const Key& k) {
 #pragma unroll
@@ -247,121 +261,159 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_decode_kernel(const __gr
         }
     };
 
-    // mp: the running maxima of what P V sums (e4m3); m, l: of the softmax itself
-    float o[16][4], m[2] = {-INFINITY, -INFINITY}, mp[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    // of queries 8 n + 2t + e: m, l of the softmax; mp (e4m3) the running maximum of what P V sums
+    float o[NT][8][4], m[NT][2], mp[NT][2], l[NT][2];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+      for (int e = 0; e < 2; ++e) {
+        m[n][e] = mp[n][e] = -INFINITY;
+        l[n][e] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
+    }
     const int pg1 = lookup(1);
     int pg2 = lookup(2);
     Key cur = find(0, lookup(0)), nxt = find(1, pg1);
     load_k(cur);
     load_v(cur);
     for (int s = 0; s < steps; ++s) {
-      const Key aft = find(s + 2, pg2);
-      pg2 = lookup(s + 3);
-      float (&sc_k)[32] = sm.scale[warp][s & 1][0], (&sc_v)[32] = sm.scale[warp][s & 1][1];
-      if (FP8) {
-        sc_k[lane] = cur.sk;
-        sc_v[lane] = cur.row >= 0 ? lg2_approx(cur.sv) : 0.f;
-        __syncwarp();
-      }
-      // S = Q K^T
-      float sc[kNt][4];
+      // sc[n][kt]: keys g (elements 0, 1) and g + 8 (2, 3) of sixteen, queries 2t (0, 2), 2t + 1 (1, 3)
+      float sc[NT][kKt][4];
 #pragma unroll
-      for (int nt = 0; nt < kNt; ++nt) {
+      for (int kt = 0; kt < kKt; ++kt) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[n][kt][e] = 0.f;
 #pragma unroll
         for (int j = 0; j < kLoadsK; ++j) {
-          if constexpr (FP8) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-              mma16<true>(sc[nt], qa[4 * j + w], f16_of_e4m3(word(kr[nt][j], w), 0), f16_of_e4m3(word(kr[nt][j], w), 1));
-          } else {
-            mma16<false>(sc[nt], qa[2 * j], kr[nt][j].x, kr[nt][j].y);
-            mma16<false>(sc[nt], qa[2 * j + 1], kr[nt][j].z, kr[nt][j].w);
+          for (int w = 0; w < (FP8 ? 4 : 2); ++w) {
+            uint32_t a[4];
+            if constexpr (FP8) {
+              a[0] = f16_of_e4m3(word(kr[kt][0][j], w), 0);
+              a[1] = f16_of_e4m3(word(kr[kt][1][j], w), 0);
+              a[2] = f16_of_e4m3(word(kr[kt][0][j], w), 1);
+              a[3] = f16_of_e4m3(word(kr[kt][1][j], w), 1);
+            } else {
+              a[0] = word(kr[kt][0][j], 2 * w);
+              a[1] = word(kr[kt][1][j], 2 * w);
+              a[2] = word(kr[kt][0][j], 2 * w + 1);
+              a[3] = word(kr[kt][1][j], 2 * w + 1);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const uint32_t (&b)[2] = qb[n][(FP8 ? 4 : 2) * j + w];
+              mma16<FP8>(sc[n][kt], a, b[0], b[1]);
+            }
           }
         }
       }
       if (s + 1 < steps) load_k(nxt);
-      if (FP8) {
+      // K's scales and log2 of V's, of keys g and g + 8
+      float lv[kKt][2];
+      const float own_lv = FP8 && cur.row >= 0 ? lg2_approx(cur.sv) : 0.f;
 #pragma unroll
-        for (int nt = 0; nt < kNt; ++nt) {
-          const float2 k = *reinterpret_cast<const float2*>(&sc_k[nt * 8 + 2 * t]);
+      for (int kt = 0; kt < kKt; ++kt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[nt][e] *= e & 1 ? k.y : k.x;
+        for (int h = 0; h < 2; ++h) {
+          lv[kt][h] = 0.f;
+          if (FP8) {
+            const float sk = __shfl_sync(0xffffffffu, cur.sk, kt * 16 + h * 8 + g);
+            lv[kt][h] = __shfl_sync(0xffffffffu, own_lv, kt * 16 + h * 8 + g);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              sc[n][kt][2 * h] *= sk;
+              sc[n][kt][2 * h + 1] *= sk;
+            }
+          }
         }
-      }
       // hidden keys -inf (most steps have none)
       const int k0 = key0(s), k1 = k0 + kStep - 1;
       const unsigned there = __ballot_sync(0xffffffffu, cur.row >= 0);
-      if (there != kAll || k1 > pc.ts.p0 ||
-          (p.g.window >= 0 && pc.ts.p1 - k0 > p.g.window && k1 >= p.g.n_meta)) {
+      if (there != kAll || k1 > pc.ts.p0 || (p.g.window >= 0 && pc.ts.p1 - k0 > p.g.window && k1 >= p.g.n_meta)) {
 #pragma unroll
-        for (int nt = 0; nt < kNt; ++nt)
+        for (int kt = 0; kt < kKt; ++kt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int c = nt * 8 + 2 * t + e;
+          for (int h = 0; h < 2; ++h) {
+            const int c = kt * 16 + h * 8 + g;
             const bool in = (there >> c) & 1u;
-            if (!in || !key_visible(p.g, i0, k0 + c)) sc[nt][e] = -INFINITY;
-            if (!in || !key_visible(p.g, i1, k0 + c)) sc[nt][2 + e] = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (!in || !key_visible(p.g, at[n][e], k0 + c)) sc[n][kt][2 * h + e] = -INFINITY;
           }
       }
-      // the maxima of both rows: of the scores and (e4m3) of the scores with log2 sv in them
-      float mx[2] = {-INFINITY, -INFINITY}, mxp[2] = {-INFINITY, -INFINITY};
-      float2 lv[kNt];
-#pragma unroll
-      for (int nt = 0; nt < kNt; ++nt) {
-        if (FP8) lv[nt] = *reinterpret_cast<const float2*>(&sc_v[nt * 8 + 2 * t]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          mx[h] = fmaxf(mx[h], fmaxf(sc[nt][2 * h], sc[nt][2 * h + 1]));
-          if (FP8)
-            mxp[h] = fmaxf(mxp[h], fmaxf(fmaf(sc[nt][2 * h], qs[h], lv[nt].x), fmaf(sc[nt][2 * h + 1], qs[h], lv[nt].y)));
-        }
-      }
+      // this lane's maxima of each query: of the scores and (e4m3) of the scores with log2 sv in
+      // them.  The lanes meet only when one of them has to move a reference: sums of 2^(s - m)
+      // stay finite far beyond m, P's 16 bits set the limit for what they hold
       bool move = false;
+      float mx[NT][2], mxp[NT][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        mx[h] *= qs[h];
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int d = 1; d < 4; d <<= 1) {
-          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], d));
-          if (FP8) mxp[h] = fmaxf(mxp[h], __shfl_xor_sync(0xffffffffu, mxp[h], d));
+        for (int e = 0; e < 2; ++e) {
+          float x = -INFINITY, y = -INFINITY;
+#pragma unroll
+          for (int kt = 0; kt < kKt; ++kt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              x = fmaxf(x, sc[n][kt][2 * h + e]);
+              if (FP8) y = fmaxf(y, fmaf(sc[n][kt][2 * h + e], qs[n][e], lv[kt][h]));
+            }
+          mx[n][e] = x * qs[n][e];
+          mxp[n][e] = y;
+          move |= mx[n][e] > m[n][e] + (FP8 ? kLazySum : kLazy) || (FP8 && y > mp[n][e] + kLazy);
         }
-        move |= mx[h] > m[h] + kLazy || (FP8 && mxp[h] > mp[h] + kLazy);
-      }
       if (__any_sync(0xffffffffu, move)) {
-        float ao[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float n = fmaxf(m[h], mx[h]), np = FP8 ? fmaxf(mp[h], mxp[h]) : n;
-          const float a = n == -INFINITY ? 1.f : ex2_approx(m[h] - n);
-          l[h] *= a;
-          ao[h] = FP8 ? (np == -INFINITY ? 1.f : ex2_approx(mp[h] - np)) : a;
-          m[h] = n;
-          mp[h] = np;
-        }
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+          for (int e = 0; e < 2; ++e) {
+            float nm = fmaxf(m[n][e], mx[n][e]), np = fmaxf(mp[n][e], mxp[n][e]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[i][e] *= ao[e >> 1];
+            for (int d = 4; d < 32; d <<= 1) {
+              nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, d));
+              if (FP8) np = fmaxf(np, __shfl_xor_sync(0xffffffffu, np, d));
+            }
+            const float al = nm == -INFINITY ? 1.f : ex2_approx(m[n][e] - nm);
+            const float ao = FP8 ? (np == -INFINITY ? 1.f : ex2_approx(mp[n][e] - np)) : al;
+            l[n][e] *= al;
+            m[n][e] = nm;
+            mp[n][e] = FP8 ? np : nm;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              o[n][i][e] *= ao;
+              o[n][i][2 + e] *= ao;
+            }
+          }
       }
-      uint32_t pa[kKt][4];   // the rows of P V, rounded once to the products' 16 bits
+      uint32_t pb[NT][kKt][2];   // P, rounded once to the products' 16 bits, transposed
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float r = m[h] == -INFINITY ? 0.f : m[h], rp = mp[h] == -INFINITY ? 0.f : mp[h] - kUp;
+      for (int n = 0; n < NT; ++n) {
+        float r[2], rp[2];
 #pragma unroll
-        for (int nt = 0; nt < kNt; ++nt) {
-          const float x0 = ex2_approx(fmaf(sc[nt][2 * h], qs[h], -r)), x1 = ex2_approx(fmaf(sc[nt][2 * h + 1], qs[h], -r));
-          l[h] += x0 + x1;
-          pa[nt >> 1][2 * (nt & 1) + h] =
-              FP8 ? pack_f16(ex2_approx(fmaf(sc[nt][2 * h], qs[h], lv[nt].x - rp)),
-                             ex2_approx(fmaf(sc[nt][2 * h + 1], qs[h], lv[nt].y - rp)))
-                  : pack_bf16(x0, x1);
+        for (int e = 0; e < 2; ++e) {
+          r[e] = m[n][e] == -INFINITY ? 0.f : m[n][e];
+          rp[e] = mp[n][e] == -INFINITY ? 0.f : mp[n][e] - kUp;
         }
+#pragma unroll
+        for (int kt = 0; kt < kKt; ++kt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float s0 = sc[n][kt][2 * h], s1 = sc[n][kt][2 * h + 1];
+            const float x0 = ex2_approx(fmaf(s0, qs[n][0], -r[0])), x1 = ex2_approx(fmaf(s1, qs[n][1], -r[1]));
+            l[n][0] += x0;
+            l[n][1] += x1;
+            pb[n][kt][h] = transpose8(FP8 ? pack_f16(ex2_approx(fmaf(s0, qs[n][0], lv[kt][h] - rp[0])),
+                                                     ex2_approx(fmaf(s1, qs[n][1], lv[kt][h] - rp[1])))
+                                          : pack_bf16(x0, x1));
+          }
       }
       // O += P V
       if (there != kAll) {
@@ -374,68 +426,53 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_decode_kernel(const __gr
               if (!((there >> (kt * 16 + 2 * t + (c & 1) + (c >> 1) * 8)) & 1u)) vr[kt][c][h] = make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int kt = 0; kt < kKt; ++kt) {
-        if constexpr (FP8) {
+      for (int kt = 0; kt < kKt; ++kt)
 #pragma unroll
-          for (int w = 0; w < 4; ++w)
+        for (int i = 0; i < 8; ++i) {   // two neighbouring dims, of two keys each: the pieces' word i / 2 (e4m3), i (bf16)
+          const int w = FP8 ? i >> 1 : i & 3, h = FP8 ? 0 : i >> 2;
+          const uint32_t a0 = word(vr[kt][0][h], w), a1 = word(vr[kt][1][h], w), a2 = word(vr[kt][2][h], w), a3 = word(vr[kt][3][h], w);
+          uint32_t a[4];
+          if constexpr (FP8) {
+            const uint32_t sel = i & 1 ? 0x7362 : 0x5140;
+            const uint32_t x = __byte_perm(a0, a1, sel), y = __byte_perm(a2, a3, sel);
+            a[0] = f16_of_e4m3(x, 0);
+            a[1] = f16_of_e4m3(x, 1);
+            a[2] = f16_of_e4m3(y, 0);
+            a[3] = f16_of_e4m3(y, 1);
+          } else {
+            a[0] = __byte_perm(a0, a1, 0x5410);
+            a[1] = __byte_perm(a0, a1, 0x7632);
+            a[2] = __byte_perm(a2, a3, 0x5410);
+            a[3] = __byte_perm(a2, a3, 0x7632);
+          }
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {   // dims 2b, 2b + 1 of the word: (key, next key) of each
-              const uint32_t sel = b ? 0x7362 : 0x5140;
-              const uint32_t x = __byte_perm(word(vr[kt][0][0], w), word(vr[kt][1][0], w), sel),
-                             y = __byte_perm(word(vr[kt][2][0], w), word(vr[kt][3][0], w), sel);
-              mma16<true>(o[4 * w + 2 * b], pa[kt], f16_of_e4m3(x, 0), f16_of_e4m3(y, 0));
-              mma16<true>(o[4 * w + 2 * b + 1], pa[kt], f16_of_e4m3(x, 1), f16_of_e4m3(y, 1));
-            }
-        } else {
-#pragma unroll
-          for (int h = 0; h < kLoadsV; ++h)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint32_t sel = e & 1 ? 0x7632 : 0x5410;
-              mma16<false>(o[8 * h + e], pa[kt], __byte_perm(word(vr[kt][0][h], e >> 1), word(vr[kt][1][h], e >> 1), sel),
-                           __byte_perm(word(vr[kt][2][h], e >> 1), word(vr[kt][3][h], e >> 1), sel));
-            }
+          for (int n = 0; n < NT; ++n) mma16<FP8>(o[n][i], a, pb[n][kt][0], pb[n][kt][1]);
         }
-      }
       if (s + 1 < steps) load_v(nxt);
       cur = nxt;
-      nxt = aft;
+      nxt = find(s + 2, pg2);
+      pg2 = lookup(s + 3);
     }
-    if (FP8) {   // O relative to m, like l
+    // the lanes of a query, then the four warps; O relative to m, like l
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float f = m[h] == -INFINITY ? 0.f : ex2_approx(mp[h] - kUp - m[h]);
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          o[i][2 * h] *= f;
-          o[i][2 * h + 1] *= f;
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * n + 2 * t + e;
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
+        if (g == 0) {
+          sm.m[warp][r] = m[n][e];
+          sm.l[warp][r] = l[n][e];
         }
-      }
-    }
-    // the four lanes of a row, then the four warps
-#pragma unroll
-    for (int d = 1; d < 4; d <<= 1) {
-      l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
-      l[1] += __shfl_xor_sync(0xffffffffu, l[1], d);
-    }
-    if (t == 0) {
-      sm.m[warp][g] = m[0];
-      sm.m[warp][g + 8] = m[1];
-      sm.l[warp][g] = l[0];
-      sm.l[warp][g + 8] = l[1];
-    }
-    // output column n = 2t + e of product i is dim 16 n + i (e4m3) or 64 (i / 8) + 8 n + i % 8 (bf16)
-#pragma unroll
-    for (int half = 0; half < 2; ++half)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
+        const float f = !FP8 ? 1.f : m[n][e] == -INFINITY ? 0.f : ex2_approx(mp[n][e] - kUp - m[n][e]);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int n = 2 * t + e, dim = FP8 ? 16 * n + 4 * q : 64 * (q >> 1) + 8 * n + 4 * (q & 1);
-          *reinterpret_cast<float4*>(&sm.o[warp][g + 8 * half][dim]) =
-              make_float4(o[4 * q][2 * half + e], o[4 * q + 1][2 * half + e], o[4 * q + 2][2 * half + e],
-                          o[4 * q + 3][2 * half + e]);
+          const int dim = FP8 ? 16 * g + 4 * q : 64 * (q >> 1) + 8 * g + 4 * (q & 1);
+          *reinterpret_cast<float4*>(&sm.o[warp][r][dim]) =
+              make_float4(o[n][2 * q][e] * f, o[n][2 * q][2 + e] * f, o[n][2 * q + 1][e] * f, o[n][2 * q + 1][2 + e] * f);
         }
+      }
     __syncthreads();
     {
       const int r = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * 4;
@@ -470,10 +507,15 @@ __global__ void __launch_bounds__(32 * kWarps, 2) paged_decode_kernel(const __gr
     }
     __syncthreads();
   }
+  // not at the start: the join's CTAs would take places next to this kernel's and keep the next
+  // call's from theirs (16 long histories, called in a row: 125 us against 78)
+  pdl_trigger();
 }
 
-// Two CTAs per SM (their registers allow no third).
-constexpr int kDecodeCtas = 2 * 148;
+// CTAs per SM that the registers allow, with one and with two tiles of queries.
+constexpr int kPerSm[2] = {3, 2};
+constexpr int kMaxSms = 148;   // the scratch is sized for the B200
+int query_tiles(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads) { return rb.max_rows * (n_q_heads / kv.hkv) <= 8 ? 1 : 2; }
 
 }  // namespace
 
@@ -482,8 +524,9 @@ bool paged_decode_takes(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads)
   return static_cast<long long>(rb.max_rows) * (n_q_heads / kv.hkv) <= kRows;
 }
 
-size_t paged_decode_scratch(const RaggedBatch& rb) {
-  return paged_scratch_layout(rb.batch, kDecodeCtas, kRows, DH).total;
+size_t paged_decode_scratch(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads) {
+  const int nt = query_tiles(kv, rb, n_q_heads);
+  return paged_scratch_layout(rb.batch, kPerSm[nt - 1] * kMaxSms, 8 * nt, DH).total;
 }
 
 cudaError_t launch_paged_decode(const PagedAttnDesc& a, cudaStream_t st) {
@@ -494,10 +537,11 @@ cudaError_t launch_paged_decode(const PagedAttnDesc& a, cudaStream_t st) {
   p.g.TQ = p.g.tile_tok = a.rb.max_rows;
   p.g.n_meta = a.n_meta;
   p.g.window = a.window;
-  p.part_rows = kRows;
+  const int nt = query_tiles(a.kv, a.rb, a.n_q_heads);
+  p.part_rows = 8 * nt;
   p.min_blocks = 1;
   p.page_shift = page_shift(a.kv.page_size);
-  const PagedScratch L = paged_scratch_layout(a.rb.batch, kDecodeCtas, kRows, DH);
+  const PagedScratch L = paged_scratch_layout(a.rb.batch, kPerSm[nt - 1] * kMaxSms, p.part_rows, DH);
   uint8_t* sc = static_cast<uint8_t*>(a.scratch);
   p.prefix = reinterpret_cast<long long*>(sc + L.prefix);
   p.part = reinterpret_cast<float*>(sc + L.part);
@@ -508,12 +552,12 @@ cudaError_t launch_paged_decode(const PagedAttnDesc& a, cudaStream_t st) {
   p.out_ld = a.out_ld;
   p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(DH));
   p.status = a.status;
-  const int ctas = 2 * num_sms() < kDecodeCtas ? 2 * num_sms() : kDecodeCtas;
+  const int ctas = kPerSm[nt - 1] * (num_sms() < kMaxSms ? num_sms() : kMaxSms);
   if (a.rb.batch > kPlanBatch)
     if (cudaError_t e = launch(paged_plan_kernel, dim3(1), dim3(1024), 0, st, a.kv, a.rb, p.g, p.prefix, a.status)) return e;
-  if (cudaError_t e = a.kv.type == CACHE_E4M3 ? launch(paged_decode_kernel<true>, dim3(ctas), dim3(32 * kWarps), 0, st, p)
-                                              : launch(paged_decode_kernel<false>, dim3(ctas), dim3(32 * kWarps), 0, st, p))
-    return e;
+  const auto kernel = a.kv.type == CACHE_E4M3 ? (nt == 1 ? paged_decode_kernel<true, 1> : paged_decode_kernel<true, 2>)
+                                              : (nt == 1 ? paged_decode_kernel<false, 1> : paged_decode_kernel<false, 2>);
+  if (cudaError_t e = launch(kernel, dim3(ctas), dim3(32 * kWarps), 0, st, p)) return e;
   return launch_paged_join(p, ctas, st);
 }
 
