@@ -57,32 +57,219 @@ __global__ void __launch_bounds__(256) dequantize_w4_kernel(const uint32_t* __re
   v.store(w + i * 8);
 }
 
-// One warp per (n, m): every lane takes eight consecutive k at a time.
-template <typename T>
-__global__ void __launch_bounds__(256) gemm_w4_simple(const T* __restrict__ a, const uint32_t* __restrict__ q4,
-                                                      const float* __restrict__ scales, T* __restrict__ c, int M,
-                                                      int N, int K, int group) {
+// C = A W^T for a few rows of A on mma.sync m16n8k16: W's rows are the products' 16 rows, A's
+// rows their 8 columns (NT tiles of them), so 16 x 16 weights meet all rows of A in one
+// instruction and the stream over W stays what bounds the kernel (CUDA-core sums would take
+// longer than the stream from three rows on).  q in [-8, 7] is exact in bf16: a group's
+// products are summed in fp32 by the tensor core and scaled once per group.  fp32 rows of A are
+// split into three bf16 columns (8 + 8 + 8 of the 24 bits), which are summed at the end.
+//
+// A CTA of 16 warps owns a range of 16-row tiles and takes K in slabs whose columns of A fit
+// shared memory, already in the order of the products.  The S warps of a group share a tile:
+// each streams chunks of 256 k (16 rows x 128 bytes) through a ring of its own by cp.async, and
+// their sums meet in shared memory at the tile's end.
+//
+// The 32 k of 16 bytes of a row are one or part of one group; lane (g, t) takes 4 of them
+// (8 k) of rows g and g + 8.  A word's nibbles i and i + 4 make one bf16 pair: (word >> 4 i)
+// & 0x000f000f over the bits of 128.0 is 128 + code, and 136 less is q.
+constexpr int kWarps = 16, kChunk = 256, kRowPitch = kChunk / 2 + 16, kTileRowsMax = 128;
+
+struct GemmW4Params {
+  const void* a;
+  const uint8_t* q4;
+  const float* scales;
+  void* c;
+  int M, N, K, gshift, tiles, slab, S;   // gshift: log2(group); slab: k of one pass; S: warps that share a tile
+};
+
+template <int NT> struct W4Shape {
+  static constexpr int ring = NT <= 2 ? 3 : 2;
+  static constexpr int slab = NT == 1 ? 4096 : NT <= 3 ? 1024 : 512;
+  static constexpr int x_bytes = slab / 32 * NT * 8 * 64;
+  static constexpr int stage = 16 * kRowPitch + 16 * 8 * 4;      // codes, then scales [row][8]
+  static constexpr int red_bytes = kWarps * 16 * 8 * NT * 4;
+  static constexpr int acc_bytes = kTileRowsMax * 8 * NT * 4;
+  static constexpr int smem = x_bytes + kWarps * ring * stage + red_bytes + acc_bytes;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// q of nibbles i and i + 4 of a word as a bf16 pair.
+__device__ __forceinline__ uint32_t q_pair(uint32_t u, int i) {
+  const uint32_t v = ((u >> (4 * i)) & 0x000f000fu) | 0x43004300u, off = 0x43084308u;   // 128 + code, 136
+  const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&off));
+  return *reinterpret_cast<const uint32_t*>(&q);
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_constant__ GemmW4Params p) {
+  using W = W4Shape<NT>;
+  constexpr int kSplit = sizeof(T) == 4 ? 3 : 1;   // columns of a row of A
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint4* sx = reinterpret_cast<uint4*>(smem);                       // [k / 32][column][t]
+  uint8_t* ring = smem + W::x_bytes;
+  float* red = reinterpret_cast<float*>(ring + kWarps * W::ring * W::stage);   // [warp][row][column]
+  float* acc = red + kWarps * 16 * 8 * NT;                                     // [row of the CTA][column]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int tile0 = static_cast<int>(static_cast<long long>(blockIdx.x) * p.tiles / gridDim.x),
+            tile1 = static_cast<int>(static_cast<long long>(blockIdx.x + 1) * p.tiles / gridDim.x);
+  const int grp = warp / p.S, ws = warp - grp * p.S, groups = kWarps / p.S;
+  const int my_tiles = (tile1 - tile0 - grp + groups - 1) / groups;   // tiles tile0 + grp, + groups, ...
+  const int per_chunk = kChunk >> p.gshift;                           // scales of a row and chunk
+  const long long row_bytes = p.K / 2, row_scales = p.K >> p.gshift;
+  // the warps of a tile (a barrier of theirs: at most eight groups of two or more)
+  auto meet = [&] {
+    if (p.S == 1) __syncwarp();
+    else bar_sync_n(1 + grp, 32 * p.S);
+  };
+  uint8_t* mine = ring + warp * W::ring * W::stage;
   pdl_trigger();
   pdl_wait();
-  const long long wid = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (wid >= static_cast<long long>(M) * N) return;
-  const int n = static_cast<int>(wid / M), m = static_cast<int>(wid % M);
-  float acc = 0.f;
-  for (int k8 = lane; k8 < K / 8; k8 += 32) {
-    const uint32_t u = q4[static_cast<long long>(n) * (K / 8) + k8];
-    const float s = scales[static_cast<long long>(n) * (K / group) + k8 / (group / 8)];
-    Vec8<T> v;
-    float f[8], t = 0.f;
-    v.load(a + static_cast<long long>(m) * K + k8 * 8);
-    v.to_f32(f);
+  for (int k0 = 0; k0 < p.K; k0 += p.slab) {
+    const int ks = min(p.slab, p.K - k0), chunks = (ks + kChunk - 1) / kChunk;
+    const int cpw = ws < chunks ? (chunks - ws + p.S - 1) / p.S : 0;   // chunks of this warp per tile
+    const int total = my_tiles * cpw;
+    auto fetch = [&](int it) {
+      if (it < total) {
+        const int ti = it / cpw, kc = (ws + (it - ti * cpw) * p.S) * kChunk + k0;   // first k of the chunk
+        const int n0 = (tile0 + grp + ti * groups) * 16;
+        const uint32_t dst = smem_u32(mine + (it % W::ring) * W::stage);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) t = fmaf(static_cast<float>(static_cast<int>((u >> (4 * e)) & 15u) - 8), f[e], t);
-    acc = fmaf(t, s, acc);
+        for (int i = 0; i < 4; ++i) {   // eight lanes: the 128 bytes of a row
+          const int row = i * 4 + (lane >> 3), k = kc + (lane & 7) * 32;
+          const bool ok = k < p.K;
+          cp_async16(dst + row * kRowPitch + (lane & 7) * 16,
+                     p.q4 + static_cast<long long>(min(n0 + row, p.N - 1)) * row_bytes + (ok ? k / 2 : 0), ok);
+        }
+        for (int i = lane; i < 16 * per_chunk; i += 32) {
+          const int row = i >> (8 - p.gshift), q = i - row * per_chunk, gi = (kc >> p.gshift) + q;
+          const bool ok = gi < row_scales;
+          cp_async4(dst + 16 * kRowPitch + (row * 8 + q) * 4,
+                    p.scales + static_cast<long long>(min(n0 + row, p.N - 1)) * row_scales + (ok ? gi : 0), ok);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i + 1 < W::ring; ++i) fetch(i);
+    // the slab's columns of A, in the products' order: x0 x4 x1 x5 x2 x6 x3 x7 of each eight
+    __syncthreads();   // (the previous slab's are no longer read)
+    for (int i = threadIdx.x; i < chunks * (kChunk / 32) * NT * 8 * 4; i += 32 * kWarps) {
+      const int tt = i & 3, q = (i >> 2) % (chunks * (kChunk / 32)), col = (i >> 2) / (chunks * (kChunk / 32));
+      const int m = col / kSplit, part = col - m * kSplit, k = q * 32 + tt * 8;
+      float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (m < p.M && k < ks) {
+        Vec8<T> v;
+        v.load(static_cast<const T*>(p.a) + static_cast<long long>(m) * p.K + k0 + k);
+        v.to_f32(f);
+      }
+      if (kSplit == 3) {   // the leading 8 bits, the next 8, the rest
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          for (int s = 0; s < part; ++s) f[e] -= __uint_as_float(__float_as_uint(f[e]) & 0xffff0000u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (part < 2) f[e] = __uint_as_float(__float_as_uint(f[e]) & 0xffff0000u);
+      }
+      sx[(q * NT * 8 + col) * 4 + tt] =
+          make_uint4(pack_bf16(f[0], f[4]), pack_bf16(f[1], f[5]), pack_bf16(f[2], f[6]), pack_bf16(f[3], f[7]));
+    }
+    __syncthreads();
+    int it = 0;
+    for (int ti = 0; ti < my_tiles; ++ti) {
+      float sum[NT][4], part[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[n][e] = part[n][e] = 0.f;
+      for (int c = 0; c < cpw; ++c, ++it) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(W::ring - 2) : "memory");
+        __syncwarp();   // every lane's pieces of this chunk are there, and the next slot is free
+        fetch(it + W::ring - 1);
+        const uint8_t* st = mine + (it % W::ring) * W::stage;
+        const uint32_t* codes = reinterpret_cast<const uint32_t*>(st);
+        const float* sc = reinterpret_cast<const float*>(st + 16 * kRowPitch);
+        const uint4* xk = sx + ((ws + c * p.S) * (kChunk / 32) * NT * 8 + g) * 4 + t;
+#pragma unroll
+        for (int q = 0; q < kChunk / 32; ++q) {
+          const uint32_t u0 = codes[g * (kRowPitch / 4) + q * 4 + t], u1 = codes[(g + 8) * (kRowPitch / 4) + q * 4 + t];
+          const uint32_t a0[4] = {q_pair(u0, 0), q_pair(u1, 0), q_pair(u0, 1), q_pair(u1, 1)};
+          const uint32_t a1[4] = {q_pair(u0, 2), q_pair(u1, 2), q_pair(u0, 3), q_pair(u1, 3)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint4 x = xk[(q * NT + n) * 32];
+            mma_bf16(part[n], a0, x.x, x.y);
+            mma_bf16(part[n], a1, x.z, x.w);
+          }
+          if ((((q + 1) * 32) & ((1 << p.gshift) - 1)) == 0) {   // the group is complete
+            const int gi = (q * 32) >> p.gshift;
+            const float s0 = sc[g * 8 + gi], s1 = sc[(g + 8) * 8 + gi];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                sum[n][e] = fmaf(part[n][e], e < 2 ? s0 : s1, sum[n][e]);
+                part[n][e] = 0.f;
+              }
+          }
+        }
+      }
+      // the warps of the tile
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<float2*>(&red[(warp * 16 + g + 8 * h) * 8 * NT + n * 8 + 2 * t]) =
+              make_float2(sum[n][2 * h], sum[n][2 * h + 1]);
+      meet();
+      const int tl = grp + ti * groups;   // tile of the CTA
+      const bool first = k0 == 0, last = k0 + p.slab >= p.K;
+      for (int i = threadIdx.x - grp * 32 * p.S; i < 16 * 8 * NT; i += 32 * p.S) {
+        float v = first ? 0.f : acc[tl * 16 * 8 * NT + i];
+        for (int w = 0; w < p.S; ++w) v += red[(grp * p.S + w) * 16 * 8 * NT + i];
+        if (!last || kSplit > 1) acc[tl * 16 * 8 * NT + i] = v;
+        const int n = (tile0 + tl) * 16 + i / (8 * NT), m = i % (8 * NT);
+        if (last && kSplit == 1 && n < p.N && m < p.M)
+          static_cast<T*>(p.c)[static_cast<long long>(m) * p.N + n] = from_f<T>(v);
+      }
+      meet();
+      if (last && kSplit > 1)
+        for (int i = threadIdx.x - grp * 32 * p.S; i < 16 * p.M; i += 32 * p.S) {
+          const int r = i / p.M, m = i - r * p.M, n = (tile0 + tl) * 16 + r;
+          const float* v = &acc[(tl * 16 + r) * 8 * NT + m * kSplit];
+          if (n < p.N) static_cast<T*>(p.c)[static_cast<long long>(m) * p.N + n] = from_f<T>((v[2] + v[1]) + v[0]);
+        }
+    }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-  if (lane == 0) c[static_cast<long long>(m) * N + n] = from_f<T>(acc);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <typename T, int NT>
+cudaError_t launch_gemm_w4_t(GemmW4Params p, cudaStream_t st) {
+  using W = W4Shape<NT>;
+  static_assert(W::smem <= 227 * 1024, "shared memory of one CTA");
+  static std::atomic<uint64_t> done{0};
+  if (cudaError_t e = smem_attr_once(gemm_w4_kernel<T, NT>, W::smem, done)) return e;
+  p.slab = W::slab;
+  const int chunks = ((p.K < p.slab ? p.K : p.slab) + kChunk - 1) / kChunk;
+  // as many warps to a tile as it has chunks: the finer the tiles are spread the evener the SMs
+  for (p.S = kWarps; p.S > chunks; p.S /= 2) {}
+  p.tiles = (p.N + 15) / 16;
+  int grid = (p.tiles + kTileRowsMax / 16 - 1) / (kTileRowsMax / 16);   // at least, for the sums in shared memory
+  const int per_cta = kWarps / p.S, want = (p.tiles + per_cta - 1) / per_cta;
+  if (grid < num_sms()) grid = want < num_sms() ? want : num_sms();
+  return launch(gemm_w4_kernel<T, NT>, dim3(grid), dim3(32 * kWarps), W::smem, st, p);
 }
 
 unsigned blocks_for(long long items, int per) { return static_cast<unsigned>((items + per - 1) / per); }
@@ -109,12 +296,13 @@ cudaError_t launch_dequantize_w4(const void* q4, const float* scales, void* w, i
 
 cudaError_t launch_gemm_w4(const void* a, const void* q4, const float* scales, void* c, int M, int N, int K, int group,
                            bool bf16, cudaStream_t st) {
-  const unsigned grid = blocks_for(static_cast<long long>(M) * N, 8);
-  return bf16 ? launch(gemm_w4_simple<__nv_bfloat16>, dim3(grid), dim3(256), 0, st,
-                       static_cast<const __nv_bfloat16*>(a), static_cast<const uint32_t*>(q4), scales,
-                       static_cast<__nv_bfloat16*>(c), M, N, K, group)
-              : launch(gemm_w4_simple<float>, dim3(grid), dim3(256), 0, st, static_cast<const float*>(a),
-                       static_cast<const uint32_t*>(q4), scales, static_cast<float*>(c), M, N, K, group);
+  GemmW4Params p{a, static_cast<const uint8_t*>(q4), scales, c, M, N, K, group == 32 ? 5 : group == 64 ? 6 : 7, 0, 0, 0};
+  if (bf16) return M <= 8 ? launch_gemm_w4_t<__nv_bfloat16, 1>(p, st) : launch_gemm_w4_t<__nv_bfloat16, 2>(p, st);
+  // three columns a row
+  if (M <= 2) return launch_gemm_w4_t<float, 1>(p, st);
+  if (M <= 5) return launch_gemm_w4_t<float, 2>(p, st);
+  if (M <= 8) return launch_gemm_w4_t<float, 3>(p, st);
+  return launch_gemm_w4_t<float, 6>(p, st);
 }
 
 }  // namespace hy
