@@ -40,7 +40,7 @@ hymba_status_t check_cache(const hymba_paged_kv_t* kv, hymba_dtype_t dtype) {
   // difference of two places in a sequence and a window
   if (static_cast<long long>(kv->n_pages) * ps > (1ll << 31) - 1 ||
       static_cast<long long>(kv->table_ld) * ps > (1ll << 30) ||
-      static_cast<long long>(kv->n_kv_heads) * kv->head_dim > (1 << 20))
+      static_cast<long long>(kv->n_kv_heads) * kv->head_dim > (1 << 16))
     return HYMBA_ERR_UNSUPPORTED;
   if (!aligned16(kv->pages) || (kv->cache_type == HYMBA_CACHE_E4M3 && !aligned16(kv->scales)))
     return HYMBA_ERR_UNSUPPORTED;

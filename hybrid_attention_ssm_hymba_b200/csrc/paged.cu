@@ -14,11 +14,35 @@ namespace {
 
 constexpr int kCopyThreads = 256;
 
+// n / d for n * d < 2^32 with d's multiplier ceil(2^32 / d) (0 for d = 1).
+HY_DEV int div_by(int n, uint32_t mul) { return mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(n), mul)) : n; }
+uint32_t multiplier(int d) { return d == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + d - 1) / d); }
+
+// The largest magnitude among a vector's eight elements, as the bits of an fp32 value: a NaN is
+// the largest of all.
+HY_DEV uint32_t most_bits(const Vec8<float>& v) {
+  const uint32_t u[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, u[i] & 0x7fffffffu);
+  return m;
+}
+HY_DEV uint32_t most_bits(const Vec8<__nv_bfloat16>& v) {   // two 16-bit maxima at a time
+  const uint32_t m = __vmaxu2(__vmaxu2(v.a.x & 0x7fff7fffu, v.a.y & 0x7fff7fffu), __vmaxu2(v.a.z & 0x7fff7fffu, v.a.w & 0x7fff7fffu));
+  return max(m << 16, m & 0xffff0000u);
+}
+HY_DEV uint32_t most_bits(const Vec8<__nv_fp8_e4m3>&) { return 0; }   // (never quantised)
+
 // WRITE: x (the batch's rows) -> cache; else cache -> x.  T: element type of x, C: of the cache.
+// Bound by HBM when there are many rows; then the instructions of the address arithmetic and the
+// conversions are what competes (a division per vector and a whole maximum per element: 41 us
+// for 4 x 8320 rows of 4 heads where the bytes take 16).
 template <typename T, typename C, bool WRITE, int ROWS>
 __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const PagedKv kv, const RaggedBatch rb, T* xk, T* xv,
-                                                                  long long ld, int lpu, unsigned* status) {
+                                                                  long long ld, int lpu, uint32_t row_mul,
+                                                                  unsigned* status) {
   constexpr bool kQuant = sizeof(C) == 1;
+  constexpr int kAhead = 4;   // vectors in flight before any is used
   __shared__ int s_page[ROWS], s_row[ROWS];
   pdl_trigger();
   pdl_wait();
@@ -43,61 +67,62 @@ __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const PagedKv 
   __syncthreads();
   const int e0 = (threadIdx.x & (lpu - 1)) * 8, per_row = 2 * kv.hkv;
   const int units = ROWS * per_row, step = kCopyThreads / lpu;
-  C* pages = static_cast<C*>(kv.pages);
-  for (int u0 = threadIdx.x / lpu; u0 < units; u0 += 4 * step) {
-    // four vectors in flight before any is used
-    Vec8<T> vx[4];
-    Vec8<C> vc[4];
-    float sc[4];
-    bool ok[4];
+  const long long v_off = static_cast<long long>(kv.n_pages) * kv.page_size * kv.hkv;   // rows x heads of one half
+  for (int u0 = threadIdx.x / lpu; u0 < units; u0 += kAhead * step) {
+    Vec8<T> vx[kAhead];
+    Vec8<C> vc[kAhead];
+    T* px[kAhead];
+    C* pc[kAhead];       // nullptr: nothing to do
+    float* ps[kAhead];
+    float sc[kAhead];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int u = u0 + k * step, i = u / per_row, w = (u - i * per_row) / kv.hkv, h = u - i * per_row - w * kv.hkv;
-      ok[k] = u < units && s_page[min(i, ROWS - 1)] >= 0 && e0 < kv.dh;
+    for (int k = 0; k < kAhead; ++k) {
+      const int u = u0 + k * step, i = min(div_by(u, row_mul), ROWS - 1), slot = u - i * per_row;
+      const int w = slot >= kv.hkv, h = slot - w * kv.hkv, page = s_page[i];
+      pc[k] = nullptr;
       sc[k] = 0.f;
-      if (!ok[k]) continue;
+      if (u >= units || page < 0 || e0 >= kv.dh) continue;
+      const long long at = static_cast<long long>(page) * kv.page_size + s_row[i];
+      pc[k] = static_cast<C*>(kv.pages) + ((at * kv.hkv + h) + (w ? v_off : 0)) * kv.dh + e0;
+      px[k] = (w ? xv : xk) + (r0 + i) * ld + h * kv.dh + e0;
+      if (kQuant) ps[k] = kv.scales + (static_cast<long long>(page) * kv.hkv + h) * kv.page_size + s_row[i] + (w ? v_off : 0);
       if (WRITE) {
-        vx[k].load((w ? xv : xk) + (r0 + i) * ld + h * kv.dh + e0);
+        vx[k].load(px[k]);
       } else {
-        vc[k].load(pages + page_elem(kv, w, s_page[i], s_row[i], h) + e0);
-        if (kQuant) sc[k] = kv.scales[page_scale(kv, w, s_page[i], s_row[i], h)];
+        vc[k].load(pc[k]);
+        if (kQuant) sc[k] = *ps[k];
       }
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int u = u0 + k * step, i = u / per_row, w = (u - i * per_row) / kv.hkv, h = u - i * per_row - w * kv.hkv;
-      float f[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = 0.f;
-      if (ok[k]) {
-        if (WRITE) vx[k].to_f32(f);
-        else vc[k].to_f32(f);
-      }
-      if (WRITE && kQuant) {
-        // the largest magnitude, as bits, so that a NaN is the largest of all
-        uint32_t mb = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) mb = max(mb, __float_as_uint(f[e]) & 0x7fffffffu);
+    for (int k = 0; k < kAhead; ++k) {
+      if (sizeof(T) == sizeof(C)) {   // as it is
+        if (!pc[k]) continue;
+        if (WRITE) *reinterpret_cast<Vec8<T>*>(&vc[k]) = vx[k];
+        else vx[k] = *reinterpret_cast<Vec8<T>*>(&vc[k]);
+      } else if (WRITE) {
+        uint32_t mb = pc[k] ? most_bits(vx[k]) : 0u;
         for (int o = lpu >> 1; o > 0; o >>= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+        if (!pc[k]) continue;
         // the floor keeps 1 / scale finite for rows of zeros and of subnormal values
         const float d = __fdiv_rn(__uint_as_float(mb), 448.f);
         sc[k] = d < 1.17549435e-38f ? 1.17549435e-38f : d;
         const float inv = __frcp_rn(sc[k]);
+        float f[8];
+        vx[k].to_f32(f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= inv;
-      } else if (kQuant) {
+        vc[k].from_f32(f);
+        if (e0 == 0) *ps[k] = sc[k];
+      } else {
+        if (!pc[k]) continue;
+        float f[8];
+        vc[k].to_f32(f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= sc[k];
-      }
-      if (!ok[k]) continue;
-      if (WRITE) {
-        vc[k].from_f32(f);
-        vc[k].store(pages + page_elem(kv, w, s_page[i], s_row[i], h) + e0);
-        if (kQuant && e0 == 0) kv.scales[page_scale(kv, w, s_page[i], s_row[i], h)] = sc[k];
-      } else {
         vx[k].from_f32(f);
-        vx[k].store((w ? xv : xk) + (r0 + i) * ld + h * kv.dh + e0);
       }
+      if (WRITE) vc[k].store(pc[k]);
+      else vx[k].store(px[k]);
     }
   }
 }
@@ -107,9 +132,13 @@ cudaError_t launch_copy_t(const PagedKv& kv, const RaggedBatch& rb, void* k, voi
                           cudaStream_t st) {
   int lpu = 2;
   while (lpu * 8 < kv.dh) lpu *= 2;
-  constexpr int kRows = 8;
-  return launch(paged_copy_kernel<T, C, WRITE, kRows>, dim3((rb.total_rows + kRows - 1) / kRows), dim3(kCopyThreads),
-                0, st, kv, rb, static_cast<T*>(k), static_cast<T*>(v), ld, lpu, status);
+  // many rows: enough vectors a thread that finding the rows' pages does not show; few: many CTAs
+  const uint32_t rm = multiplier(2 * kv.hkv);
+  const auto go = [&](auto kernel, int rows) {
+    return launch(kernel, dim3((rb.total_rows + rows - 1) / rows), dim3(kCopyThreads), 0, st, kv, rb, static_cast<T*>(k),
+                  static_cast<T*>(v), ld, lpu, rm, status);
+  };
+  return rb.total_rows >= 16 * 4 * num_sms() ? go(paged_copy_kernel<T, C, WRITE, 16>, 16) : go(paged_copy_kernel<T, C, WRITE, 4>, 4);
 }
 
 template <bool WRITE>

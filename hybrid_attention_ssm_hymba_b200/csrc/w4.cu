@@ -139,35 +139,43 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_co
   for (int k0 = 0; k0 < p.K; k0 += p.slab) {
     const int ks = min(p.slab, p.K - k0), chunks = (ks + kChunk - 1) / kChunk;
     const int cpw = ws < chunks ? (chunks - ws + p.S - 1) / p.S : 0;   // chunks of this warp per tile
-    const int total = my_tiles * cpw;
-    auto fetch = [&](int it) {
-      if (it < total) {
-        const int ti = it / cpw, kc = (ws + (it - ti * cpw) * p.S) * kChunk + k0;   // first k of the chunk
-        const int n0 = (tile0 + grp + ti * groups) * 16;
-        const uint32_t dst = smem_u32(mine + (it % W::ring) * W::stage);
+    // the next chunk to fetch: its tile (of this group), its number in the tile, its slot
+    int ft = 0, fc = 0, fs = 0;
+    auto fetch = [&]() {
+      if (ft < my_tiles && cpw > 0) {
+        const int kc = (ws + fc * p.S) * kChunk + k0, n0 = (tile0 + grp + ft * groups) * 16;
+        const uint32_t dst = smem_u32(mine + fs * W::stage);
+        const int k = kc + (lane & 7) * 32;
+        const bool ok = k < p.K;
+        const uint8_t* src = p.q4 + (ok ? k >> 1 : 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {   // eight lanes: the 128 bytes of a row
-          const int row = i * 4 + (lane >> 3), k = kc + (lane & 7) * 32;
-          const bool ok = k < p.K;
-          cp_async16(dst + row * kRowPitch + (lane & 7) * 16,
-                     p.q4 + static_cast<long long>(min(n0 + row, p.N - 1)) * row_bytes + (ok ? k / 2 : 0), ok);
+          const int row = i * 4 + (lane >> 3);
+          cp_async16(dst + row * kRowPitch + (lane & 7) * 16, src + min(n0 + row, p.N - 1) * row_bytes, ok);
         }
         for (int i = lane; i < 16 * per_chunk; i += 32) {
-          const int row = i >> (8 - p.gshift), q = i - row * per_chunk, gi = (kc >> p.gshift) + q;
-          const bool ok = gi < row_scales;
-          cp_async4(dst + 16 * kRowPitch + (row * 8 + q) * 4,
-                    p.scales + static_cast<long long>(min(n0 + row, p.N - 1)) * row_scales + (ok ? gi : 0), ok);
+          const int row = i >> (8 - p.gshift), q = i & (per_chunk - 1), gi = (kc >> p.gshift) + q;
+          const bool have = gi < row_scales;
+          cp_async4(dst + 16 * kRowPitch + (row * 8 + q) * 4, p.scales + min(n0 + row, p.N - 1) * row_scales + (have ? gi : 0),
+                    have);
         }
+        if (++fc == cpw) {
+          fc = 0;
+          ++ft;
+        }
+        fs = fs + 1 == W::ring ? 0 : fs + 1;
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int i = 0; i + 1 < W::ring; ++i) fetch(i);
+    for (int i = 0; i + 1 < W::ring; ++i) fetch();
     // the slab's columns of A, in the products' order: x0 x4 x1 x5 x2 x6 x3 x7 of each eight
     __syncthreads();   // (the previous slab's are no longer read)
-    for (int i = threadIdx.x; i < chunks * (kChunk / 32) * NT * 8 * 4; i += 32 * kWarps) {
-      const int tt = i & 3, q = (i >> 2) % (chunks * (kChunk / 32)), col = (i >> 2) / (chunks * (kChunk / 32));
-      const int m = col / kSplit, part = col - m * kSplit, k = q * 32 + tt * 8;
+    constexpr int kColWarps = NT * 8 >= kWarps ? 1 : 2;   // warps that share a column
+    for (int col = warp / kColWarps; col < NT * 8; col += kWarps / kColWarps) {
+      const int m = col / kSplit, part = col - m * kSplit;
+      for (int q8 = (warp % kColWarps) * 32 + lane; q8 < chunks * (kChunk / 8); q8 += 32 * kColWarps) {
+      const int q = q8 >> 2, tt = q8 & 3, k = q8 * 8;
       float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       if (m < p.M && k < ks) {
         Vec8<T> v;
@@ -184,20 +192,22 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_co
       }
       sx[(q * NT * 8 + col) * 4 + tt] =
           make_uint4(pack_bf16(f[0], f[4]), pack_bf16(f[1], f[5]), pack_bf16(f[2], f[6]), pack_bf16(f[3], f[7]));
+      }
     }
     __syncthreads();
-    int it = 0;
+    int slot = 0;
     for (int ti = 0; ti < my_tiles; ++ti) {
       float sum[NT][4], part[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[n][e] = part[n][e] = 0.f;
-      for (int c = 0; c < cpw; ++c, ++it) {
+      for (int c = 0; c < cpw; ++c) {
         asm volatile("cp.async.wait_group %0;" ::"n"(W::ring - 2) : "memory");
         __syncwarp();   // every lane's pieces of this chunk are there, and the next slot is free
-        fetch(it + W::ring - 1);
-        const uint8_t* st = mine + (it % W::ring) * W::stage;
+        fetch();
+        const uint8_t* st = mine + slot * W::stage;
+        slot = slot + 1 == W::ring ? 0 : slot + 1;
         const uint32_t* codes = reinterpret_cast<const uint32_t*>(st);
         const float* sc = reinterpret_cast<const float*>(st + 16 * kRowPitch);
         const uint4* xk = sx + ((ws + c * p.S) * (kChunk / 32) * NT * 8 + g) * 4 + t;
@@ -263,12 +273,23 @@ cudaError_t launch_gemm_w4_t(GemmW4Params p, cudaStream_t st) {
   if (cudaError_t e = smem_attr_once(gemm_w4_kernel<T, NT>, W::smem, done)) return e;
   p.slab = W::slab;
   const int chunks = ((p.K < p.slab ? p.K : p.slab) + kChunk - 1) / kChunk;
-  // as many warps to a tile as it has chunks: the finer the tiles are spread the evener the SMs
-  for (p.S = kWarps; p.S > chunks; p.S /= 2) {}
   p.tiles = (p.N + 15) / 16;
-  int grid = (p.tiles + kTileRowsMax / 16 - 1) / (kTileRowsMax / 16);   // at least, for the sums in shared memory
-  const int per_cta = kWarps / p.S, want = (p.tiles + per_cta - 1) / per_cta;
-  if (grid < num_sms()) grid = want < num_sms() ? want : num_sms();
+  const int sms = num_sms(), least = (p.tiles + kTileRowsMax / 16 - 1) / (kTileRowsMax / 16);   // CTAs: the sums' room
+  // S: a warp's chunks of a tile and, as one more, the meeting of a tile's warps, times the tiles
+  // one after another (16384 x 8192: S = 2, one round of 8 chunks a slab, against S = 16, seven
+  // rounds of one: 24 us to 42)
+  int best = 1 << 30, grid = 1;
+  for (int S = 1; S <= kWarps && S <= chunks; S *= 2) {
+    const int per_cta = kWarps / S, want = (p.tiles + per_cta - 1) / per_cta;
+    const int ctas = least > sms ? least : (want < sms ? (want > least ? want : least) : sms);
+    const int rounds = ((p.tiles + ctas - 1) / ctas + per_cta - 1) / per_cta;
+    const int cost = rounds * ((chunks + S - 1) / S + 1);
+    if (cost < best) {
+      best = cost;
+      p.S = S;
+      grid = ctas;
+    }
+  }
   return launch(gemm_w4_kernel<T, NT>, dim3(grid), dim3(32 * kWarps), W::smem, st, p);
 }
 
