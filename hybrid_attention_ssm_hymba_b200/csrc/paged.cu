@@ -14,10 +14,6 @@ namespace {
 
 constexpr int kCopyThreads = 256;
 
-// n / d for n * d < 2^32 with d's multiplier ceil(2^32 / d) (0 for d = 1).
-HY_DEV int div_by(int n, uint32_t mul) { return mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(n), mul)) : n; }
-uint32_t multiplier(int d) { return d == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + d - 1) / d); }
-
 // The largest magnitude among a vector's eight elements, as the bits of an fp32 value: a NaN is
 // the largest of all.
 HY_DEV uint32_t most_bits(const Vec8<float>& v) {
@@ -33,17 +29,29 @@ HY_DEV uint32_t most_bits(const Vec8<__nv_bfloat16>& v) {   // two 16-bit maxima
 }
 HY_DEV uint32_t most_bits(const Vec8<__nv_fp8_e4m3>&) { return 0; }   // (never quantised)
 
+// m / 448 rounded to nearest: a quotient within an ulp, corrected once by its exact remainder
+// (Markstein's theorem on correctly rounded division; a subnormal quotient is replaced by the
+// caller's floor, and the remainder of an infinity or NaN gives NaN).
+HY_DEV float div448(float m) {
+  constexpr float y = 1.f / 448.f;
+  const float q = m * y;
+  return fmaf(fmaf(-q, 448.f, m), y, q);
+}
+
+// Quantising spends most on what a lane does once per vector (its part of the maximum, the
+// scale, the addresses), so a lane then holds 16 elements instead of 8.
+template <typename C, bool WRITE> HY_DEV constexpr int lane_vectors() { return WRITE && sizeof(C) == 1 ? 2 : 1; }
+
 // WRITE: x (the batch's rows) -> cache; else cache -> x.  T: element type of x, C: of the cache.
-// Bound by HBM when there are many rows; then the instructions of the address arithmetic and the
-// conversions are what competes (a division per vector and a whole maximum per element: 41 us
-// for 4 x 8320 rows of 4 heads where the bytes take 16).
+// Bound by HBM when there are many rows; what competes are the instructions around each vector,
+// so a thread keeps its place in a row (K or V, head, elements) and walks the rows.
 template <typename T, typename C, bool WRITE, int ROWS>
 __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const PagedKv kv, const RaggedBatch rb, T* xk, T* xv,
-                                                                  long long ld, int lpu, uint32_t row_mul,
-                                                                  unsigned* status) {
+                                                                  long long ld, int lpu, unsigned* status) {
   constexpr bool kQuant = sizeof(C) == 1;
-  constexpr int kAhead = 4;   // vectors in flight before any is used
-  __shared__ int s_page[ROWS], s_row[ROWS];
+  constexpr int kVec = lane_vectors<C, WRITE>();   // eights of elements a lane holds
+  constexpr int kAhead = 4 / kVec;                 // vectors in flight before any is used
+  __shared__ long long s_elem[ROWS], s_scale[ROWS];   // the row's place in the pool (-1: none) and among the scales
   pdl_trigger();
   pdl_wait();
   const int r0 = blockIdx.x * ROWS;
@@ -61,68 +69,79 @@ __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const PagedKv 
         if (page < 0) report_invalid(status);
       }
     }
-    s_page[i] = page;
-    s_row[i] = row;
+    s_elem[i] = page < 0 ? -1 : (static_cast<long long>(page) * kv.page_size + row) * kv.hkv * kv.dh;
+    s_scale[i] = static_cast<long long>(page) * kv.hkv * kv.page_size + row;
   }
   __syncthreads();
-  const int e0 = (threadIdx.x & (lpu - 1)) * 8, per_row = 2 * kv.hkv;
-  const int units = ROWS * per_row, step = kCopyThreads / lpu;
-  const long long v_off = static_cast<long long>(kv.n_pages) * kv.page_size * kv.hkv;   // rows x heads of one half
-  for (int u0 = threadIdx.x / lpu; u0 < units; u0 += kAhead * step) {
-    Vec8<T> vx[kAhead];
-    Vec8<C> vc[kAhead];
-    T* px[kAhead];
-    C* pc[kAhead];       // nullptr: nothing to do
-    float* ps[kAhead];
-    float sc[kAhead];
+  // lpu lanes hold a vector; with fewer (K or V, head) places than groups
+  // of lanes the groups share the rows
+  const int grp = threadIdx.x / lpu, groups = kCopyThreads / lpu, places = 2 * kv.hkv;
+  const int e0 = (threadIdx.x & (lpu - 1)) * 8 * kVec, share = places < groups ? groups / places : 1;
+  const int first = places < groups ? grp / places : 0;
+  const unsigned mask = (lpu == 32 ? 0xffffffffu : ((1u << lpu) - 1u) << ((threadIdx.x & 31) & ~(lpu - 1)));
+  const long long half = static_cast<long long>(kv.n_pages) * kv.page_size * kv.hkv;   // rows x heads of K
+  if (first >= share) return;
+  for (int place = grp - first * places; place < places; place += groups) {
+    const int w = place >= kv.hkv, h = place - w * kv.hkv;
+    C* cache = static_cast<C*>(kv.pages) + (w ? half : 0) * kv.dh + h * kv.dh + e0;
+    T* x = (w ? xv : xk) + r0 * ld + h * kv.dh + e0;
+    float* scales = kQuant ? kv.scales + (w ? half : 0) + static_cast<long long>(h) * kv.page_size : nullptr;
+    for (int i0 = first; i0 < ROWS; i0 += kAhead * share) {
+      Vec8<T> vx[kAhead][kVec];
+      Vec8<C> vc[kAhead][kVec];
+      float sc[kAhead];
+      long long at[kAhead];   // the row's place in the pool, -1: nothing to do
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int u = u0 + k * step, i = min(div_by(u, row_mul), ROWS - 1), slot = u - i * per_row;
-      const int w = slot >= kv.hkv, h = slot - w * kv.hkv, page = s_page[i];
-      pc[k] = nullptr;
-      sc[k] = 0.f;
-      if (u >= units || page < 0 || e0 >= kv.dh) continue;
-      const long long at = static_cast<long long>(page) * kv.page_size + s_row[i];
-      pc[k] = static_cast<C*>(kv.pages) + ((at * kv.hkv + h) + (w ? v_off : 0)) * kv.dh + e0;
-      px[k] = (w ? xv : xk) + (r0 + i) * ld + h * kv.dh + e0;
-      if (kQuant) ps[k] = kv.scales + (static_cast<long long>(page) * kv.hkv + h) * kv.page_size + s_row[i] + (w ? v_off : 0);
-      if (WRITE) {
-        vx[k].load(px[k]);
-      } else {
-        vc[k].load(pc[k]);
-        if (kQuant) sc[k] = *ps[k];
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = i0 + k * share;
+        at[k] = i < ROWS && e0 < kv.dh ? s_elem[i] : -1;
+        sc[k] = 0.f;
+        if (at[k] < 0) continue;
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+          if (WRITE) vx[k][v].load(x + i * ld + 8 * v);
+          else vc[k][v].load(cache + at[k] + 8 * v);
+        }
+        if (!WRITE && kQuant) sc[k] = scales[s_scale[i]];
       }
-    }
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (sizeof(T) == sizeof(C)) {   // as it is
-        if (!pc[k]) continue;
-        if (WRITE) *reinterpret_cast<Vec8<T>*>(&vc[k]) = vx[k];
-        else vx[k] = *reinterpret_cast<Vec8<T>*>(&vc[k]);
-      } else if (WRITE) {
-        uint32_t mb = pc[k] ? most_bits(vx[k]) : 0u;
-        for (int o = lpu >> 1; o > 0; o >>= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-        if (!pc[k]) continue;
-        // the floor keeps 1 / scale finite for rows of zeros and of subnormal values
-        const float d = __fdiv_rn(__uint_as_float(mb), 448.f);
-        sc[k] = d < 1.17549435e-38f ? 1.17549435e-38f : d;
-        const float inv = __frcp_rn(sc[k]);
-        float f[8];
-        vx[k].to_f32(f);
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = i0 + k * share;
+        float inv = 0.f, s = 0.f;
+        if (WRITE && kQuant) {
+          uint32_t mb = 0;
+          if (at[k] >= 0) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= inv;
-        vc[k].from_f32(f);
-        if (e0 == 0) *ps[k] = sc[k];
-      } else {
-        if (!pc[k]) continue;
-        float f[8];
-        vc[k].to_f32(f);
+            for (int v = 0; v < kVec; ++v) mb = max(mb, most_bits(vx[k][v]));
+          }
+          for (int o = lpu >> 1; o > 0; o >>= 1) mb = max(mb, __shfl_xor_sync(mask, mb, o));
+          // the floor keeps 1 / scale finite for rows of zeros and of subnormal values
+          const float d = div448(__uint_as_float(mb));
+          s = d < 1.17549435e-38f ? 1.17549435e-38f : d;
+          inv = __frcp_rn(s);
+        }
+        if (at[k] < 0) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= sc[k];
-        vx[k].from_f32(f);
+        for (int v = 0; v < kVec; ++v) {
+          if constexpr (sizeof(T) == sizeof(C)) {   // as it is
+            if (WRITE) vx[k][v].store(reinterpret_cast<T*>(cache + at[k] + 8 * v));
+            else vc[k][v].store(reinterpret_cast<C*>(x + i * ld + 8 * v));
+          } else {
+            float f[8];
+            if (WRITE) vx[k][v].to_f32(f);
+            else vc[k][v].to_f32(f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] *= WRITE ? inv : sc[k];
+            if (WRITE) vc[k][v].from_f32(f);
+            else vx[k][v].from_f32(f);
+            if (!WRITE) vx[k][v].store(x + i * ld + 8 * v);
+          }
+        }
+        if constexpr (WRITE && kQuant) {
+          *reinterpret_cast<uint4*>(cache + at[k]) = make_uint4(vc[k][0].a.x, vc[k][0].a.y, vc[k][kVec - 1].a.x, vc[k][kVec - 1].a.y);
+          if (e0 == 0) scales[s_scale[i]] = s;
+        }
       }
-      if (WRITE) vc[k].store(pc[k]);
-      else vx[k].store(px[k]);
     }
   }
 }
@@ -130,15 +149,15 @@ __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const PagedKv 
 template <typename T, typename C, bool WRITE>
 cudaError_t launch_copy_t(const PagedKv& kv, const RaggedBatch& rb, void* k, void* v, long long ld, unsigned* status,
                           cudaStream_t st) {
-  int lpu = 2;
-  while (lpu * 8 < kv.dh) lpu *= 2;
+  const int per_lane = WRITE && sizeof(C) == 1 ? 16 : 8;
+  int lpu = 1;
+  while (lpu * per_lane < kv.dh) lpu *= 2;
   // many rows: enough vectors a thread that finding the rows' pages does not show; few: many CTAs
-  const uint32_t rm = multiplier(2 * kv.hkv);
   const auto go = [&](auto kernel, int rows) {
     return launch(kernel, dim3((rb.total_rows + rows - 1) / rows), dim3(kCopyThreads), 0, st, kv, rb, static_cast<T*>(k),
-                  static_cast<T*>(v), ld, lpu, rm, status);
+                  static_cast<T*>(v), ld, lpu, status);
   };
-  return rb.total_rows >= 16 * 4 * num_sms() ? go(paged_copy_kernel<T, C, WRITE, 16>, 16) : go(paged_copy_kernel<T, C, WRITE, 4>, 4);
+  return rb.total_rows >= 16 * 4 * num_sms() ? go(paged_copy_kernel<T, C, WRITE, 32>, 32) : go(paged_copy_kernel<T, C, WRITE, 4>, 4);
 }
 
 template <bool WRITE>

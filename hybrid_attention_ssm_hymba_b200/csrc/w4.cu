@@ -5,56 +5,94 @@
 namespace hy {
 namespace {
 
-// Eight weights per lane; the group / 8 lanes of a group share its maximum by shuffles.
+// Eight weights per lane and four such vectors in flight; the group / 8 lanes of a group share
+// its maximum by shuffles.  HBM bound: 2 or 4 bytes in and half a byte out per weight.
+constexpr int kQuantAhead = 4;
+
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_w4_kernel(const T* __restrict__ w, uint32_t* __restrict__ q4,
-                                                          float* __restrict__ scales, long long n8, int group) {
+                                                          float* __restrict__ scales, long long n8, int lshift) {
   pdl_trigger();
   pdl_wait();
-  const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int lpg = group / 8;
-  float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (i < n8) {
-    Vec8<T> v;
-    v.load(w + i * 8);
-    v.to_f32(f);
-  }
-  float m = 0.f;
+  const long long i0 = static_cast<long long>(blockIdx.x) * (256 * kQuantAhead) + threadIdx.x;
+  Vec8<T> v[kQuantAhead];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
-  for (int o = lpg >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (i >= n8) return;
-  const float most = fmaxf(m, 1.17549435e-38f), r = __fdiv_rn(7.f, most);
-  uint32_t u = 0;
+  for (int k = 0; k < kQuantAhead; ++k)
+    if (i0 + k * 256 < n8) v[k].load(w + (i0 + k * 256) * 8);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    // t is within 7 * 2^-22 of 7 w / most: only next to a half does the exact quotient decide
-    // (and where 7 / most overflows, which leaves t - c no number)
-    const float t = f[e] * r;
-    float c = rintf(t);
-    if (!(fabsf(t - c) <= 0.49999f)) c = static_cast<float>(rint(7.0 * f[e] / static_cast<double>(most)));
-    u |= static_cast<uint32_t>(static_cast<int>(c) + 8) << (4 * e);
+  for (int k = 0; k < kQuantAhead; ++k) {
+    const long long i = i0 + k * 256;
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (i < n8) v[k].to_f32(f);
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+    for (int o = 1 << (lshift - 1); o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (i >= n8) continue;
+    const float most = fmaxf(m, 1.17549435e-38f), r = __fdiv_rn(7.f, most);
+    // t is within 7 * 2^-22 of 7 w / most, and adding 1.5 * 2^23 rounds it to the nearest integer
+    // in the sum's low bits; only next to a half does the exact quotient decide (and where
+    // 7 / most overflows, which leaves t - c no number)
+    uint32_t u = 0;
+    bool near = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float t = f[e] * r, s = t + 12582912.f;
+      near |= !(fabsf(t - (s - 12582912.f)) <= 0.49999f);
+      u |= ((__float_as_uint(s) + 8u) & 15u) << (4 * e);
+    }
+    if (near) {   // often for bf16 weights, whose quotients are halves more than by chance
+      u = 0;
+      if (sizeof(T) == 2 && most > 1e-30f) {
+        // 7 w, c most and their difference have few bits: all exact in fp32
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float s = f[e] * r + 12582912.f, c = s - 12582912.f, d = fmaf(-c, most, 7.f * f[e]);
+          const int odd = __float_as_int(s) & 1, up = d > 0.f ? 1 : -1, k = static_cast<int>(__float_as_uint(s)) + 8;
+          const float over = fabsf(d) + fabsf(d) - most;   // beyond a half, or at one with c odd: the neighbour
+          u |= ((over > 0.f || (over == 0.f && odd) ? k + up : k) & 15u) << (4 * e);
+        }
+      } else {
+#pragma unroll 1
+        for (int e = 0; e < 8; ++e) {
+          u = (u >> 4) | static_cast<uint32_t>(static_cast<int>(rint(7.0 * f[0] / static_cast<double>(most))) + 8) << 28;
+#pragma unroll
+          for (int x = 0; x < 7; ++x) f[x] = f[x + 1];
+        }
+      }
+    }
+    q4[i] = u;
+    if ((i & ((1 << lshift) - 1)) == 0) scales[i >> lshift] = fmaxf(__fdiv_rn(m, 7.f), 1.17549435e-38f);
   }
-  q4[i] = u;
-  if ((i % lpg) == 0) scales[i / lpg] = fmaxf(__fdiv_rn(m, 7.f), 1.17549435e-38f);
 }
 
 template <typename T>
 __global__ void __launch_bounds__(256) dequantize_w4_kernel(const uint32_t* __restrict__ q4,
                                                             const float* __restrict__ scales, T* __restrict__ w,
-                                                            long long n8, int group) {
+                                                            long long n8, int lshift) {
   pdl_trigger();
   pdl_wait();
-  const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= n8) return;
-  const uint32_t u = q4[i];
-  const float s = scales[i / (group / 8)];
-  float f[8];
+  const long long i0 = static_cast<long long>(blockIdx.x) * (256 * kQuantAhead) + threadIdx.x;
+  uint32_t u[kQuantAhead];
+  float s[kQuantAhead];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = static_cast<float>(static_cast<int>((u >> (4 * e)) & 15u) - 8) * s;
-  Vec8<T> v;
-  v.from_f32(f);
-  v.store(w + i * 8);
+  for (int k = 0; k < kQuantAhead; ++k)
+    if (i0 + k * 256 < n8) {
+      u[k] = q4[i0 + k * 256];
+      s[k] = scales[(i0 + k * 256) >> lshift];
+    }
+#pragma unroll
+  for (int k = 0; k < kQuantAhead; ++k) {
+    const long long i = i0 + k * 256;
+    if (i >= n8) continue;
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)   // 2^23 + code, less 2^23 + 8
+      f[e] = (__uint_as_float(0x4b000000u | ((u[k] >> (4 * e)) & 15u)) - 8388616.f) * s[k];
+    Vec8<T> v;
+    v.from_f32(f);
+    v.store(w + i * 8);
+  }
 }
 
 // C = A W^T for a few rows of A on mma.sync m16n8k16: W's rows are the products' 16 rows, A's
@@ -300,19 +338,23 @@ unsigned blocks_for(long long items, int per) { return static_cast<unsigned>((it
 cudaError_t launch_quantize_w4(const void* w, void* q4, float* scales, int N, int K, int group, bool bf16,
                                cudaStream_t st) {
   const long long n8 = static_cast<long long>(N) * K / 8;
-  return bf16 ? launch(quantize_w4_kernel<__nv_bfloat16>, dim3(blocks_for(n8, 256)), dim3(256), 0, st,
-                       static_cast<const __nv_bfloat16*>(w), static_cast<uint32_t*>(q4), scales, n8, group)
-              : launch(quantize_w4_kernel<float>, dim3(blocks_for(n8, 256)), dim3(256), 0, st,
-                       static_cast<const float*>(w), static_cast<uint32_t*>(q4), scales, n8, group);
+  const dim3 grid(blocks_for(n8, 256 * kQuantAhead));
+  const int ls = group == 32 ? 2 : group == 64 ? 3 : 4;   // log2 of a group's lanes
+  return bf16 ? launch(quantize_w4_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, static_cast<const __nv_bfloat16*>(w),
+                       static_cast<uint32_t*>(q4), scales, n8, ls)
+              : launch(quantize_w4_kernel<float>, grid, dim3(256), 0, st, static_cast<const float*>(w),
+                       static_cast<uint32_t*>(q4), scales, n8, ls);
 }
 
 cudaError_t launch_dequantize_w4(const void* q4, const float* scales, void* w, int N, int K, int group, bool bf16,
                                  cudaStream_t st) {
   const long long n8 = static_cast<long long>(N) * K / 8;
-  return bf16 ? launch(dequantize_w4_kernel<__nv_bfloat16>, dim3(blocks_for(n8, 256)), dim3(256), 0, st,
-                       static_cast<const uint32_t*>(q4), scales, static_cast<__nv_bfloat16*>(w), n8, group)
-              : launch(dequantize_w4_kernel<float>, dim3(blocks_for(n8, 256)), dim3(256), 0, st,
-                       static_cast<const uint32_t*>(q4), scales, static_cast<float*>(w), n8, group);
+  const dim3 grid(blocks_for(n8, 256 * kQuantAhead));
+  const int ls = group == 32 ? 2 : group == 64 ? 3 : 4;
+  return bf16 ? launch(dequantize_w4_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, static_cast<const uint32_t*>(q4),
+                       scales, static_cast<__nv_bfloat16*>(w), n8, ls)
+              : launch(dequantize_w4_kernel<float>, grid, dim3(256), 0, st, static_cast<const uint32_t*>(q4), scales,
+                       static_cast<float*>(w), n8, ls);
 }
 
 cudaError_t launch_gemm_w4(const void* a, const void* q4, const float* scales, void* c, int M, int N, int K, int group,
