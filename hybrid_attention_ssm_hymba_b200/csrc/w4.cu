@@ -5,22 +5,23 @@
 namespace hy {
 namespace {
 
-// Eight weights per lane and four such vectors in flight; the group / 8 lanes of a group share
+// Eight weights per lane and two (fp32) or four (bf16) such vectors in flight; the group / 8 lanes of a group share
 // its maximum by shuffles.  HBM bound: 2 or 4 bytes in and half a byte out per weight.
-constexpr int kQuantAhead = 4;
+template <typename T> constexpr int kQuantAhead = sizeof(T) == 4 ? 2 : 4;
 
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_w4_kernel(const T* __restrict__ w, uint32_t* __restrict__ q4,
                                                           float* __restrict__ scales, long long n8, int lshift) {
   pdl_trigger();
   pdl_wait();
-  const long long i0 = static_cast<long long>(blockIdx.x) * (256 * kQuantAhead) + threadIdx.x;
-  Vec8<T> v[kQuantAhead];
+  constexpr int kAhead = kQuantAhead<T>;
+  const long long i0 = static_cast<long long>(blockIdx.x) * (256 * kAhead) + threadIdx.x;
+  Vec8<T> v[kAhead];
 #pragma unroll
-  for (int k = 0; k < kQuantAhead; ++k)
+  for (int k = 0; k < kAhead; ++k)
     if (i0 + k * 256 < n8) v[k].load(w + (i0 + k * 256) * 8);
 #pragma unroll
-  for (int k = 0; k < kQuantAhead; ++k) {
+  for (int k = 0; k < kAhead; ++k) {
     const long long i = i0 + k * 256;
     float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (i < n8) v[k].to_f32(f);
@@ -29,36 +30,26 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const T* __restrict__ 
     for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
     for (int o = 1 << (lshift - 1); o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (i >= n8) continue;
-    const float most = fmaxf(m, 1.17549435e-38f), r = __fdiv_rn(7.f, most);
-    // t is within 7 * 2^-22 of 7 w / most, and adding 1.5 * 2^23 rounds it to the nearest integer
-    // in the sum's low bits; only next to a half does the exact quotient decide (and where
-    // 7 / most overflows, which leaves t - c no number)
+    const float most = fmaxf(m, 1.17549435e-38f), y = __frcp_rn(most);
+    // the quotient 7 w / most, within an ulp and then corrected by its remainder (Markstein's
+    // theorem: rounded to nearest, so a half that is exact stays one), and 1.5 * 2^23 added, which
+    // rounds it to the nearest even integer in the sum's low bits.  bf16: 7 w is exact.  fp32: it
+    // is not, and next to a half 64 bits decide, as where the remainder is subnormal.
     uint32_t u = 0;
-    bool near = false;
+    bool near = most < 1e-30f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float t = f[e] * r, s = t + 12582912.f;
-      near |= !(fabsf(t - (s - 12582912.f)) <= 0.49999f);
+      const float w7 = 7.f * f[e], t0 = w7 * y, t = fmaf(fmaf(-t0, most, w7), y, t0), s = t + 12582912.f;
+      if (sizeof(T) == 4) near |= !(fabsf(t - (s - 12582912.f)) <= 0.49999f);
       u |= ((__float_as_uint(s) + 8u) & 15u) << (4 * e);
     }
-    if (near) {   // often for bf16 weights, whose quotients are halves more than by chance
+    if (near) {
       u = 0;
-      if (sizeof(T) == 2 && most > 1e-30f) {
-        // 7 w, c most and their difference have few bits: all exact in fp32
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float s = f[e] * r + 12582912.f, c = s - 12582912.f, d = fmaf(-c, most, 7.f * f[e]);
-          const int odd = __float_as_int(s) & 1, up = d > 0.f ? 1 : -1, k = static_cast<int>(__float_as_uint(s)) + 8;
-          const float over = fabsf(d) + fabsf(d) - most;   // beyond a half, or at one with c odd: the neighbour
-          u |= ((over > 0.f || (over == 0.f && odd) ? k + up : k) & 15u) << (4 * e);
-        }
-      } else {
 #pragma unroll 1
-        for (int e = 0; e < 8; ++e) {
-          u = (u >> 4) | static_cast<uint32_t>(static_cast<int>(rint(7.0 * f[0] / static_cast<double>(most))) + 8) << 28;
+      for (int e = 0; e < 8; ++e) {
+        u = (u >> 4) | static_cast<uint32_t>(static_cast<int>(rint(7.0 * f[0] / static_cast<double>(most))) + 8) << 28;
 #pragma unroll
-          for (int x = 0; x < 7; ++x) f[x] = f[x + 1];
-        }
+        for (int x = 0; x < 7; ++x) f[x] = f[x + 1];
       }
     }
     q4[i] = u;
@@ -72,17 +63,18 @@ __global__ void __launch_bounds__(256) dequantize_w4_kernel(const uint32_t* __re
                                                             long long n8, int lshift) {
   pdl_trigger();
   pdl_wait();
-  const long long i0 = static_cast<long long>(blockIdx.x) * (256 * kQuantAhead) + threadIdx.x;
-  uint32_t u[kQuantAhead];
-  float s[kQuantAhead];
+  constexpr int kAhead = kQuantAhead<T>;
+  const long long i0 = static_cast<long long>(blockIdx.x) * (256 * kAhead) + threadIdx.x;
+  uint32_t u[kAhead];
+  float s[kAhead];
 #pragma unroll
-  for (int k = 0; k < kQuantAhead; ++k)
+  for (int k = 0; k < kAhead; ++k)
     if (i0 + k * 256 < n8) {
       u[k] = q4[i0 + k * 256];
       s[k] = scales[(i0 + k * 256) >> lshift];
     }
 #pragma unroll
-  for (int k = 0; k < kQuantAhead; ++k) {
+  for (int k = 0; k < kAhead; ++k) {
     const long long i = i0 + k * 256;
     if (i >= n8) continue;
     float f[8];
@@ -171,7 +163,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_co
     if (p.S == 1) __syncwarp();
     else bar_sync_n(1 + grp, 32 * p.S);
   };
-  uint8_t* mine = ring + warp * W::ring * W::stage;
+  const uint32_t my_ring = smem_u32(ring + warp * W::ring * W::stage);
+  // bit q: a group ends with the chunk's q-th 32 k
+  const unsigned ends = p.gshift == 5 ? 0xffu : p.gshift == 6 ? 0xaau : 0x88u;
   pdl_trigger();
   pdl_wait();
   for (int k0 = 0; k0 < p.K; k0 += p.slab) {
@@ -182,20 +176,26 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_co
     auto fetch = [&]() {
       if (ft < my_tiles && cpw > 0) {
         const int kc = (ws + fc * p.S) * kChunk + k0, n0 = (tile0 + grp + ft * groups) * 16;
-        const uint32_t dst = smem_u32(mine + fs * W::stage);
+        const uint32_t dst = my_ring + fs * W::stage, dq = dst + (lane >> 3) * kRowPitch + (lane & 7) * 16;
         const int k = kc + (lane & 7) * 32;
-        const bool ok = k < p.K;
-        const uint8_t* src = p.q4 + (ok ? k >> 1 : 0);
+        if (n0 + 16 <= p.N && kc + kChunk <= p.K) {   // eight lanes: the 128 bytes of a row
+          const uint8_t* src = p.q4 + (n0 + (lane >> 3)) * row_bytes + (k >> 1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {   // eight lanes: the 128 bytes of a row
-          const int row = i * 4 + (lane >> 3);
-          cp_async16(dst + row * kRowPitch + (lane & 7) * 16, src + min(n0 + row, p.N - 1) * row_bytes, ok);
-        }
-        for (int i = lane; i < 16 * per_chunk; i += 32) {
-          const int row = i >> (8 - p.gshift), q = i & (per_chunk - 1), gi = (kc >> p.gshift) + q;
-          const bool have = gi < row_scales;
-          cp_async4(dst + 16 * kRowPitch + (row * 8 + q) * 4, p.scales + min(n0 + row, p.N - 1) * row_scales + (have ? gi : 0),
-                    have);
+          for (int i = 0; i < 4; ++i) cp_async16(dq + i * 4 * kRowPitch, src + i * 4 * row_bytes, true);
+          for (int i = lane; i < 16 * per_chunk; i += 32)
+            cp_async4(dst + 16 * kRowPitch + ((i >> (8 - p.gshift)) * 8 + (i & (per_chunk - 1))) * 4,
+                      p.scales + (n0 + (i >> (8 - p.gshift))) * row_scales + (kc >> p.gshift) + (i & (per_chunk - 1)), true);
+        } else {   // rows behind the last read it again, k behind the last count as zeros
+          const bool ok = k < p.K;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            cp_async16(dq + i * 4 * kRowPitch, p.q4 + min(n0 + i * 4 + (lane >> 3), p.N - 1) * row_bytes + (ok ? k >> 1 : 0), ok);
+          for (int i = lane; i < 16 * per_chunk; i += 32) {
+            const int row = i >> (8 - p.gshift), q = i & (per_chunk - 1), gi = (kc >> p.gshift) + q;
+            const bool have = gi < row_scales;
+            cp_async4(dst + 16 * kRowPitch + (row * 8 + q) * 4, p.scales + min(n0 + row, p.N - 1) * row_scales + (have ? gi : 0),
+                      have);
+          }
         }
         if (++fc == cpw) {
           fc = 0;
@@ -244,25 +244,24 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_co
         asm volatile("cp.async.wait_group %0;" ::"n"(W::ring - 2) : "memory");
         __syncwarp();   // every lane's pieces of this chunk are there, and the next slot is free
         fetch();
-        const uint8_t* st = mine + slot * W::stage;
+        const uint32_t st = my_ring + slot * W::stage, codes = st + g * kRowPitch + t * 4;
+        uint32_t sc = st + 16 * kRowPitch + g * 32;
         slot = slot + 1 == W::ring ? 0 : slot + 1;
-        const uint32_t* codes = reinterpret_cast<const uint32_t*>(st);
-        const float* sc = reinterpret_cast<const float*>(st + 16 * kRowPitch);
-        const uint4* xk = sx + ((ws + c * p.S) * (kChunk / 32) * NT * 8 + g) * 4 + t;
+        const uint32_t xk = smem_u32(sx) + (((ws + c * p.S) * (kChunk / 32) * NT * 8 + g) * 4 + t) * 16;
 #pragma unroll
         for (int q = 0; q < kChunk / 32; ++q) {
-          const uint32_t u0 = codes[g * (kRowPitch / 4) + q * 4 + t], u1 = codes[(g + 8) * (kRowPitch / 4) + q * 4 + t];
+          const uint32_t u0 = lds_u32(codes + q * 16), u1 = lds_u32(codes + 8 * kRowPitch + q * 16);
           const uint32_t a0[4] = {q_pair(u0, 0), q_pair(u1, 0), q_pair(u0, 1), q_pair(u1, 1)};
           const uint32_t a1[4] = {q_pair(u0, 2), q_pair(u1, 2), q_pair(u0, 3), q_pair(u1, 3)};
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const uint4 x = xk[(q * NT + n) * 32];
-            mma_bf16(part[n], a0, x.x, x.y);
-            mma_bf16(part[n], a1, x.z, x.w);
+            const float4 x = lds_f4(xk + (q * NT + n) * 512);
+            mma_bf16(part[n], a0, __float_as_uint(x.x), __float_as_uint(x.y));
+            mma_bf16(part[n], a1, __float_as_uint(x.z), __float_as_uint(x.w));
           }
-          if ((((q + 1) * 32) & ((1 << p.gshift) - 1)) == 0) {   // the group is complete
-            const int gi = (q * 32) >> p.gshift;
-            const float s0 = sc[g * 8 + gi], s1 = sc[(g + 8) * 8 + gi];
+          if ((ends >> q) & 1u) {   // the group is complete
+            const float s0 = lds_f32(sc), s1 = lds_f32(sc + 8 * 32);
+            sc += 4;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -338,7 +337,7 @@ unsigned blocks_for(long long items, int per) { return static_cast<unsigned>((it
 cudaError_t launch_quantize_w4(const void* w, void* q4, float* scales, int N, int K, int group, bool bf16,
                                cudaStream_t st) {
   const long long n8 = static_cast<long long>(N) * K / 8;
-  const dim3 grid(blocks_for(n8, 256 * kQuantAhead));
+  const dim3 grid(blocks_for(n8, 256 * (bf16 ? kQuantAhead<__nv_bfloat16> : kQuantAhead<float>)));
   const int ls = group == 32 ? 2 : group == 64 ? 3 : 4;   // log2 of a group's lanes
   return bf16 ? launch(quantize_w4_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, static_cast<const __nv_bfloat16*>(w),
                        static_cast<uint32_t*>(q4), scales, n8, ls)
@@ -349,7 +348,7 @@ cudaError_t launch_quantize_w4(const void* w, void* q4, float* scales, int N, in
 cudaError_t launch_dequantize_w4(const void* q4, const float* scales, void* w, int N, int K, int group, bool bf16,
                                  cudaStream_t st) {
   const long long n8 = static_cast<long long>(N) * K / 8;
-  const dim3 grid(blocks_for(n8, 256 * kQuantAhead));
+  const dim3 grid(blocks_for(n8, 256 * (bf16 ? kQuantAhead<__nv_bfloat16> : kQuantAhead<float>)));
   const int ls = group == 32 ? 2 : group == 64 ? 3 : 4;
   return bf16 ? launch(dequantize_w4_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, static_cast<const uint32_t*>(q4),
                        scales, static_cast<__nv_bfloat16*>(w), n8, ls)
