@@ -109,7 +109,7 @@ struct GemmW4Params {
   const uint8_t* q4;
   const float* scales;
   void* c;
-  int M, N, K, gshift, tiles, slab, S;   // gshift: log2(group); slab: k of one pass; S: warps that share a tile
+  int M, N, K, tiles, slab, S;   // slab: k of one pass; S: warps that share a tile
 };
 
 template <int NT> struct W4Shape {
@@ -137,12 +137,15 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 }
 // q of nibbles i and i + 4 of a word as a bf16 pair.
 __device__ __forceinline__ uint32_t q_pair(uint32_t u, int i) {
-  const uint32_t v = ((u >> (4 * i)) & 0x000f000fu) | 0x43004300u, off = 0x43084308u;   // 128 + code, 136
+  uint32_t v;
+  const uint32_t off = 0x43084308u;   // 136
+  asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(v) : "r"(u >> (4 * i)));   // (u & mask) | 128.0: 128 + code
   const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&off));
   return *reinterpret_cast<const uint32_t*>(&q);
 }
 
-template <typename T, int NT>
+// GS: log2 of the group.
+template <typename T, int NT, int GS>
 __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_constant__ GemmW4Params p) {
   using W = W4Shape<NT>;
   constexpr int kSplit = sizeof(T) == 4 ? 3 : 1;   // columns of a row of A
@@ -156,16 +159,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_co
             tile1 = static_cast<int>(static_cast<long long>(blockIdx.x + 1) * p.tiles / gridDim.x);
   const int grp = warp / p.S, ws = warp - grp * p.S, groups = kWarps / p.S;
   const int my_tiles = (tile1 - tile0 - grp + groups - 1) / groups;   // tiles tile0 + grp, + groups, ...
-  const int per_chunk = kChunk >> p.gshift;                           // scales of a row and chunk
-  const long long row_bytes = p.K / 2, row_scales = p.K >> p.gshift;
+  constexpr int per_chunk = kChunk >> GS, kLog = 8 - GS;              // scales of a row and chunk
+  const long long row_bytes = p.K / 2, row_scales = p.K >> GS;
   // the warps of a tile (a barrier of theirs: at most eight groups of two or more)
   auto meet = [&] {
     if (p.S == 1) __syncwarp();
     else bar_sync_n(1 + grp, 32 * p.S);
   };
   const uint32_t my_ring = smem_u32(ring + warp * W::ring * W::stage);
-  // bit q: a group ends with the chunk's q-th 32 k
-  const unsigned ends = p.gshift == 5 ? 0xffu : p.gshift == 6 ? 0xaau : 0x88u;
   pdl_trigger();
   pdl_wait();
   for (int k0 = 0; k0 < p.K; k0 += p.slab) {
@@ -182,16 +183,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_co
           const uint8_t* src = p.q4 + (n0 + (lane >> 3)) * row_bytes + (k >> 1);
 #pragma unroll
           for (int i = 0; i < 4; ++i) cp_async16(dq + i * 4 * kRowPitch, src + i * 4 * row_bytes, true);
+#pragma unroll
           for (int i = lane; i < 16 * per_chunk; i += 32)
-            cp_async4(dst + 16 * kRowPitch + ((i >> (8 - p.gshift)) * 8 + (i & (per_chunk - 1))) * 4,
-                      p.scales + (n0 + (i >> (8 - p.gshift))) * row_scales + (kc >> p.gshift) + (i & (per_chunk - 1)), true);
+            cp_async4(dst + 16 * kRowPitch + ((i >> kLog) * 8 + (i & (per_chunk - 1))) * 4,
+                      p.scales + (n0 + (i >> kLog)) * row_scales + (kc >> GS) + (i & (per_chunk - 1)), true);
         } else {   // rows behind the last read it again, k behind the last count as zeros
           const bool ok = k < p.K;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             cp_async16(dq + i * 4 * kRowPitch, p.q4 + min(n0 + i * 4 + (lane >> 3), p.N - 1) * row_bytes + (ok ? k >> 1 : 0), ok);
           for (int i = lane; i < 16 * per_chunk; i += 32) {
-            const int row = i >> (8 - p.gshift), q = i & (per_chunk - 1), gi = (kc >> p.gshift) + q;
+            const int row = i >> kLog, q = i & (per_chunk - 1), gi = (kc >> GS) + q;
             const bool have = gi < row_scales;
             cp_async4(dst + 16 * kRowPitch + (row * 8 + q) * 4, p.scales + min(n0 + row, p.N - 1) * row_scales + (have ? gi : 0),
                       have);
@@ -212,24 +214,31 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_co
     constexpr int kColWarps = NT * 8 >= kWarps ? 1 : 2;   // warps that share a column
     for (int col = warp / kColWarps; col < NT * 8; col += kWarps / kColWarps) {
       const int m = col / kSplit, part = col - m * kSplit;
-      for (int q8 = (warp % kColWarps) * 32 + lane; q8 < chunks * (kChunk / 8); q8 += 32 * kColWarps) {
-      const int q = q8 >> 2, tt = q8 & 3, k = q8 * 8;
-      float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (m < p.M && k < ks) {
-        Vec8<T> v;
-        v.load(static_cast<const T*>(p.a) + static_cast<long long>(m) * p.K + k0 + k);
-        v.to_f32(f);
-      }
-      if (kSplit == 3) {   // the leading 8 bits, the next 8, the rest
+      const T* a = static_cast<const T*>(p.a) + static_cast<long long>(m) * p.K + k0;
+      for (int b8 = (warp % kColWarps) * 32 + lane; b8 < chunks * (kChunk / 8); b8 += 4 * 32 * kColWarps) {
+        Vec8<T> v[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          for (int s = 0; s < part; ++s) f[e] -= __uint_as_float(__float_as_uint(f[e]) & 0xffff0000u);
+        for (int j = 0; j < 4; ++j) {
+          const int k = (b8 + j * 32 * kColWarps) * 8;
+          if (m < p.M && k < ks) v[j].load(a + k);
+        }
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (part < 2) f[e] = __uint_as_float(__float_as_uint(f[e]) & 0xffff0000u);
-      }
-      sx[(q * NT * 8 + col) * 4 + tt] =
-          make_uint4(pack_bf16(f[0], f[4]), pack_bf16(f[1], f[5]), pack_bf16(f[2], f[6]), pack_bf16(f[3], f[7]));
+        for (int j = 0; j < 4; ++j) {
+          const int q8 = b8 + j * 32 * kColWarps;
+          float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          if (q8 >= chunks * (kChunk / 8)) break;
+          if (m < p.M && q8 * 8 < ks) v[j].to_f32(f);
+          if (kSplit == 3) {   // the leading 8 bits, the next 8, the rest
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float hi = __uint_as_float(__float_as_uint(f[e]) & 0xffff0000u), r = f[e] - hi;
+              const float mid = __uint_as_float(__float_as_uint(r) & 0xffff0000u);
+              f[e] = part == 0 ? hi : part == 1 ? mid : r - mid;
+            }
+          }
+          sx[((q8 >> 2) * NT * 8 + col) * 4 + (q8 & 3)] =
+              make_uint4(pack_bf16(f[0], f[4]), pack_bf16(f[1], f[5]), pack_bf16(f[2], f[6]), pack_bf16(f[3], f[7]));
+        }
       }
     }
     __syncthreads();
@@ -239,13 +248,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_co
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum[n][e] = part[n][e] = 0.f;
+        for (int e = 0; e < 4; ++e) sum[n][e] = 0.f;
       for (int c = 0; c < cpw; ++c) {
         asm volatile("cp.async.wait_group %0;" ::"n"(W::ring - 2) : "memory");
         __syncwarp();   // every lane's pieces of this chunk are there, and the next slot is free
         fetch();
         const uint32_t st = my_ring + slot * W::stage, codes = st + g * kRowPitch + t * 4;
-        uint32_t sc = st + 16 * kRowPitch + g * 32;
+        const uint32_t sc = st + 16 * kRowPitch + g * 32;
         slot = slot + 1 == W::ring ? 0 : slot + 1;
         const uint32_t xk = smem_u32(sx) + (((ws + c * p.S) * (kChunk / 32) * NT * 8 + g) * 4 + t) * 16;
 #pragma unroll
@@ -256,19 +265,19 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_co
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const float4 x = lds_f4(xk + (q * NT + n) * 512);
+            if ((q * 32) % (1 << GS) == 0) {   // a group begins
+#pragma unroll
+              for (int e = 0; e < 4; ++e) part[n][e] = 0.f;
+            }
             mma_bf16(part[n], a0, __float_as_uint(x.x), __float_as_uint(x.y));
             mma_bf16(part[n], a1, __float_as_uint(x.z), __float_as_uint(x.w));
           }
-          if ((ends >> q) & 1u) {   // the group is complete
-            const float s0 = lds_f32(sc), s1 = lds_f32(sc + 8 * 32);
-            sc += 4;
+          if ((q * 32 + 32) % (1 << GS) == 0) {   // the group is complete
+            const float s0 = lds_f32(sc + (q * 32 >> GS) * 4), s1 = lds_f32(sc + 8 * 32 + (q * 32 >> GS) * 4);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                sum[n][e] = fmaf(part[n][e], e < 2 ? s0 : s1, sum[n][e]);
-                part[n][e] = 0.f;
-              }
+              for (int e = 0; e < 4; ++e) sum[n][e] = fmaf(part[n][e], e < 2 ? s0 : s1, sum[n][e]);
           }
         }
       }
@@ -303,11 +312,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_co
 }
 
 template <typename T, int NT>
-cudaError_t launch_gemm_w4_t(GemmW4Params p, cudaStream_t st) {
+cudaError_t launch_gemm_w4_t(GemmW4Params p, int group, cudaStream_t st) {
   using W = W4Shape<NT>;
   static_assert(W::smem <= 227 * 1024, "shared memory of one CTA");
-  static std::atomic<uint64_t> done{0};
-  if (cudaError_t e = smem_attr_once(gemm_w4_kernel<T, NT>, W::smem, done)) return e;
+  static std::atomic<uint64_t> done[3];
+  const int gs = group == 32 ? 0 : group == 64 ? 1 : 2;
+  const auto kernel = gs == 0 ? gemm_w4_kernel<T, NT, 5> : gs == 1 ? gemm_w4_kernel<T, NT, 6> : gemm_w4_kernel<T, NT, 7>;
+  if (cudaError_t e = smem_attr_once(kernel, W::smem, done[gs])) return e;
   p.slab = W::slab;
   const int chunks = ((p.K < p.slab ? p.K : p.slab) + kChunk - 1) / kChunk;
   p.tiles = (p.N + 15) / 16;
@@ -327,7 +338,7 @@ cudaError_t launch_gemm_w4_t(GemmW4Params p, cudaStream_t st) {
       grid = ctas;
     }
   }
-  return launch(gemm_w4_kernel<T, NT>, dim3(grid), dim3(32 * kWarps), W::smem, st, p);
+  return launch(kernel, dim3(grid), dim3(32 * kWarps), W::smem, st, p);
 }
 
 unsigned blocks_for(long long items, int per) { return static_cast<unsigned>((items + per - 1) / per); }
@@ -358,13 +369,13 @@ cudaError_t launch_dequantize_w4(const void* q4, const float* scales, void* w, i
 
 cudaError_t launch_gemm_w4(const void* a, const void* q4, const float* scales, void* c, int M, int N, int K, int group,
                            bool bf16, cudaStream_t st) {
-  GemmW4Params p{a, static_cast<const uint8_t*>(q4), scales, c, M, N, K, group == 32 ? 5 : group == 64 ? 6 : 7, 0, 0, 0};
-  if (bf16) return M <= 8 ? launch_gemm_w4_t<__nv_bfloat16, 1>(p, st) : launch_gemm_w4_t<__nv_bfloat16, 2>(p, st);
+  GemmW4Params p{a, static_cast<const uint8_t*>(q4), scales, c, M, N, K, 0, 0, 0};
+  if (bf16) return M <= 8 ? launch_gemm_w4_t<__nv_bfloat16, 1>(p, group, st) : launch_gemm_w4_t<__nv_bfloat16, 2>(p, group, st);
   // three columns a row
-  if (M <= 2) return launch_gemm_w4_t<float, 1>(p, st);
-  if (M <= 5) return launch_gemm_w4_t<float, 2>(p, st);
-  if (M <= 8) return launch_gemm_w4_t<float, 3>(p, st);
-  return launch_gemm_w4_t<float, 6>(p, st);
+  if (M <= 2) return launch_gemm_w4_t<float, 1>(p, group, st);
+  if (M <= 5) return launch_gemm_w4_t<float, 2>(p, group, st);
+  if (M <= 8) return launch_gemm_w4_t<float, 3>(p, group, st);
+  return launch_gemm_w4_t<float, 6>(p, group, st);
 }
 
 }  // namespace hy
