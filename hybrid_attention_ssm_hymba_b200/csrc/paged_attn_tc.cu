@@ -15,9 +15,13 @@
 //   warp 1      UMMA issuer, per block: P_a V, S_a of the next block, P_b V, S_b of the next
 //   warps 2..9  softmax of group a, warps 10..17 of group b: two threads per row, each over 64
 //               of the block's keys and 64 of O's columns
-//   warps 18, 19 (e4m3 cache only) turn the 8-bit K and V of a block into the bf16 tiles the
-//               tensor core reads.  An e4m3 code is exact in bf16, so the row scales stay out of
-//               the products: the softmax threads multiply S's columns by K's and P's by V's.
+//   warps 18, 19 (e4m3 cache only) turn the 8-bit K and V of a block into the fp16 tiles the
+//               tensor core reads.  An e4m3 code is exact in fp16 (one conversion for two, where
+//               bf16 takes ten instructions: two warps could not keep up), so the row scales stay
+//               out of the products: the softmax threads multiply S's columns by K's and P's by
+//               V's.  Powers of two keep fp16's range: a row of Q is scaled to at most 2^8, V's
+//               scales to at most 2^10 of the largest that the tile has met, and P stays below
+//               2^4, so a product keeps 11 bits down to 2^-24 of the largest and 8 to 2^-27.
 // TMEM (512 columns): S_a | S_b | O_a | O_b; P in bf16 over the consumed S columns.
 //
 // Rows of V that no query of the tile sees (behind the sequence, between the meta rows and
@@ -30,7 +34,11 @@ namespace hy {
 namespace {
 
 constexpr int DH = 128, TILE_BYTES = 128 * DH * 2, HALF = 128 * 64 * 2;
-constexpr uint32_t IDESC_QK = idesc_bf16(128, 128, false, false), IDESC_PV = idesc_bf16(128, DH, false, true);
+// kind::f16 with bf16 or (FP8) fp16 operands
+constexpr uint32_t kFmtBits = (1u << 7) | (1u << 10);
+template <bool FP8> constexpr uint32_t IDESC_QK = idesc_bf16(128, 128, false, false) & ~(FP8 ? kFmtBits : 0u);
+template <bool FP8> constexpr uint32_t IDESC_PV = idesc_bf16(128, DH, false, true) & ~(FP8 ? kFmtBits : 0u);
+constexpr int kUp = 10;   // FP8: V's scales are at most 2^kUp
 
 // What the producer tells the softmax threads of each tile (they give the slot back) and of
 // each key block (it is at most four blocks ahead of them: a ring of 8 needs no giving back).
@@ -45,7 +53,8 @@ struct TileInfo {
 struct BlockInfo {
   int k0;
   uint32_t flags;     // bit x: group x masks; bit 2: some rows of V are to be zeroed
-  uint32_t pad[2];
+  int e;              // FP8: V's scales are held times 2^(kUp - e)
+  uint32_t pad;
   uint32_t valid[4];  // rows whose page number is valid, one bit each
 };
 constexpr uint32_t kZeroV = 4u;
@@ -66,7 +75,7 @@ template <> struct Smem<false> {   // behind the six tiles
 // through a ring of four blocks (the producer is at most three blocks ahead of the softmax).
 constexpr int kRawStages = 3, kRawBytes = 64 * DH, kScaleSlots = 4;
 template <> struct Smem<true> : Smem<false> {
-  uint64_t raw_full[kRawStages], raw_empty[kRawStages], scale_full[kScaleSlots];
+  uint64_t raw_full[kRawStages], raw_empty[kRawStages], scale_full[kScaleSlots], q_ready[2];
   alignas(16) float scale[kScaleSlots][2][128];   // [slot][K, V][row]
 };
 template <bool FP8> constexpr int smem_bytes() {
@@ -103,9 +112,9 @@ __device__ __forceinline__ void scale64(uint32_t (&sv)[64], uint32_t vec) {
     sv[4 * q + 3] = __float_as_uint(b.y);
   }
 }
-// row_exp64 with P's columns times V's scales before their rounding (the sum is without them).
-// Where a mask may have hidden a key its scale may be anything, and 0 stays 0.
-__device__ __forceinline__ float row_exp64_scaled(uint32_t (&sv)[64], float scale_log2, float m_ref, uint32_t vec, bool masked) {
+// row_exp64 with P's columns times V's scales before their rounding to fp16 (the sum is without
+// them).
+__device__ __forceinline__ float row_exp64_scaled(uint32_t (&sv)[64], float scale_log2, float m_ref, uint32_t vec) {
   const float2 sc = make_float2(scale_log2, scale_log2), nm = make_float2(-m_ref, -m_ref);
   float2 acc[2];
   acc[0] = acc[1] = make_float2(0.f, 0.f);
@@ -117,14 +126,22 @@ __device__ __forceinline__ float row_exp64_scaled(uint32_t (&sv)[64], float scal
       const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[4 * q + 2 * h]), __uint_as_float(sv[4 * q + 2 * h + 1])), sc, nm);
       const float2 pq = make_float2(ex2_approx(x.x), ex2_approx(x.y));
       acc[h] = __fadd2_rn(acc[h], pq);
-      float2 w = __fmul2_rn(pq, h ? make_float2(k.z, k.w) : make_float2(k.x, k.y));
-      if (masked) w = make_float2(pq.x == 0.f ? 0.f : w.x, pq.y == 0.f ? 0.f : w.y);
-      sv[2 * q + h] = pack_bf16(w.x, w.y);
+      const float2 w = __fmul2_rn(pq, h ? make_float2(k.z, k.w) : make_float2(k.x, k.y));
+      const __half2 r = __floats2half2_rn(w.x, w.y);
+      sv[2 * q + h] = *reinterpret_cast<const uint32_t*>(&r);
     }
   }
   const float2 t = __fadd2_rn(acc[0], acc[1]);
   return t.x + t.y;
 }
+// Two e4m3 codes (the low or the high half of u) as fp16.
+__device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t u, int half) {
+  uint32_t v;
+  if (half) asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, hi;}" : "=r"(v) : "r"(u));
+  else asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, lo;}" : "=r"(v) : "r"(u));
+  return v;
+}
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
 // P = 2^(S scale - m_ref), packed in place as bf16 pairs (sv[q] <- p[2q], p[2q + 1]); returns
 // the sum of the fp32 values.  P is rounded to bf16 once, as the P V operand.
 __device__ __forceinline__ float row_exp64(uint32_t (&sv)[64], float scale_log2, float m_ref) {
@@ -183,6 +200,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
         mbar_init(&sm.raw_empty[s], 64);
       }
       for (int s = 0; s < kScaleSlots; ++s) mbar_init(&sm.scale_full[s], 1);
+      for (int s = 0; s < 2; ++s) mbar_init(&sm.q_ready[s], 256);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -355,7 +373,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
 #pragma unroll
         for (int k = 0; k < DH / 16; ++k) {
           const uint32_t off = (k >> 2) * HALF + (k & 3) * 32;
-          umma_bf16_ss(tmem_base + x * 128, sdesc_add(qd, off), sdesc_add(kd, off), IDESC_QK, k != 0 ? 1u : 0u);
+          umma_bf16_ss(tmem_base + x * 128, sdesc_add(qd, off), sdesc_add(kd, off), IDESC_QK<FP8>, k != 0 ? 1u : 0u);
         }
         umma_commit(&sm.s_full[x]);
       };
@@ -363,11 +381,12 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
         const uint64_t vd = sdesc_add(dV, s * TILE_BYTES);
 #pragma unroll
         for (int k = 0; k < 128 / 16; ++k)
-          umma_bf16_ts(tmem_base + 256 + x * 128, tmem_base + x * 128 + k * 8, sdesc_add(vd, k * 16 * 128), IDESC_PV,
+          umma_bf16_ts(tmem_base + 256 + x * 128, tmem_base + x * 128 + k * 8, sdesc_add(vd, k * 16 * 128), IDESC_PV<FP8>,
                        (acc || k != 0) ? 1u : 0u);
         umma_commit(&sm.o_done[x]);
       };
       uint32_t jb = 0, cnt[2] = {0, 0};   // blocks so far: all, and per group
+      uint32_t tiles[2] = {0, 0};         // and tiles, per group
       bool ok = true;
       for (uint32_t seg = 0; ok; ++seg) {
         const TileInfo& ti = sm.tile[seg & (kTileSlots - 1)];
@@ -376,6 +395,11 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
         const int n = ti.n, gr = ti.groups;
         ok = mbar_wait(&sm.q_full, seg & 1, p.status, abort_flag) &&
              mbar_wait(&sm.k_full[jb & 1], (jb >> 1) & 1, p.status, abort_flag);
+        if constexpr (FP8) {   // Q in fp16
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (ok && x < gr) ok = mbar_wait(&sm.q_ready[x], tiles[x]++ & 1, p.status, abort_flag);
+        }
         // S_x goes over the TMEM columns that the last P V of the previous tile reads
         for (int x = 0; ok && x < gr; ++x)
           if (cnt[x] > 0) ok = mbar_wait(&sm.o_done[x], (cnt[x] - 1) & 1, p.status, abort_flag);
@@ -425,35 +449,71 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(&sm.tile_full[seg & (kTileSlots - 1)], (seg / kTileSlots) & 1, p.status,
                                                abort_flag));
         if (!ok || ti.toks == 0) break;
-        const int n = ti.n;
+        const int n = ti.n, p1 = ti.p1, lo = p.g.window < 0 ? 0 : ti.p0 - p.g.window;
+        uint32_t most = 0;   // the largest of V's scales so far, as bits
         for (int j = 0; ok && j < n; ++j, ++jb) {
           const uint32_t s = jb & 1, par = (jb >> 1) & 1;
 #pragma unroll 1
           for (int u = 0; u < 4; ++u, ++raw) {
             const uint32_t rs = raw % kRawStages;
-            if ((u & 1) == 0) ok = __all_sync(0xffffffffu, mbar_wait(u ? &sm.v_empty[s] : &sm.k_empty[s], par ^ 1u, p.status, abort_flag));
+            if ((u & 1) == 0)
+              ok = __all_sync(0xffffffffu, mbar_wait(u ? &sm.v_empty[s] : &sm.k_empty[s], par ^ 1u, p.status, abort_flag));
             ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.raw_full[rs], (raw / kRawStages) & 1, p.status, abort_flag));
+            BlockInfo& bi = sm.block[jb & (kBlockSlots - 1)];
+            if (u == 0 && warp == 18 && ok) {
+              // V's scales: 0 for rows that no query of the tile sees, the others brought to fp16's
+              // range.  Done before k_full, so that S of the block implies it.
+              ok = __all_sync(0xffffffffu, mbar_wait(&sm.scale_full[jb % kScaleSlots], (jb / kScaleSlots) & 1, p.status, abort_flag));
+              float4& v4 = *reinterpret_cast<float4*>(&sm.scale[jb % kScaleSlots][1][lane * 4]);
+              float v[4] = {v4.x, v4.y, v4.z, v4.w};
+              const uint32_t valid = bi.valid[lane >> 3] >> ((lane & 7) * 4);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int key = bi.k0 + lane * 4 + e;
+                if (!((valid >> e) & 1u) || key > p1 || (key < lo && key >= p.g.n_meta)) v[e] = 0.f;
+                most = max(most, __float_as_uint(v[e]) & 0x7fffffffu);
+              }
+              most = __reduce_max_sync(0xffffffffu, most);
+              const int ex = max(static_cast<int>(most >> 23) - 126, kUp - 127);   // every scale is below 2^ex
+              const float f = pow2(kUp - ex);
+              v4 = make_float4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
+              if (lane == 0) bi.e = ex;
+              __syncwarp();
+            }
             if (!ok) break;
             const uint32_t src = smem_u32(sRaw + rs * kRawBytes) + t * 16;
-            uint8_t* dst = (u < 2 ? sK : sV) + s * TILE_BYTES + ((t & 4) ? HALF : 0);
+            const uint32_t dst = smem_u32((u < 2 ? sK : sV) + s * TILE_BYTES + ((t & 4) ? HALF : 0));
+            const bool hide = u >= 2 && (bi.flags & kZeroV);
+            const int k0 = bi.k0;
             // 16 codes (one of a row's eight chunks) at a time, to two 16-byte chunks of the
             // swizzled tile; the four lanes of the upper half store theirs in the other order,
             // so that the eight lanes of a row meet no bank twice
             const int c = (t & 3) * 2, flip = (t >> 2) & 1;
+            float4 r4[8];   // all in flight before the first is used
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r4[i] = lds_f4(src + i * 1024);
+            mbar_arrive(&sm.raw_empty[rs]);
+            if (hide) {   // rows of V that no query of the tile sees (they may hold NaN codes)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int key = k0 + (u & 1) * 64 + i * 8 + (t >> 3);
+                if (key > p1 || (key < lo && key >= p.g.n_meta)) r4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+              }
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int row = (u & 1) * 64 + i * 8 + (t >> 3);
-              const float4 raw4 = lds_f4(src + i * 1024);
-              const uint2 a = bf16_of_e4m3(__float_as_uint(raw4.x)), b = bf16_of_e4m3(__float_as_uint(raw4.y)),
-                          d = bf16_of_e4m3(__float_as_uint(raw4.z)), e = bf16_of_e4m3(__float_as_uint(raw4.w));
-              const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, e.x, e.y);
-              const uint32_t at = smem_u32(dst) + row * 128, sw = row & 7;
-              const uint4 v0 = flip ? hi : lo, v1 = flip ? lo : hi;
-              sts_u32x4(at + (((c + flip) ^ sw) << 4), v0.x, v0.y, v0.z, v0.w);
-              sts_u32x4(at + (((c + (flip ^ 1)) ^ sw) << 4), v1.x, v1.y, v1.z, v1.w);
+              const uint32_t w[4] = {__float_as_uint(r4[i].x), __float_as_uint(r4[i].y), __float_as_uint(r4[i].z),
+                                     __float_as_uint(r4[i].w)};
+              uint32_t h[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) h[e] = f16_of_e4m3(w[e >> 1], e & 1);
+              const uint32_t at = dst + row * 128, sw = row & 7;
+              const uint32_t a0 = at + (((c + flip) ^ sw) << 4), a1 = at + (((c + (flip ^ 1)) ^ sw) << 4);
+              sts_u32x4(a0, flip ? h[4] : h[0], flip ? h[5] : h[1], flip ? h[6] : h[2], flip ? h[7] : h[3]);
+              sts_u32x4(a1, flip ? h[0] : h[4], flip ? h[1] : h[5], flip ? h[2] : h[6], flip ? h[3] : h[7]);
             }
             fence_proxy_async_smem();
-            mbar_arrive(&sm.raw_empty[rs]);
             mbar_arrive(u < 2 ? &sm.k_full[s] : &sm.v_full[s]);
           }
         }
@@ -467,7 +527,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tSx = tmem_base + x * 128 + lane_off, tOx = tmem_base + 256 + x * 128 + lane_off + kh * 64;
     const int rtok = x * p.g.TQ + r / p.g.G;   // this row's token of the tile
-    constexpr float kRescaleLog2 = 8.0f;
+    constexpr float kRescaleLog2 = FP8 ? 4.0f : 8.0f;
     uint32_t jb = 0, cnt = 0;
     bool ok = true;
     for (uint32_t seg = 0;; ++seg) {
@@ -485,7 +545,41 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
         if (lane == 0) mbar_arrive(&sm.tile_empty[seg & (kTileSlots - 1)]);
         continue;
       }
-      float m_used = -INFINITY, l = 0.f;
+      float m_used = -INFINITY, l = 0.f, to_log2 = p.scale_log2;
+      int e_used = 0;   // FP8: the exponent of V's scales that O is held with
+      if constexpr (FP8) {
+        // this half of the row of Q from bf16 to fp16, its largest value in [2^7, 2^8)
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.q_full, seg & 1, p.status, abort_flag));
+        const uint32_t row = smem_u32(sQ + x * TILE_BYTES + kh * HALF + r * 128);
+        uint32_t q[32], mx = 0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const float4 v = lds_f4(row + ((c ^ (r & 7)) << 4));
+          q[4 * c] = __float_as_uint(v.x);
+          q[4 * c + 1] = __float_as_uint(v.y);
+          q[4 * c + 2] = __float_as_uint(v.z);
+          q[4 * c + 3] = __float_as_uint(v.w);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx = max(mx, max(q[4 * c + e] & 0x7fffu, (q[4 * c + e] >> 16) & 0x7fffu));
+        }
+        sm.smax[cnt & 1][x][kh][r] = __uint_as_float(mx);
+        bar_sync_n(1 + x, 256);
+        mx = max(mx, __float_as_uint(sm.smax[cnt & 1][x][kh ^ 1][r]));
+        const int f = min(134 - static_cast<int>(mx >> 7), 126);
+        const float up = pow2(f);
+        to_log2 *= pow2(-f);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __half2 h = __floats2half2_rn(bf16lo(q[4 * c + e]) * up, bf16hi(q[4 * c + e]) * up);
+            q[4 * c + e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          sts_u32x4(row + ((c ^ (r & 7)) << 4), q[4 * c], q[4 * c + 1], q[4 * c + 2], q[4 * c + 3]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&sm.q_ready[x]);
+      }
       for (int j = 0; j < n; ++j, ++jb, ++cnt) {
         ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.s_full[x], cnt & 1, p.status, abort_flag));
         uint32_t sv[64];
@@ -512,7 +606,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
               if (!vis) sv[e] = __float_as_uint(-INFINITY);
             }
           }
-          m_half = row_max64(sv) * p.scale_log2;
+          m_half = row_max64(sv) * to_log2;
         }
         // the row maximum over both halves; the barrier also orders this half's reads of
         // S before the other half's P stores (P of keys 64..127 lands in S columns 32..63)
@@ -531,12 +625,19 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
           const float m_ref = (m_used == -INFINITY) ? 0.f : m_used;
           float sum;
           if constexpr (FP8)
-            sum = row_exp64_scaled(sv, p.scale_log2, m_ref, smem_u32(&sm.scale[jb % kScaleSlots][1][kh * 64]),
-                                   (bi.flags & (1u << x)) != 0);
+            sum = row_exp64_scaled(sv, to_log2, m_ref, smem_u32(&sm.scale[jb % kScaleSlots][1][kh * 64]));
           else
-            sum = row_exp64(sv, p.scale_log2, m_ref);
+            sum = row_exp64(sv, to_log2, m_ref);
+          float alpha_o = alpha;
+          bool moved = need;
+          if constexpr (FP8) {
+            const int e = bi.e;
+            moved |= e != e_used;
+            alpha_o *= pow2(e_used - e);
+            e_used = e;
+          }
           tmem_st32(tSx + kh * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-          if (j > 0 && __any_sync(0xffffffffu, need)) {
+          if (j > 0 && __any_sync(0xffffffffu, moved)) {
             // rescale this half of O (every earlier P V of this group has completed: S_x(j)
             // was issued after it, and P_x V_j cannot start before p_full below)
 #pragma unroll 1
@@ -545,7 +646,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
               tmem_ld16(tOx + c * 16, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha_o);
               tmem_st16(tOx + c * 16, o);
             }
           }
@@ -580,7 +681,8 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
       if (ok) {
         tc_fence_after();
         const bool mine = rtok < (x + 1) * p.g.TQ && rtok < ti.toks, whole = ti.part < 0;
-        const float inv = lsum != 0.f ? 1.f / lsum : 0.f;
+        // FP8: O is held times 2^(kUp - e_used), taken out in two steps that stay normal numbers
+        const float down = FP8 ? pow2(e_used) : 1.f, inv = (lsum != 0.f ? 1.f / lsum : 0.f) * (FP8 ? pow2(-kUp) : 1.f);
         __nv_bfloat16* orow = p.out + static_cast<long long>(ti.row0 + rtok) * p.out_ld +
                               (ti.kvh * p.g.G + r % p.g.G) * DH + kh * 64;
         const long long prow = (static_cast<long long>(blockIdx.x) * 2 + ti.part) * p.part_rows + x * 128 + r;
@@ -591,6 +693,11 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
           uint32_t o[16];
           tmem_ld16(tOx + c * 16, o);
           tmem_wait_ld();
+          if constexpr (FP8) {
+            const float f = whole ? down : down * pow2(-kUp);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+          }
           if (!whole) {
             uint4* dst = reinterpret_cast<uint4*>(part + c * 16);
 #pragma unroll

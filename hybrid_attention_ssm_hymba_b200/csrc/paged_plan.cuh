@@ -239,19 +239,4 @@ struct PieceWalk {
   }
 };
 
-// Two e4m3 codes in the high bytes of 16-bit halves (the low bytes may be anything) as bf16,
-// exactly: a code's exponent and mantissa go to the low end of bf16's exponent and the top of
-// its mantissa, which is the value times 2^-120 (also for subnormal codes).  The NaN code
-// comes out as 480: a row that holds a NaN has a NaN scale.
-HY_DEV uint32_t bf16_of_e4m3_high(uint32_t h) {
-  const __nv_bfloat162 up = __float2bfloat162_rn(1.329227995784916e36f);   // 2^120
-  const uint32_t b = (h & 0x80008000u) | ((h >> 4) & 0x07f007f0u);
-  const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), up);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-// Four consecutive codes as two bf16 pairs.
-HY_DEV uint2 bf16_of_e4m3(uint32_t u) {
-  return make_uint2(bf16_of_e4m3_high(__byte_perm(u, u, 0x1100)), bf16_of_e4m3_high(__byte_perm(u, u, 0x3322)));
-}
-
 }  // namespace hy
