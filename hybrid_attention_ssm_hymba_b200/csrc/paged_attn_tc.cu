@@ -83,6 +83,8 @@ template <bool FP8> constexpr int smem_bytes() {
 }
 static_assert(smem_bytes<true>() <= 227 * 1024, "shared memory of one CTA");
 
+// The n low bits of a word (n <= 0: none, n >= 32: all).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 __device__ __forceinline__ float max3f(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
       mbar_init(&sm.v_full[s], FP8 ? 128 : 1);
       mbar_init(&sm.v_empty[s], 1);
       mbar_init(&sm.s_full[s], 1);
-      mbar_init(&sm.p_full[s], 256);
+      mbar_init(&sm.p_full[s], 8);   // a lane of each warp
       mbar_init(&sm.o_done[s], 1);
     }
     for (int s = 0; s < kTileSlots; ++s) {
@@ -200,7 +202,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
         mbar_init(&sm.raw_empty[s], 64);
       }
       for (int s = 0; s < kScaleSlots; ++s) mbar_init(&sm.scale_full[s], 1);
-      for (int s = 0; s < 2; ++s) mbar_init(&sm.q_ready[s], 256);
+      for (int s = 0; s < 2; ++s) mbar_init(&sm.q_ready[s], 8);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -492,7 +494,6 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
             float4 r4[8];   // all in flight before the first is used
 #pragma unroll
             for (int i = 0; i < 8; ++i) r4[i] = lds_f4(src + i * 1024);
-            mbar_arrive(&sm.raw_empty[rs]);
             if (hide) {   // rows of V that no query of the tile sees (they may hold NaN codes)
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
@@ -514,6 +515,9 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
               sts_u32x4(a1, flip ? h[0] : h[4], flip ? h[1] : h[5], flip ? h[2] : h[6], flip ? h[3] : h[7]);
             }
             fence_proxy_async_smem();
+            // only now: an arrival right behind the loads can overtake them, and the next copy would
+            // land in what they still read
+            mbar_arrive(&sm.raw_empty[rs]);
             mbar_arrive(u < 2 ? &sm.k_full[s] : &sm.v_full[s]);
           }
         }
@@ -578,7 +582,8 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
           sts_u32x4(row + ((c ^ (r & 7)) << 4), q[4 * c], q[4 * c + 1], q[4 * c + 2], q[4 * c + 3]);
         }
         fence_proxy_async_smem();
-        mbar_arrive(&sm.q_ready[x]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_ready[x]);
       }
       for (int j = 0; j < n; ++j, ++jb, ++cnt) {
         ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.s_full[x], cnt & 1, p.status, abort_flag));
@@ -598,12 +603,13 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
           if (flags & (1u << x)) {
             // key e of this half is visible iff e <= hi and (e >= lo or e < me), on a valid page
             const int base = bi.k0 + kh * 64, hi = ti.p0 + rtok - base, me = p.g.n_meta - base;
-            const int lo = p.g.window < 0 ? 0 : hi - p.g.window;
-            const uint32_t v0 = bi.valid[kh * 2], v1 = bi.valid[kh * 2 + 1];
+            const int lo = p.g.window < 0 ? -base : hi - p.g.window;
 #pragma unroll
-            for (int e = 0; e < 64; ++e) {
-              const bool vis = e <= hi && (e >= lo || e < me) && (((e < 32 ? v0 : v1) >> (e & 31)) & 1u);
-              if (!vis) sv[e] = __float_as_uint(-INFINITY);
+            for (int w = 0; w < 2; ++w) {
+              const uint32_t see = low_bits(hi + 1 - 32 * w) & (~low_bits(lo - 32 * w) | low_bits(me - 32 * w)) & bi.valid[kh * 2 + w];
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(see & (1u << e))) sv[32 * w + e] = __float_as_uint(-INFINITY);
             }
           }
           m_half = row_max64(sv) * to_log2;
@@ -671,7 +677,8 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
           l = fmaf(l, alpha, sum);
         }
         tc_fence_before();
-        mbar_arrive(&sm.p_full[x]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[x]);
       }
       ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.o_done[x], (cnt - 1) & 1, p.status, abort_flag));
       // the row sum over both halves
