@@ -59,6 +59,7 @@ struct BlockInfo {
 };
 constexpr uint32_t kZeroV = 4u;
 
+constexpr int kPlanBatch = 64;   // batches up to this are planned by every CTA itself
 template <bool FP8> struct Smem;
 template <> struct Smem<true>;   // with the scales and barriers of the 8-bit path, below
 template <> struct Smem<false> {   // behind the six tiles
@@ -70,6 +71,7 @@ template <> struct Smem<false> {   // behind the six tiles
   alignas(16) TileInfo tile[kTileSlots];
   alignas(16) BlockInfo block[kBlockSlots];
   float smax[2][2][2][128];   // [block parity][group][half][row]
+  long long prefix[kPlanBatch + 1];
 };
 // 8-bit path: raw K and V come in half tiles of 64 rows through a ring of three, their scales
 // through a ring of four blocks (the producer is at most three blocks ahead of the softmax).
@@ -219,10 +221,15 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = sm.tmem_slot;
   pdl_wait();
+  const long long* prefix = p.prefix;
+  if (p.rb.batch <= kPlanBatch) {
+    plan_by_warps(p, sm.prefix, blockIdx.x == 0);
+    prefix = sm.prefix;
+  }
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer (whole warp)
-    PieceWalk walk;
+    PieceWalk walk(p, prefix);
     Piece pc;
     const int npc = 128 / p.piece;   // K/V loads per block and half: lane i < npc issues piece i's
     const int none = p.kv.n_pages * p.kv.page_size;   // a row beyond the map: zeros
@@ -230,9 +237,8 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
     uint32_t k_iss = 0, v_iss = 0, k_par = 0, v_par = 0;
     uint32_t raw = 0, scales_issued = 0;   // FP8: half tiles, and blocks whose scales are under way
     bool ok = true;
-    walk.init(p, p.prefix);
     for (;;) {
-      const bool more = walk.next(p, &pc);
+      const bool more = walk.next(p, &pc, lane == 0);
       const int groups = pc.ts.toks > p.g.TQ ? 2 : 1;   // row groups with tokens
       ok = mbar_wait(&sm.q_empty, (seg & 1) ^ 1u, p.status, abort_flag) &&
            mbar_wait(&sm.tile_empty[seg & (kTileSlots - 1)], ((seg / kTileSlots) & 1) ^ 1u, p.status, abort_flag);
@@ -590,11 +596,11 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
         uint32_t sv[64];
         float m_half = -INFINITY;
         const volatile BlockInfo& bi = sm.block[jb & (kBlockSlots - 1)];
+        const uint32_t flags = bi.flags;
         if (ok) {
           tc_fence_after();
           tmem_ld32(tSx + kh * 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
           tmem_ld32(tSx + kh * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-          const uint32_t flags = bi.flags;
           tmem_wait_ld();
           if constexpr (FP8) {
             ok = __all_sync(0xffffffffu, mbar_wait(&sm.scale_full[jb % kScaleSlots], (jb / kScaleSlots) & 1, p.status, abort_flag));
@@ -656,7 +662,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
               tmem_st16(tOx + c * 16, o);
             }
           }
-          if (!FP8 && (bi.flags & kZeroV)) {
+          if (!FP8 && (flags & kZeroV)) {
             // rows of V that no query of the tile sees: [a0, a1) between the meta rows and the
             // window, [b0, 128) behind the last query
             const int k0 = bi.k0, tid = (warp - 2 - 8 * x) * 32 + lane;
@@ -732,44 +738,36 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
   }
 }
 
-// Joins the parts of each tile that a boundary cut: CTA (i, y) looks at the boundary between
-// CTAs i and i + 1 of the attention and takes every gridDim.y-th group of eight rows (a warp
-// each) of the tile, if this is its first boundary.  A row's parts are weighted by 2^(m - max).
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedAttnParams p, int ctas) {
+// Joins the parts of the tile that CTA i of the attention began and others finished: a warp a
+// row, gridDim.y CTAs a tile.  A row's parts are weighted by 2^(m - max).
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedAttnParams p) {
   pdl_trigger();
   pdl_wait();
-  const PieceLine line(p.prefix[p.rb.batch], ctas, p.min_blocks);
   const int i = blockIdx.x;
-  if (i + 1 >= line.n) return;
-  Walk w;
-  const long long at = line.start(i + 1);
-  w.seek(p.rb, p.kv, p.g, p.prefix, at);
-  if (w.off == 0 || line.start(i) > at - w.off) return;   // not cut here, or cut before
-  const TileSpan ts = tile_span(p.g, w.s, w.t);
-  const long long end = at - w.off + ts.n;
-  int last = i + 1;                                      // the last CTA with a part
-  while (last + 1 < line.n && line.start(last + 1) < end) ++last;
+  const CutRecord cut = p.cut[i];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group_rows = p.g.TQ * p.g.G;
-  for (int rr = blockIdx.y * 8 + warp; rr < ts.toks * p.g.G; rr += gridDim.y * 8) {
+  for (int rr = blockIdx.y * 8 + warp; rr < cut.toks * p.g.G; rr += gridDim.y * 8) {
     const int x = rr / group_rows, r = rr - x * group_rows, tok = x * p.g.TQ + r / p.g.G, rg = r % p.g.G;
+    // part c of the row lies at first[(2 c + (c == i)) * part_rows]: the first one is CTA i's own
+    const long long row = x * 128 + r;
     float m = -INFINITY;
-    for (int c = i + lane; c <= last; c += 32)
-      m = fmaxf(m, p.part_ml[(2LL * c + (c == i ? 1 : 0)) * p.part_rows + x * 128 + r].x);
+    for (int c = i + lane; c <= cut.last; c += 32)
+      m = fmaxf(m, p.part_ml[(2LL * c + (c == i)) * p.part_rows + row].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
-    for (int c = i; c <= last; ++c) {
-      const long long row = (2LL * c + (c == i ? 1 : 0)) * p.part_rows + x * 128 + r;
-      const float2 ml = p.part_ml[row];
-      const float4 v = reinterpret_cast<const float4*>(p.part + row * DH)[lane];
-      if (ml.x == -INFINITY) continue;
-      const float f = ex2_approx(ml.x - m);
+#pragma unroll 4
+    for (int c = i; c <= cut.last; ++c) {
+      const long long at = (2LL * c + (c == i)) * p.part_rows + row;
+      const float2 ml = p.part_ml[at];
+      const float4 v = reinterpret_cast<const float4*>(p.part + at * DH)[lane];
+      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
       l = fmaf(ml.y, f, l);
-      acc = make_float4(fmaf(v.x, f, acc.x), fmaf(v.y, f, acc.y), fmaf(v.z, f, acc.z), fmaf(v.w, f, acc.w));
+      if (f != 0.f) acc = make_float4(fmaf(v.x, f, acc.x), fmaf(v.y, f, acc.y), fmaf(v.z, f, acc.z), fmaf(v.w, f, acc.w));
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;
-    __nv_bfloat16* o = p.out + static_cast<long long>(w.s.q0 + ts.tok0 + tok) * p.out_ld + (w.kvh * p.g.G + rg) * DH;
+    __nv_bfloat16* o = p.out + static_cast<long long>(cut.row0 + tok) * p.out_ld + (cut.kvh * p.g.G + rg) * DH;
     reinterpret_cast<uint2*>(o)[lane] = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
   }
 }
@@ -805,7 +803,7 @@ bool encode(CUtensorMap* m, bool bytes, int rank, const void* base, const cuuint
 
 cudaError_t launch_paged_join(const PagedAttnParams& p, int ctas, cudaStream_t st) {
   if (ctas < 2) return cudaSuccess;
-  return launch(paged_join_kernel, dim3(ctas - 1, (p.part_rows + 31) / 32), dim3(256), 0, st, p, ctas);
+  return launch(paged_join_kernel, dim3(ctas - 1, (p.part_rows + 31) / 32), dim3(256), 0, st, p);
 }
 
 // The scratch is sized for the B200's 148 SMs; a launch uses at most that many CTAs.
@@ -841,6 +839,7 @@ cudaError_t launch_paged_attention_tc(const PagedAttnDesc& a, cudaStream_t st) {
   p.prefix = reinterpret_cast<long long*>(sc + L.prefix);
   p.part = reinterpret_cast<float*>(sc + L.part);
   p.part_ml = reinterpret_cast<float2*>(sc + L.ml);
+  p.cut = reinterpret_cast<CutRecord*>(sc + L.cut);
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.out_ld = a.out_ld;
   const int most = fp8 ? 64 : 128;
@@ -858,9 +857,8 @@ cudaError_t launch_paged_attention_tc(const PagedAttnDesc& a, cudaStream_t st) {
   if (!encode(&tq, false, 3, a.q, qd, qs, qb) || !encode(&tk, fp8, 2, a.kv.pages, kd, ks, kb) ||
       !encode(&tv, fp8, 2, static_cast<const uint8_t*>(a.kv.pages) + rows * row_bytes, kd, ks, kb))
     return cudaErrorInvalidValue;
-  if (cudaError_t e = launch(paged_plan_kernel, dim3(1), dim3(1024), 0, st, a.kv, a.rb, p.g, p.prefix,
-                             a.status))
-    return e;
+  if (a.rb.batch > kPlanBatch)
+    if (cudaError_t e = launch(paged_plan_kernel, dim3(1), dim3(1024), 0, st, a.kv, a.rb, p.g, p.prefix, a.status)) return e;
   if (cudaError_t e = fp8 ? launch(paged_attn_tc<true>, dim3(ctas), dim3(kThreadsFp8), smem_bytes<true>(), st, tq, tk, tv, p)
                           : launch(paged_attn_tc<false>, dim3(ctas), dim3(kThreads), smem_bytes<false>(), st, tq, tk, tv, p))
     return e;

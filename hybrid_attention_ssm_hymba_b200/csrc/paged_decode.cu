@@ -131,8 +131,6 @@ __device__ void plan_here(const PagedAttnParams& p, Shared& sm, bool report) {
   }
   if (threadIdx.x == 0) sm.prefix[p.rb.batch] = carry;
   __syncthreads();
-  if (report)   // the join reads it
-    for (int b = threadIdx.x; b <= p.rb.batch; b += 32 * kWarps) p.prefix[b] = sm.prefix[b];
 }
 
 // NT: tiles of eight queries.
@@ -155,10 +153,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) paged_decode_ker
   const uint8_t* vbase = kbase + static_cast<long long>(p.kv.n_pages) * p.kv.page_size * p.kv.hkv * DH * es;
   const long long row_bytes = static_cast<long long>(p.kv.hkv) * DH * es;
 
-  PieceWalk walk;
+  PieceWalk walk(p, prefix);
   Piece pc;
-  walk.init(p, prefix);
-  while (walk.next(p, &pc)) {
+  while (walk.next(p, &pc, threadIdx.x == 0)) {
     const int rows = pc.ts.toks * p.g.G;
     // Q of queries 8 n + g in the dims' order; qs turns the products of queries 8 n + 2t + e into
     // log2 units; at: those queries' places in the sequence
@@ -546,6 +543,7 @@ cudaError_t launch_paged_decode(const PagedAttnDesc& a, cudaStream_t st) {
   p.prefix = reinterpret_cast<long long*>(sc + L.prefix);
   p.part = reinterpret_cast<float*>(sc + L.part);
   p.part_ml = reinterpret_cast<float2*>(sc + L.ml);
+  p.cut = reinterpret_cast<CutRecord*>(sc + L.cut);
   p.q = static_cast<const __nv_bfloat16*>(a.q);
   p.q_ld = a.q_ld;
   p.out = static_cast<__nv_bfloat16*>(a.out);

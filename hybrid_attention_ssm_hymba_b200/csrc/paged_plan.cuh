@@ -19,6 +19,12 @@ struct PagedGeo {
   int n_meta, window;
 };
 
+// A tile that CTA i begins and others finish: its rows, and the last CTA with a part of it.
+// toks = 0: CTA i leaves no tile unfinished.
+struct CutRecord {
+  int row0, toks, kvh, last;
+};
+
 // What the attention kernels and the join share.
 struct PagedAttnParams {
   PagedKv kv;
@@ -32,6 +38,7 @@ struct PagedAttnParams {
   long long out_ld;
   float* part;          // [CTA][2][part_rows][dh]: 0 = the CTA's first tile continued, 1 = its last tile begun
   float2* part_ml;      // [CTA][2][part_rows] (m in log2 units, sum)
+  CutRecord* cut;       // [CTA]
   int part_rows;
   int page_shift;       // log2(page_size) where that is a power of two, else -1
   int piece;            // tensor-core kernel: rows of one K/V load
@@ -44,7 +51,7 @@ inline int page_shift(int page_size) {
   return (1 << s) == page_size ? s : -1;
 }
 struct PagedScratch {
-  size_t prefix, part, ml, total;
+  size_t prefix, part, ml, cut, total;
 };
 inline PagedScratch paged_scratch_layout(int batch, int ctas, int part_rows, int dh) {
   auto al = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
@@ -53,6 +60,7 @@ inline PagedScratch paged_scratch_layout(int batch, int ctas, int part_rows, int
   s.prefix = o; o = al(o + (static_cast<size_t>(batch) + 1) * 8);
   s.part = o; o = al(o + static_cast<size_t>(ctas) * 2 * part_rows * dh * 4);
   s.ml = o; o = al(o + static_cast<size_t>(ctas) * 2 * part_rows * 8);
+  s.cut = o; o = al(o + static_cast<size_t>(ctas) * sizeof(CutRecord));
   s.total = o;
   return s;
 }
@@ -136,15 +144,28 @@ static __global__ void __launch_bounds__(1024) paged_plan_kernel(const PagedKv k
   if (threadIdx.x == 0) prefix[rb.batch] = carry;
 }
 
-// CTA i's piece of the line of W blocks, over at most n CTAs.
+// a / b for non-negative a and positive b (32-bit where that does: a 64-bit division costs a
+// kernel's first microsecond)
+HY_DEV long long div_pos(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
+
+// The pieces of a line of W blocks over at most `ctas` CTAs: the first `more` have one block more
+// than the rest.
 struct PieceLine {
-  long long W;
+  long long each, more;
   int n;
-  HY_DEV PieceLine(long long w, int ctas, int min_blocks) : W(w) {
-    const long long most = (w + min_blocks - 1) / min_blocks;
+  HY_DEV PieceLine(long long w, int ctas, int min_blocks) {
+    const long long most = div_pos(w + min_blocks - 1, min_blocks);
     n = static_cast<int>(most < ctas ? most : ctas);
+    each = n ? div_pos(w, n) : 0;
+    more = w - each * n;
   }
-  HY_DEV long long start(int i) const { return i * W / n; }   // i <= n
+  HY_DEV long long start(int i) const { return i * each + (i < more ? i : more); }   // i <= n
+  HY_DEV int owner(long long block) const {
+    const long long wide = more * (each + 1);
+    return static_cast<int>(block < wide ? div_pos(block, each + 1) : more + div_pos(block - wide, each));
+  }
 };
 
 // A walk along the line from block `w`; every lane of a warp holds the same state.
@@ -166,8 +187,8 @@ struct Walk {
     b = lo;
     load(rb, kv, g);
     long long rem = w - prefix[b];
-    const long long per = (prefix[b + 1] - prefix[b]) / kv.hkv;
-    kvh = static_cast<int>(rem / per);
+    const long long per = div_pos(prefix[b + 1] - prefix[b], kv.hkv);
+    kvh = static_cast<int>(div_pos(rem, per));
     rem -= kvh * per;
     const int lane = threadIdx.x & 31;
     for (int t0 = 0;; t0 += 32) {   // ends: rem < per = the sum over the tiles
@@ -212,20 +233,24 @@ struct Piece {
 };
 struct PieceWalk {
   Walk w;
-  long long left;
+  long long left, at;    // blocks left of the piece, and the place on the line
+  PieceLine line;
   bool first = true;
-  HY_DEV void init(const PagedAttnParams& p, const long long* prefix) {
-    const PieceLine line(prefix[p.rb.batch], gridDim.x, p.min_blocks);
+  HY_DEV PieceWalk(const PagedAttnParams& p, const long long* prefix)
+      : line(prefix[p.rb.batch], gridDim.x, p.min_blocks) {
     const int cta = blockIdx.x;
     left = 0;
     if (cta >= line.n) return;
-    const long long w0 = line.start(cta);
-    left = line.start(cta + 1) - w0;
-    w.seek(p.rb, p.kv, p.g, prefix, w0);
+    at = line.start(cta);
+    left = line.start(cta + 1) - at;
+    w.seek(p.rb, p.kv, p.g, prefix, at);
   }
-  HY_DEV bool next(const PagedAttnParams& p, Piece* o) {
-    if (left <= 0) return false;
-    if (!first && !w.advance(p.rb, p.kv, p.g)) return false;
+  // `writer`: the one thread of the CTA that records what it leaves unfinished
+  HY_DEV bool next(const PagedAttnParams& p, Piece* o, bool writer) {
+    if (left <= 0 || (!first && !w.advance(p.rb, p.kv, p.g))) {
+      if (writer && first) p.cut[blockIdx.x] = {0, 0, 0, 0};
+      return false;
+    }
     first = false;
     o->ts = tile_span(p.g, w.s, w.t);
     o->b = w.b;
@@ -235,8 +260,42 @@ struct PieceWalk {
     o->blk1 = static_cast<int>(min(static_cast<long long>(o->ts.n), w.off + left));
     o->whole = o->blk0 == 0 && o->blk1 == o->ts.n;
     left -= o->blk1 - o->blk0;
+    at += o->blk1 - o->blk0;
+    if (writer && left <= 0) {
+      CutRecord c = {o->row0, 0, o->kvh, 0};
+      if (o->blk0 == 0 && !o->whole) {
+        c.toks = o->ts.toks;
+        c.last = line.owner(at + (o->ts.n - o->blk1) - 1);
+      }
+      p.cut[blockIdx.x] = c;
+    }
     return true;
   }
 };
+
+// The same prefix by a CTA itself, for a small batch: one warp a sequence.  cnt: shared,
+// [batch + 1]; every thread of the CTA calls it.  `keep`: also written to p.prefix and what does
+// not fit recorded (one CTA of the launch).
+HY_DEV void plan_by_warps(const PagedAttnParams& p, long long* cnt, bool keep) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int b = warp; b < p.rb.batch; b += blockDim.x >> 5) {
+    Seq s;
+    long long c = 0;
+    if (load_seq(p.rb, p.kv, b, &s)) c = seq_blocks(p.g, s) * p.kv.hkv;
+    else if (keep && lane == 0) report_invalid(p.status);
+    if (lane == 0) cnt[b] = c;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    long long sum = 0;
+    for (int b = 0; b < p.rb.batch; ++b) {
+      const long long c = cnt[b];
+      cnt[b] = sum;
+      sum += c;
+    }
+    cnt[p.rb.batch] = sum;
+  }
+  __syncthreads();
+}
 
 }  // namespace hy
