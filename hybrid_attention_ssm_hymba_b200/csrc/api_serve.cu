@@ -80,7 +80,7 @@ hymba_status_t check_attention(const hymba_paged_kv_t* kv, int batch, int total_
     return HYMBA_ERR_INVALID_ARG;
   if (dtype == HYMBA_BF16 ? (kv->head_dim != 128 || n_q_heads / kv->n_kv_heads > 128) : kv->head_dim > 128)
     return HYMBA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(n_q_heads) * kv->head_dim > (1 << 20) ||
+  if (static_cast<long long>(n_q_heads) * kv->head_dim > (1 << 19) ||
       static_cast<long long>(total_rows) * n_q_heads > (1ll << 31) - 1)
     return HYMBA_ERR_UNSUPPORTED;
   return HYMBA_OK;

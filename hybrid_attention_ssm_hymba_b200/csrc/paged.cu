@@ -171,65 +171,200 @@ cudaError_t launch_copy(const PagedKv& kv, const RaggedBatch& rb, void* k, void*
               : launch_copy_t<float, float, WRITE>(kv, rb, k, v, ld, status, st);
 }
 
-// Attention, one warp per (new row, query head): online softmax in fp32 over the visible
-// keys (meta rows below the window, then the window up to the row itself).
-template <typename T, typename C>
-__global__ void __launch_bounds__(128) paged_attn_simt(const PagedAttnDesc p, float scale) {
+// Attention in fp32 on the CUDA cores: a CTA of four warps per (new row, K/V head, up to eight of
+// its query heads).  A warp takes 32 of the visible keys (meta rows below the window, then the
+// window up to the row itself) at a time: lane = key for the scores (its K row against the queries
+// in shared memory), lane = dims for P V (whole V rows, eight in flight); online softmax, the warps
+// joined at the end.  Fp32 products have no tensor-core form that keeps their 24 bits; what bounds
+// this kernel is its FMAs and the re-reading of K and V by every row (L2).  With few rows the keys
+// of a row are split over `splits` CTAs, each leaving its unnormalised output, m and sum per head
+// in part[(row * Hq + head) * splits + split][dh + 2]; paged_join_simt joins them.
+constexpr int kSimtWarps = 4, kSimtHeads = 8, kSimtDh = 128;
+
+template <typename C>
+__global__ void __launch_bounds__(32 * kSimtWarps) paged_attn_simt(const PagedAttnDesc p, float scale_log2, int splits) {
+  constexpr bool kScaled = sizeof(C) == 1;
+  __shared__ __align__(16) float sq[kSimtHeads][kSimtDh];
+  __shared__ float s_m[kSimtWarps][kSimtHeads], s_l[kSimtWarps][kSimtHeads];
+  __shared__ float s_o[kSimtWarps][kSimtHeads][kSimtDh];
   pdl_trigger();
   pdl_wait();
   const PagedKv& kv = p.kv;
-  const long long wid = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31, dh = kv.dh;
-  if (blockIdx.x == 0) check_batch(p.rb, kv, p.status);
-  if (wid >= static_cast<long long>(p.rb.total_rows) * p.n_q_heads) return;
-  const int r = static_cast<int>(wid / p.n_q_heads), h = static_cast<int>(wid % p.n_q_heads);
-  const int kvh = h / (p.n_q_heads / kv.hkv);
+  const int r = blockIdx.x, kvh = blockIdx.y, group = p.n_q_heads / kv.hkv, dh = kv.dh;
+  const int hz = blockIdx.z / splits, split = blockIdx.z - hz * splits;
+  const int h0 = kvh * group + hz * kSimtHeads, heads = min(kSimtHeads, group - hz * kSimtHeads);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) check_batch(p.rb, kv, p.status);
   const int b = seq_of_row(p.rb, r);
   if (b < 0) return;
   Seq s;
   if (!load_seq(p.rb, kv, b, &s) || r < s.q0 || r >= s.q0 + s.n) return;
   const int i = s.len - s.n + (r - s.q0);
-  float qv[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
-  const T* q = static_cast<const T*>(p.q) + r * p.q_ld + h * dh;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) qv[e] = lane + 32 * e < dh ? to_f<T>(q[lane + 32 * e]) : 0.f;
+  const float* q = static_cast<const float*>(p.q) + r * p.q_ld + static_cast<long long>(h0) * dh;
+  for (int x = threadIdx.x; x < heads * dh; x += 32 * kSimtWarps) sq[x / dh][x % dh] = q[x];
+  __syncthreads();
   const int w_lo = p.window < 0 ? 0 : max(0, i - p.window), m_cnt = min(p.n_meta, w_lo);
-  const int n = m_cnt + (i - w_lo + 1);
+  const int all = m_cnt + (i - w_lo + 1);
+  // this CTA's keys: a multiple of 128 of them each
+  const int per = ((all + splits - 1) / splits + 127) / 128 * 128, first = min(all, split * per), n = min(all, first + per);
   const C* pages = static_cast<const C*>(kv.pages);
-  float m = -INFINITY, l = 0.f;
-  for (int x = 0; x < n; ++x) {
-    const int j = x < m_cnt ? x : w_lo + (x - m_cnt);
-    const int page = page_of(kv, b, j), row = j % kv.page_size;
-    if (page < 0) {
-      if (lane == 0) report_invalid(p.status);
-      continue;
-    }
-    const C* k = pages + page_elem(kv, 0, page, row, kvh);
-    const C* v = pages + page_elem(kv, 1, page, row, kvh);
-    float sk = 1.f, sv = 1.f;
-    if (kv.type == CACHE_E4M3) {
-      sk = kv.scales[page_scale(kv, 0, page, row, kvh)];
-      sv = kv.scales[page_scale(kv, 1, page, row, kvh)];
-    }
-    float t = 0.f;
+  const long long half = static_cast<long long>(kv.n_pages) * kv.page_size * kv.hkv;   // rows x heads of K
+  float m[kSimtHeads], l[kSimtHeads], o[kSimtHeads][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (lane + 32 * e < dh) t = fmaf(qv[e], static_cast<float>(k[lane + 32 * e]), t);
+  for (int g = 0; g < kSimtHeads; ++g) {
+    m[g] = -INFINITY;
+    l[g] = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    t *= scale * sk;
-    const float mn = fmaxf(m, t);
-    const float corr = expf(m - mn), pj = expf(t - mn);
-    l = l * corr + pj;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (lane + 32 * e < dh) acc[e] = acc[e] * corr + pj * sv * static_cast<float>(v[lane + 32 * e]);
-    m = mn;
+    for (int e = 0; e < 4; ++e) o[g][e] = 0.f;
   }
-  T* out = static_cast<T*>(p.out) + r * p.out_ld + h * dh;
+  for (int c0 = first + warp * 32; c0 < n; c0 += 32 * kSimtWarps) {
+    const int x = c0 + lane, j = x < m_cnt ? x : w_lo + (x - m_cnt);
+    long long at = -1;   // the key's row x head of the pool, -1: none
+    float sk = 1.f, sv = 1.f;
+    if (x < n) {
+      const int page = page_of(kv, b, j);
+      if (page < 0) {
+        report_invalid(p.status);
+      } else {
+        const int row = j % kv.page_size;
+        at = (static_cast<long long>(page) * kv.page_size + row) * kv.hkv + kvh;
+        if (kScaled) {
+          sk = kv.scales[page_scale(kv, 0, page, row, kvh)];
+          sv = kv.scales[page_scale(kv, 1, page, row, kvh)];
+        }
+      }
+    }
+    float t[kSimtHeads];
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (lane + 32 * e < dh) out[lane + 32 * e] = from_f<T>(l != 0.f ? acc[e] / l : 0.f);
+    for (int g = 0; g < kSimtHeads; ++g) t[g] = 0.f;
+    if (at >= 0) {
+      for (int d = 0; d < dh; d += 16) {
+        Vec8<C> v[2];
+        v[0].load(pages + at * dh + d);
+        v[1].load(pages + at * dh + d + 8);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float f[8];
+          v[u].to_f32(f);
+#pragma unroll
+          for (int g = 0; g < kSimtHeads; ++g) {
+            if (g >= heads) break;
+            const float4 a = *reinterpret_cast<const float4*>(&sq[g][d + 8 * u]), c = *reinterpret_cast<const float4*>(&sq[g][d + 8 * u + 4]);
+            t[g] = fmaf(a.x, f[0], fmaf(a.y, f[1], fmaf(a.z, f[2], fmaf(a.w, f[3], t[g]))));
+            t[g] = fmaf(c.x, f[4], fmaf(c.y, f[5], fmaf(c.z, f[6], fmaf(c.w, f[7], t[g]))));
+          }
+        }
+      }
+    }
+    float pr[kSimtHeads];
+#pragma unroll
+    for (int g = 0; g < kSimtHeads; ++g) {
+      pr[g] = 0.f;
+      if (g >= heads) break;
+      const float v = at >= 0 ? t[g] * sk * scale_log2 : -INFINITY;
+      float mx = v;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      const float mn = fmaxf(m[g], mx);
+      if (mn == -INFINITY) continue;   // no key so far
+      const float corr = exp2f(m[g] - mn), e = exp2f(v - mn);
+      float sum = e;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      l[g] = fmaf(l[g], corr, sum);
+      m[g] = mn;
+      pr[g] = at >= 0 ? e * sv : 0.f;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) o[g][d] *= corr;
+    }
+    const int nk = min(32, n - c0);
+    for (int k0 = 0; k0 < nk; k0 += 8) {
+      float vf[8][4];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const long long row = __shfl_sync(0xffffffffu, at, k0 + u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          vf[u][e] = row >= 0 && lane + 32 * e < dh ? static_cast<float>(pages[(half + row) * dh + lane + 32 * e]) : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int g = 0; g < kSimtHeads; ++g) {
+          if (g >= heads) break;
+          const float w = __shfl_sync(0xffffffffu, pr[g], k0 + u);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[g][e] = fmaf(w, vf[u][e], o[g][e]);
+        }
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < kSimtHeads; ++g) {
+    if (g >= heads) break;
+    if (lane == 0) {
+      s_m[warp][g] = m[g];
+      s_l[warp][g] = l[g];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (lane + 32 * e < dh) s_o[warp][g][lane + 32 * e] = o[g][e];
+  }
+  __syncthreads();
+  float* out = static_cast<float*>(p.out) + r * p.out_ld + static_cast<long long>(h0) * dh;
+  for (int x = threadIdx.x; x < heads * dh; x += 32 * kSimtWarps) {
+    const int g = x / dh, d = x - g * dh;
+    float mm = -INFINITY, ll = 0.f, oo = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSimtWarps; ++w) mm = fmaxf(mm, s_m[w][g]);
+#pragma unroll
+    for (int w = 0; w < kSimtWarps; ++w) {
+      const float f = s_m[w][g] == -INFINITY ? 0.f : exp2f(s_m[w][g] - mm);
+      ll = fmaf(s_l[w][g], f, ll);
+      oo = fmaf(s_o[w][g][d], f, oo);
+    }
+    if (splits == 1) {
+      out[x] = ll != 0.f ? oo / ll : 0.f;
+    } else {
+      float* part = static_cast<float*>(p.scratch) +
+                    ((static_cast<long long>(r) * p.n_q_heads + h0 + g) * splits + split) * (dh + 2);
+      part[d] = oo;
+      if (d == 0) {
+        part[dh] = mm;
+        part[dh + 1] = ll;
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(128) paged_join_simt(const PagedAttnDesc p, int splits) {
+  pdl_trigger();
+  pdl_wait();
+  const int r = blockIdx.x, h = blockIdx.y, dh = p.kv.dh, b = seq_of_row(p.rb, r);
+  Seq s;
+  if (b < 0 || !load_seq(p.rb, p.kv, b, &s) || r < s.q0 || r >= s.q0 + s.n) return;   // (left as it was)
+  const float* part = static_cast<const float*>(p.scratch) + (static_cast<long long>(r) * p.n_q_heads + h) * splits * (dh + 2);
+  float mm = -INFINITY;
+  for (int c = 0; c < splits; ++c) mm = fmaxf(mm, part[c * (dh + 2) + dh]);
+  for (int d = threadIdx.x; d < dh; d += 128) {
+    float ll = 0.f, oo = 0.f;
+    for (int c = 0; c < splits; ++c) {
+      const float* q = part + c * (dh + 2);
+      const float f = q[dh] == -INFINITY ? 0.f : exp2f(q[dh] - mm);
+      ll = fmaf(q[dh + 1], f, ll);
+      oo = fmaf(q[d], f, oo);
+    }
+    static_cast<float*>(p.out)[r * p.out_ld + static_cast<long long>(h) * dh + d] = ll != 0.f ? oo / ll : 0.f;
+  }
+}
+
+// CTAs over which the keys of a row are split: four CTAs per SM of the B200 in all, and no piece
+// shorter than the cache's longest sequence allows.
+int simt_splits(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads) {
+  const long long ctas = static_cast<long long>(rb.total_rows) * kv.hkv * ((n_q_heads / kv.hkv + kSimtHeads - 1) / kSimtHeads);
+  const long long most = (static_cast<long long>(kv.table_ld) * kv.page_size + 127) / 128;
+  long long s = ctas > 0 ? 4 * 148 / ctas : 1;
+  s = s < most ? s : most;
+  return s < 1 ? 1 : s > 64 ? 64 : static_cast<int>(s);
 }
 
 }  // namespace
@@ -252,18 +387,23 @@ size_t paged_attention_tc_scratch(const PagedKv& kv, const RaggedBatch& rb, int 
 cudaError_t launch_paged_attention_tc(const PagedAttnDesc& a, cudaStream_t st);
 
 size_t paged_attention_scratch(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads, bool bf16) {
-  if (!bf16) return 0;
+  if (!bf16) {
+    const int s = simt_splits(kv, rb, n_q_heads);
+    return s == 1 ? 0 : static_cast<size_t>(rb.total_rows) * n_q_heads * s * (kv.dh + 2) * 4;
+  }
   return paged_decode_takes(kv, rb, n_q_heads) ? paged_decode_scratch(kv, rb, n_q_heads) : paged_attention_tc_scratch(kv, rb, n_q_heads);
 }
 
 cudaError_t launch_paged_attention(const PagedAttnDesc& a, cudaStream_t st) {
   if (a.bf16) return paged_decode_takes(a.kv, a.rb, a.n_q_heads) ? launch_paged_decode(a, st) : launch_paged_attention_tc(a, st);
-  const long long warps = static_cast<long long>(a.rb.total_rows) * a.n_q_heads;
-  if (warps <= 0) return cudaSuccess;
-  const dim3 grid(static_cast<unsigned>((warps + 3) / 4));
-  const float scale = 1.f / sqrtf(static_cast<float>(a.kv.dh));
-  return a.kv.type == CACHE_E4M3 ? launch(paged_attn_simt<float, __nv_fp8_e4m3>, grid, dim3(128), 0, st, a, scale)
-                                 : launch(paged_attn_simt<float, float>, grid, dim3(128), 0, st, a, scale);
+  const int group = a.n_q_heads / a.kv.hkv, splits = simt_splits(a.kv, a.rb, a.n_q_heads);
+  const dim3 grid(a.rb.total_rows, a.kv.hkv, (group + kSimtHeads - 1) / kSimtHeads * splits);
+  const float scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(a.kv.dh));
+  const cudaError_t e =
+      a.kv.type == CACHE_E4M3 ? launch(paged_attn_simt<__nv_fp8_e4m3>, grid, dim3(32 * kSimtWarps), 0, st, a, scale_log2, splits)
+                              : launch(paged_attn_simt<float>, grid, dim3(32 * kSimtWarps), 0, st, a, scale_log2, splits);
+  if (e != cudaSuccess || splits == 1) return e;
+  return launch(paged_join_simt, dim3(a.rb.total_rows, a.n_q_heads), dim3(128), 0, st, a, splits);
 }
 
 }  // namespace hy
