@@ -114,7 +114,7 @@ struct GemmW4Params {
 
 template <int NT> struct W4Shape {
   static constexpr int ring = NT <= 2 ? 3 : 2;
-  static constexpr int slab = NT == 1 ? 4096 : NT <= 3 ? 1024 : 512;
+  static constexpr int slab = NT == 1 ? 4096 : NT == 2 ? 2048 : NT == 3 ? 1024 : 512;
   static constexpr int x_bytes = slab / 32 * NT * 8 * 64;
   static constexpr int stage = 16 * kRowPitch + 16 * 8 * 4;      // codes, then scales [row][8]
   static constexpr int red_bytes = kWarps * 16 * 8 * NT * 4;
