@@ -16,12 +16,14 @@
 //   warps 2..9  softmax of group a, warps 10..17 of group b: two threads per row, each over 64
 //               of the block's keys and 64 of O's columns
 //   warps 18, 19 (e4m3 cache only) turn the 8-bit K and V of a block into the fp16 tiles the
-//               tensor core reads.  An e4m3 code is exact in fp16 (one conversion for two, where
-//               bf16 takes ten instructions: two warps could not keep up), so the row scales stay
-//               out of the products: the softmax threads multiply S's columns by K's and P's by
-//               V's.  Powers of two keep fp16's range: a row of Q is scaled to at most 2^8, V's
-//               scales to at most 2^10 of the largest that the tile has met, and P stays below
-//               2^4, so a product keeps 11 bits down to 2^-24 of the largest and 8 to 2^-27.
+//               tensor core reads.  An e4m3 code is exact in fp16.  V: code times scale is rounded
+//               once to fp16's 11 bits (2^-12, where the output's own rounding is 2^-8).  K: a
+//               score of hundreds would lose too much that way, so K is the code times the power
+//               of two in its scale, exactly, and the softmax threads multiply S's columns by the
+//               scale's mantissa.  Powers of two, the same for all rows of a tile, keep fp16's
+//               range: scales are held below 2^7 of the largest that the tile has met, a row of Q
+//               is scaled to at most 2^8, and P to at most 2^15; each keeps 11 bits down to 2^-25
+//               and more below its largest value.
 // TMEM (512 columns): S_a | S_b | O_a | O_b; P in bf16 over the consumed S columns.
 //
 // Rows of V that no query of the tile sees (behind the sequence, between the meta rows and
@@ -38,7 +40,8 @@ constexpr int DH = 128, TILE_BYTES = 128 * DH * 2, HALF = 128 * 64 * 2;
 constexpr uint32_t kFmtBits = (1u << 7) | (1u << 10);
 template <bool FP8> constexpr uint32_t IDESC_QK = idesc_bf16(128, 128, false, false) & ~(FP8 ? kFmtBits : 0u);
 template <bool FP8> constexpr uint32_t IDESC_PV = idesc_bf16(128, DH, false, true) & ~(FP8 ? kFmtBits : 0u);
-constexpr int kUp = 10;   // FP8: V's scales are at most 2^kUp
+constexpr int kUp = 7;         // FP8: K's and V's scales are held below 2^kUp, code times scale below 2^16
+constexpr float kPUp = 11.f;   // FP8: P is 2^(s - m + kPUp)
 
 // What the producer tells the softmax threads of each tile (they give the slot back) and of
 // each key block (it is at most four blocks ahead of them: a ring of 8 needs no giving back).
@@ -53,8 +56,7 @@ struct TileInfo {
 struct BlockInfo {
   int k0;
   uint32_t flags;     // bit x: group x masks; bit 2: some rows of V are to be zeroed
-  int e;              // FP8: V's scales are held times 2^(kUp - e)
-  uint32_t pad;
+  int ek, ev;         // FP8: K's and V's scales are held times 2^(kUp - ek), 2^(kUp - ev)
   uint32_t valid[4];  // rows whose page number is valid, one bit each
 };
 constexpr uint32_t kZeroV = 4u;
@@ -77,8 +79,10 @@ template <> struct Smem<false> {   // behind the six tiles
 // through a ring of four blocks (the producer is at most three blocks ahead of the softmax).
 constexpr int kRawStages = 3, kRawBytes = 64 * DH, kScaleSlots = 4;
 template <> struct Smem<true> : Smem<false> {
-  uint64_t raw_full[kRawStages], raw_empty[kRawStages], scale_full[kScaleSlots], q_ready[2];
-  alignas(16) float scale[kScaleSlots][2][128];   // [slot][K, V][row]
+  uint64_t raw_full[kRawStages], raw_empty[kRawStages], scale_full[kScaleSlots], scale_ready[kScaleSlots], q_ready[2];
+  // As copied: K's and V's scales [slot][K, V][row].  As used: the mantissa of K's scale in [1, 2),
+  // and (fp16 pair) V's scale and the power of two of K's, in fp16's range.
+  alignas(16) float scale[kScaleSlots][2][128];
 };
 template <bool FP8> constexpr int smem_bytes() {
   return 6 * TILE_BYTES + 1024 + (FP8 ? kRawStages * kRawBytes : 0) + static_cast<int>(sizeof(Smem<FP8>));
@@ -103,11 +107,13 @@ __device__ __forceinline__ float row_max64(const uint32_t (&sv)[64]) {
     for (int i = 0; i < 8; ++i) m[i] = max3f(m[i], __uint_as_float(sv[e + i]), __uint_as_float(sv[e + 8 + i]));
   return max3f(max3f(m[0], m[1], m[2]), max3f(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
 }
-// f[2q], f[2q + 1] times a shared vector (the same for every row): 64 values.
+// 64 values times a shared vector, the same for every row.
 __device__ __forceinline__ void scale64(uint32_t (&sv)[64], uint32_t vec) {
+  float4 next = lds_f4(vec);   // one load ahead: shared memory is busy with the tensor core's operands
 #pragma unroll
   for (int q = 0; q < 16; ++q) {
-    const float4 k = lds_f4(vec + 16 * q);
+    const float4 k = next;
+    if (q < 15) next = lds_f4(vec + 16 * q + 16);
     const float2 a = __fmul2_rn(make_float2(__uint_as_float(sv[4 * q]), __uint_as_float(sv[4 * q + 1])), make_float2(k.x, k.y));
     const float2 b = __fmul2_rn(make_float2(__uint_as_float(sv[4 * q + 2]), __uint_as_float(sv[4 * q + 3])), make_float2(k.z, k.w));
     sv[4 * q] = __float_as_uint(a.x);
@@ -115,28 +121,6 @@ __device__ __forceinline__ void scale64(uint32_t (&sv)[64], uint32_t vec) {
     sv[4 * q + 2] = __float_as_uint(b.x);
     sv[4 * q + 3] = __float_as_uint(b.y);
   }
-}
-// row_exp64 with P's columns times V's scales before their rounding to fp16 (the sum is without
-// them).
-__device__ __forceinline__ float row_exp64_scaled(uint32_t (&sv)[64], float scale_log2, float m_ref, uint32_t vec) {
-  const float2 sc = make_float2(scale_log2, scale_log2), nm = make_float2(-m_ref, -m_ref);
-  float2 acc[2];
-  acc[0] = acc[1] = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int q = 0; q < 16; ++q) {
-    const float4 k = lds_f4(vec + 16 * q);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[4 * q + 2 * h]), __uint_as_float(sv[4 * q + 2 * h + 1])), sc, nm);
-      const float2 pq = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-      acc[h] = __fadd2_rn(acc[h], pq);
-      const float2 w = __fmul2_rn(pq, h ? make_float2(k.z, k.w) : make_float2(k.x, k.y));
-      const __half2 r = __floats2half2_rn(w.x, w.y);
-      sv[2 * q + h] = *reinterpret_cast<const uint32_t*>(&r);
-    }
-  }
-  const float2 t = __fadd2_rn(acc[0], acc[1]);
-  return t.x + t.y;
 }
 // Two e4m3 codes (the low or the high half of u) as fp16.
 __device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t u, int half) {
@@ -146,8 +130,9 @@ __device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t u, int half) {
   return v;
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
-// P = 2^(S scale - m_ref), packed in place as bf16 pairs (sv[q] <- p[2q], p[2q + 1]); returns
-// the sum of the fp32 values.  P is rounded to bf16 once, as the P V operand.
+// P = 2^(S scale - m_ref), packed in place as pairs of bf16 or fp16 (sv[q] <- p[2q], p[2q + 1]);
+// returns the sum of the fp32 values.  P is rounded once, as the P V operand.
+template <bool F16>
 __device__ __forceinline__ float row_exp64(uint32_t (&sv)[64], float scale_log2, float m_ref) {
   const float2 sc = make_float2(scale_log2, scale_log2), nm = make_float2(-m_ref, -m_ref);
   float2 acc[4];
@@ -158,7 +143,12 @@ __device__ __forceinline__ float row_exp64(uint32_t (&sv)[64], float scale_log2,
     const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[2 * q]), __uint_as_float(sv[2 * q + 1])), sc, nm);
     const float2 pq = make_float2(ex2_approx(x.x), ex2_approx(x.y));
     acc[q & 3] = __fadd2_rn(acc[q & 3], pq);
-    sv[q] = pack_bf16(pq.x, pq.y);
+    if (F16) {
+      const __half2 r = __floats2half2_rn(pq.x, pq.y);
+      sv[q] = *reinterpret_cast<const uint32_t*>(&r);
+    } else {
+      sv[q] = pack_bf16(pq.x, pq.y);
+    }
   }
   const float2 t = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
   return t.x + t.y;
@@ -203,7 +193,10 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
         mbar_init(&sm.raw_full[s], 1);
         mbar_init(&sm.raw_empty[s], 64);
       }
-      for (int s = 0; s < kScaleSlots; ++s) mbar_init(&sm.scale_full[s], 1);
+      for (int s = 0; s < kScaleSlots; ++s) {
+        mbar_init(&sm.scale_full[s], 1);
+        mbar_init(&sm.scale_ready[s], 1);
+      }
       for (int s = 0; s < 2; ++s) mbar_init(&sm.q_ready[s], 8);
     }
     *abort_flag = 0;
@@ -458,67 +451,93 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
                                                abort_flag));
         if (!ok || ti.toks == 0) break;
         const int n = ti.n, p1 = ti.p1, lo = p.g.window < 0 ? 0 : ti.p0 - p.g.window;
-        uint32_t most = 0;   // the largest of V's scales so far, as bits
+        uint32_t most[2] = {0, 0};   // the largest of K's and of V's scales so far, as bits
         for (int j = 0; ok && j < n; ++j, ++jb) {
-          const uint32_t s = jb & 1, par = (jb >> 1) & 1;
+          const uint32_t s = jb & 1, par = (jb >> 1) & 1, slot = jb % kScaleSlots, slot_par = (jb / kScaleSlots) & 1;
+          BlockInfo& bi = sm.block[jb & (kBlockSlots - 1)];
+          if (warp == 18) {
+            // the scales as fp16 pairs in fp16's range, 0 for rows that no query of the tile sees.
+            // Done before k_full, so that S of the block implies it.
+            ok = __all_sync(0xffffffffu, mbar_wait(&sm.scale_full[slot], slot_par, p.status, abort_flag));
+            if (!ok) break;
+            const uint32_t valid = bi.valid[lane >> 3] >> ((lane & 7) * 4);
+            const int key0 = bi.k0 + lane * 4;
+            uint32_t seen = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (((valid >> e) & 1u) && key0 + e <= p1 && (key0 + e >= lo || key0 + e < p.g.n_meta)) seen |= 1u << e;
+            float4& k4 = *reinterpret_cast<float4*>(&sm.scale[slot][0][lane * 4]);
+            float4& v4 = *reinterpret_cast<float4*>(&sm.scale[slot][1][lane * 4]);
+            float k[4] = {k4.x, k4.y, k4.z, k4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w}, up[2];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (!((seen >> e) & 1u)) k[e] = v[e] = 0.f;
+              most[0] = max(most[0], __float_as_uint(k[e]) & 0x7fffffffu);
+              most[1] = max(most[1], __float_as_uint(v[e]) & 0x7fffffffu);
+            }
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              most[w] = __reduce_max_sync(0xffffffffu, most[w]);
+              const int ex = max(static_cast<int>(most[w] >> 23) - 126, kUp - 127);   // every scale is below 2^ex
+              up[w] = pow2(kUp - ex);
+              if (lane == 0) (w ? bi.ev : bi.ek) = ex;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t kb = __float_as_uint(k[e]);
+              const __half2 h = __floats2half2_rn(v[e] * up[1], __uint_as_float(kb & 0x7f800000u) * up[0]);
+              v[e] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h));
+              k[e] = __uint_as_float((kb & 0x7fffffu) | 0x3f800000u);
+            }
+            k4 = make_float4(k[0], k[1], k[2], k[3]);
+            v4 = make_float4(v[0], v[1], v[2], v[3]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.scale_ready[slot]);
+          }
+          ok = __all_sync(0xffffffffu, mbar_wait(&sm.scale_ready[slot], slot_par, p.status, abort_flag));
 #pragma unroll 1
-          for (int u = 0; u < 4; ++u, ++raw) {
+          for (int u = 0; ok && u < 4; ++u, ++raw) {
             const uint32_t rs = raw % kRawStages;
             if ((u & 1) == 0)
               ok = __all_sync(0xffffffffu, mbar_wait(u ? &sm.v_empty[s] : &sm.k_empty[s], par ^ 1u, p.status, abort_flag));
             ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.raw_full[rs], (raw / kRawStages) & 1, p.status, abort_flag));
-            BlockInfo& bi = sm.block[jb & (kBlockSlots - 1)];
-            if (u == 0 && warp == 18 && ok) {
-              // V's scales: 0 for rows that no query of the tile sees, the others brought to fp16's
-              // range.  Done before k_full, so that S of the block implies it.
-              ok = __all_sync(0xffffffffu, mbar_wait(&sm.scale_full[jb % kScaleSlots], (jb / kScaleSlots) & 1, p.status, abort_flag));
-              float4& v4 = *reinterpret_cast<float4*>(&sm.scale[jb % kScaleSlots][1][lane * 4]);
-              float v[4] = {v4.x, v4.y, v4.z, v4.w};
-              const uint32_t valid = bi.valid[lane >> 3] >> ((lane & 7) * 4);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int key = bi.k0 + lane * 4 + e;
-                if (!((valid >> e) & 1u) || key > p1 || (key < lo && key >= p.g.n_meta)) v[e] = 0.f;
-                most = max(most, __float_as_uint(v[e]) & 0x7fffffffu);
-              }
-              most = __reduce_max_sync(0xffffffffu, most);
-              const int ex = max(static_cast<int>(most >> 23) - 126, kUp - 127);   // every scale is below 2^ex
-              const float f = pow2(kUp - ex);
-              v4 = make_float4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
-              if (lane == 0) bi.e = ex;
-              __syncwarp();
-            }
             if (!ok) break;
-            const uint32_t src = smem_u32(sRaw + rs * kRawBytes) + t * 16;
-            const uint32_t dst = smem_u32((u < 2 ? sK : sV) + s * TILE_BYTES + ((t & 4) ? HALF : 0));
+            // 16 codes (one of a row's eight chunks) at a time, to two 16-byte chunks of the swizzled
+            // tile.  The lanes of a row's upper half take the neighbouring row, so that eight lanes
+            // meet no bank twice in either tile.
+            const int up = (t >> 2) & 1, row0 = (t >> 3) ^ up, c = (t & 3) * 2;
+            const uint32_t src = smem_u32(sRaw + rs * kRawBytes) + row0 * DH + (t & 7) * 16;
+            const uint32_t dst = smem_u32((u < 2 ? sK : sV) + s * TILE_BYTES + up * HALF + ((u & 1) * 64 + row0) * 128);
+            const uint32_t fs = smem_u32(&sm.scale[slot][1][(u & 1) * 64 + row0]);
+            const uint32_t at0 = dst + ((c ^ row0) << 4), at1 = dst + (((c + 1) ^ row0) << 4);   // row & 7 = row0
             const bool hide = u >= 2 && (bi.flags & kZeroV);
-            const int k0 = bi.k0;
-            // 16 codes (one of a row's eight chunks) at a time, to two 16-byte chunks of the
-            // swizzled tile; the four lanes of the upper half store theirs in the other order,
-            // so that the eight lanes of a row meet no bank twice
-            const int c = (t & 3) * 2, flip = (t >> 2) & 1;
+            const int key0 = bi.k0 + (u & 1) * 64 + row0;
             float4 r4[8];   // all in flight before the first is used
+            uint32_t f[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) r4[i] = lds_f4(src + i * 1024);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = __byte_perm(lds_u32(fs + i * 32), 0u, u < 2 ? 0x3232 : 0x1010);
             if (hide) {   // rows of V that no query of the tile sees (they may hold NaN codes)
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const int key = k0 + (u & 1) * 64 + i * 8 + (t >> 3);
+                const int key = key0 + i * 8;
                 if (key > p1 || (key < lo && key >= p.g.n_meta)) r4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
               }
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const int row = (u & 1) * 64 + i * 8 + (t >> 3);
               const uint32_t w[4] = {__float_as_uint(r4[i].x), __float_as_uint(r4[i].y), __float_as_uint(r4[i].z),
                                      __float_as_uint(r4[i].w)};
               uint32_t h[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) h[e] = f16_of_e4m3(w[e >> 1], e & 1);
-              const uint32_t at = dst + row * 128, sw = row & 7;
-              const uint32_t a0 = at + (((c + flip) ^ sw) << 4), a1 = at + (((c + (flip ^ 1)) ^ sw) << 4);
-              sts_u32x4(a0, flip ? h[4] : h[0], flip ? h[5] : h[1], flip ? h[6] : h[2], flip ? h[7] : h[3]);
-              sts_u32x4(a1, flip ? h[0] : h[4], flip ? h[1] : h[5], flip ? h[2] : h[6], flip ? h[3] : h[7]);
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t x = f16_of_e4m3(w[e >> 1], e & 1);
+                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&f[i]));
+                h[e] = *reinterpret_cast<const uint32_t*>(&y);
+              }
+              sts_u32x4(at0 + i * 1024, h[0], h[1], h[2], h[3]);
+              sts_u32x4(at1 + i * 1024, h[4], h[5], h[6], h[7]);
             }
             fence_proxy_async_smem();
             // only now: an arrival right behind the loads can overtake them, and the next copy would
@@ -594,18 +613,16 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
       for (int j = 0; j < n; ++j, ++jb, ++cnt) {
         ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.s_full[x], cnt & 1, p.status, abort_flag));
         uint32_t sv[64];
-        float m_half = -INFINITY;
+        float m_half = -INFINITY, to_block = to_log2;   // from this block's S to log2 units
         const volatile BlockInfo& bi = sm.block[jb & (kBlockSlots - 1)];
         const uint32_t flags = bi.flags;
+        if constexpr (FP8) to_block *= pow2(bi.ek - kUp);
         if (ok) {
           tc_fence_after();
           tmem_ld32(tSx + kh * 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
           tmem_ld32(tSx + kh * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
           tmem_wait_ld();
-          if constexpr (FP8) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&sm.scale_full[jb % kScaleSlots], (jb / kScaleSlots) & 1, p.status, abort_flag));
-            scale64(sv, smem_u32(&sm.scale[jb % kScaleSlots][0][kh * 64]));
-          }
+          if constexpr (FP8) scale64(sv, smem_u32(&sm.scale[jb % kScaleSlots][0][kh * 64]));
           if (flags & (1u << x)) {
             // key e of this half is visible iff e <= hi and (e >= lo or e < me), on a valid page
             const int base = bi.k0 + kh * 64, hi = ti.p0 + rtok - base, me = p.g.n_meta - base;
@@ -618,7 +635,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
                 if (!(see & (1u << e))) sv[32 * w + e] = __float_as_uint(-INFINITY);
             }
           }
-          m_half = row_max64(sv) * to_log2;
+          m_half = row_max64(sv) * to_block;
         }
         // the row maximum over both halves; the barrier also orders this half's reads of
         // S before the other half's P stores (P of keys 64..127 lands in S columns 32..63)
@@ -634,16 +651,12 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
             alpha = ex2_approx(m_used - m_cand);  // 0 when m_used is -inf
             m_used = m_cand;
           }
-          const float m_ref = (m_used == -INFINITY) ? 0.f : m_used;
-          float sum;
-          if constexpr (FP8)
-            sum = row_exp64_scaled(sv, to_log2, m_ref, smem_u32(&sm.scale[jb % kScaleSlots][1][kh * 64]));
-          else
-            sum = row_exp64(sv, to_log2, m_ref);
+          const float m_ref = (m_used == -INFINITY) ? 0.f : (FP8 ? m_used - kPUp : m_used);
+          const float sum = row_exp64<FP8>(sv, to_block, m_ref);
           float alpha_o = alpha;
           bool moved = need;
           if constexpr (FP8) {
-            const int e = bi.e;
+            const int e = bi.ev;
             moved |= e != e_used;
             alpha_o *= pow2(e_used - e);
             e_used = e;
@@ -700,7 +713,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
                               (ti.kvh * p.g.G + r % p.g.G) * DH + kh * 64;
         const long long prow = (static_cast<long long>(blockIdx.x) * 2 + ti.part) * p.part_rows + x * 128 + r;
         float* part = p.part + prow * DH + kh * 64;
-        if (!whole && kh == 0) p.part_ml[prow] = make_float2(m_used, lsum);
+        if (!whole && kh == 0) p.part_ml[prow] = make_float2(FP8 ? m_used - kPUp : m_used, lsum);
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t o[16];
