@@ -24,7 +24,7 @@
 //               range: scales are held below 2^7 of the largest that the tile has met, a row of Q
 //               is scaled to at most 2^8, and P to at most 2^15; each keeps 11 bits down to 2^-25
 //               and more below its largest value.
-// TMEM (512 columns): S_a | S_b | O_a | O_b; P in bf16 over the consumed S columns.
+// TMEM (512 columns): S_a | S_b | O_a | O_b; P in 16 bits over the consumed S columns.
 //
 // Rows of V that no query of the tile sees (behind the sequence, between the meta rows and
 // the window) may hold NaN, and 0 x NaN would reach every output: page pieces of such rows
@@ -42,6 +42,9 @@ template <bool FP8> constexpr uint32_t IDESC_QK = idesc_bf16(128, 128, false, fa
 template <bool FP8> constexpr uint32_t IDESC_PV = idesc_bf16(128, DH, false, true) & ~(FP8 ? kFmtBits : 0u);
 constexpr int kUp = 7;         // FP8: K's and V's scales are held below 2^kUp, code times scale below 2^16
 constexpr float kPUp = 11.f;   // FP8: P is 2^(s - m + kPUp)
+// FP8: Q and K are scaled up by at most 2^kMostUp each, so that the factor from their product to
+// log2 units stays a normal number (0 times a hidden score's -inf would be no number).
+constexpr int kMostUp = 60;
 
 // What the producer tells the softmax threads of each tile (they give the slot back) and of
 // each key block (it is at most four blocks ahead of them: a ring of 8 needs no giving back).
@@ -222,7 +225,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer (whole warp)
-    PieceWalk walk(p, prefix);
+    PieceWalk walk(p, prefix, lane == 0);
     Piece pc;
     const int npc = 128 / p.piece;   // K/V loads per block and half: lane i < npc issues piece i's
     const int none = p.kv.n_pages * p.kv.page_size;   // a row beyond the map: zeros
@@ -440,7 +443,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
       mbar_wait(&sm.mma_done, 0, nullptr, &never, 100000000ull);
     }
   } else if (FP8 && warp >= 18) {
-    // ---------------------------------------------------------------- e4m3 -> bf16 (two warps)
+    // ---------------------------------------------------------------- e4m3 -> fp16 (two warps)
     if constexpr (FP8) {
       const int t = threadIdx.x - 18 * 32;   // of 64
       uint32_t jb = 0, raw = 0;
@@ -456,7 +459,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
           const uint32_t s = jb & 1, par = (jb >> 1) & 1, slot = jb % kScaleSlots, slot_par = (jb / kScaleSlots) & 1;
           BlockInfo& bi = sm.block[jb & (kBlockSlots - 1)];
           if (warp == 18) {
-            // the scales as fp16 pairs in fp16's range, 0 for rows that no query of the tile sees.
+            // the scales as the products use them (see Smem), 0 for rows that no query of the tile sees.
             // Done before k_full, so that S of the block implies it.
             ok = __all_sync(0xffffffffu, mbar_wait(&sm.scale_full[slot], slot_par, p.status, abort_flag));
             if (!ok) break;
@@ -478,7 +481,8 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               most[w] = __reduce_max_sync(0xffffffffu, most[w]);
-              const int ex = max(static_cast<int>(most[w] >> 23) - 126, kUp - 127);   // every scale is below 2^ex
+              // every scale is below 2^ex
+              const int ex = max(static_cast<int>(most[w] >> 23) - 126, w ? kUp - 127 : kUp - kMostUp);
               up[w] = pow2(kUp - ex);
               if (lane == 0) (w ? bi.ev : bi.ek) = ex;
             }
@@ -594,7 +598,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
         sm.smax[cnt & 1][x][kh][r] = __uint_as_float(mx);
         bar_sync_n(1 + x, 256);
         mx = max(mx, __float_as_uint(sm.smax[cnt & 1][x][kh ^ 1][r]));
-        const int f = min(134 - static_cast<int>(mx >> 7), 126);
+        const int f = min(134 - static_cast<int>(mx >> 7), kMostUp);   // (a row of zeros: kMostUp)
         const float up = pow2(f);
         to_log2 *= pow2(-f);
 #pragma unroll

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) paged_decode_ker
   const uint8_t* vbase = kbase + static_cast<long long>(p.kv.n_pages) * p.kv.page_size * p.kv.hkv * DH * es;
   const long long row_bytes = static_cast<long long>(p.kv.hkv) * DH * es;
 
-  PieceWalk walk(p, prefix);
+  PieceWalk walk(p, prefix, threadIdx.x == 0);
   Piece pc;
   while (walk.next(p, &pc, threadIdx.x == 0)) {
     const int rows = pc.ts.toks * p.g.G;

@@ -4,8 +4,9 @@
 // tokens (TQ * G <= 128 rows); a tile is `groups` row groups that share every K/V block, and
 // visits 128-key blocks: those of the meta rows, then those of the window up to its last row.
 // All blocks of all tiles, in the order (sequence, K/V head, tile, block), form one line of W
-// blocks; CTA i of n takes [i W / n, (i + 1) W / n) of it.  A tile cut by such a boundary is
-// computed in parts, which a second kernel joins in the order of the CTAs.
+// blocks, of which each of n CTAs takes W / n or one more.  A tile cut by such a boundary is
+// computed in parts; the CTA that begins it records who has the others, and a second kernel joins
+// them in the order of the CTAs.
 #pragma once
 
 #include "paged.cuh"
@@ -236,21 +237,20 @@ struct PieceWalk {
   long long left, at;    // blocks left of the piece, and the place on the line
   PieceLine line;
   bool first = true;
-  HY_DEV PieceWalk(const PagedAttnParams& p, const long long* prefix)
+  // `writer`: the one thread of the CTA that records what it leaves unfinished (nothing, until
+  // its walk comes to it: a CTA that gives up leaves no record of an earlier call)
+  HY_DEV PieceWalk(const PagedAttnParams& p, const long long* prefix, bool writer)
       : line(prefix[p.rb.batch], gridDim.x, p.min_blocks) {
     const int cta = blockIdx.x;
+    if (writer) p.cut[cta] = {0, 0, 0, 0};
     left = 0;
     if (cta >= line.n) return;
     at = line.start(cta);
     left = line.start(cta + 1) - at;
     w.seek(p.rb, p.kv, p.g, prefix, at);
   }
-  // `writer`: the one thread of the CTA that records what it leaves unfinished
   HY_DEV bool next(const PagedAttnParams& p, Piece* o, bool writer) {
-    if (left <= 0 || (!first && !w.advance(p.rb, p.kv, p.g))) {
-      if (writer && first) p.cut[blockIdx.x] = {0, 0, 0, 0};
-      return false;
-    }
+    if (left <= 0 || (!first && !w.advance(p.rb, p.kv, p.g))) return false;
     first = false;
     o->ts = tile_span(p.g, w.s, w.t);
     o->b = w.b;
@@ -261,28 +261,22 @@ struct PieceWalk {
     o->whole = o->blk0 == 0 && o->blk1 == o->ts.n;
     left -= o->blk1 - o->blk0;
     at += o->blk1 - o->blk0;
-    if (writer && left <= 0) {
-      CutRecord c = {o->row0, 0, o->kvh, 0};
-      if (o->blk0 == 0 && !o->whole) {
-        c.toks = o->ts.toks;
-        c.last = line.owner(at + (o->ts.n - o->blk1) - 1);
-      }
-      p.cut[blockIdx.x] = c;
-    }
+    if (writer && left <= 0 && o->blk0 == 0 && !o->whole)
+      p.cut[blockIdx.x] = {o->row0, o->ts.toks, o->kvh, line.owner(at + (o->ts.n - o->blk1) - 1)};
     return true;
   }
 };
 
 // The same prefix by a CTA itself, for a small batch: one warp a sequence.  cnt: shared,
-// [batch + 1]; every thread of the CTA calls it.  `keep`: also written to p.prefix and what does
-// not fit recorded (one CTA of the launch).
-HY_DEV void plan_by_warps(const PagedAttnParams& p, long long* cnt, bool keep) {
+// [batch + 1]; every thread of the CTA calls it.  `report`: what does not fit is recorded (one
+// CTA of the launch).
+HY_DEV void plan_by_warps(const PagedAttnParams& p, long long* cnt, bool report) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int b = warp; b < p.rb.batch; b += blockDim.x >> 5) {
     Seq s;
     long long c = 0;
     if (load_seq(p.rb, p.kv, b, &s)) c = seq_blocks(p.g, s) * p.kv.hkv;
-    else if (keep && lane == 0) report_invalid(p.status);
+    else if (report && lane == 0) report_invalid(p.status);
     if (lane == 0) cnt[b] = c;
   }
   __syncthreads();

@@ -409,3 +409,85 @@ def test_attention_is_the_same_between_other_work(cache):
         out.zero_()
         c.attend(q, out, 16, 8, -1, ws=ws)
         assert torch.equal(out, ref), f"call {k}"
+
+
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("bf16", "e4m3"), ("f32", "e4m3")])
+@pytest.mark.parametrize("ns", [[1, 1], [40, 200]])
+def test_attention_zero_queries_and_tiny_rows(dtype, cache, ns):
+    """Rows of Q that are zero (a padded batch's) see the mean of V, beside masked keys and whatever
+    the magnitudes of K and V are."""
+    c = Paged(dtype, cache, 2, 128, 64, ns, [100, 333], seed=16)
+    for b in range(2):
+        for w, size in ((0, 1e-9), (1, 1e-12)):
+            c.put(w, b, 0, (size * c.rng.standard_normal((c.lens[b], 2, 128))).astype(np.float32))
+    c.upload()
+    q, qd = _q(c, 4)
+    q[::2], qd[::2] = 0, 0
+    out = torch.full((c.total, 4, 128), 7.0, dtype=TORCH[dtype], device="cuda")
+    status_ok(c.attend(q, out, 4, 8, 50))
+    want, tol = c.attention(qd, 4, 8, 50)
+    _check(f64(out), want, tol)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 90])
+def test_attention_scales_far_apart(cache, n):
+    """K and V rows whose magnitudes differ by 2^20 within a head, the large ones early or late."""
+    c = Paged("bf16", cache, 2, 128, 64, [n, n], [400, 300], seed=17)
+    for b in range(2):
+        for j in (5, 200, 290):
+            c.put(0, b, j, (2.0 ** -20 * c.rng.standard_normal((1, 2, 128))).astype(np.float32))
+            c.put(1, b, j, (2.0 ** (20 if j == 200 else -20) * c.rng.standard_normal((1, 2, 128))).astype(np.float32))
+    _attend(c, 8, 0, 64)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("batch,n", [(70, 33), (1100, 1)])
+def test_attention_large_batches(cache, batch, n):
+    """Batches beyond what a CTA plans itself, some sequences empty."""
+    r = np.random.default_rng(18)
+    ns = r.integers(0, n + 1, batch)
+    _attend(Paged("bf16", cache, 1, 128, 16, list(ns), list(r.integers(0, 60, batch)), seed=18), 2, 8, -1)
+
+
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("bf16", "e4m3"), ("f32", "f32")])
+def test_sequences_may_share_pages(dtype, cache):
+    """The pages of one prompt's beginning in the tables of several sequences."""
+    c = Paged(dtype, cache, 2, 128, 64, [1, 1, 20], [200, 250, 300], seed=19)
+    c.table[1, :2] = c.table[0, :2]
+    c.table[2, :2] = c.table[0, :2]
+    _attend(c, 4, 0, -1)
+
+
+@pytest.mark.parametrize("dtype,cache,most", [("bf16", "bf16", 1), ("bf16", "e4m3", 300), ("f32", "f32", 5)])
+def test_attention_of_no_rows(dtype, cache, most):
+    c = Paged(dtype, cache, 2, 128, 64, [0, 0], [30, 0], pad=4).upload()
+    q, _ = _q(c, 4)
+    out = torch.full((4, 4, 128), 7.0, dtype=TORCH[dtype], device="cuda")
+    status_ok(c.attend(q, out, 4, 0, -1, max_rows=most))
+    assert (out == 7.0).all()
+
+
+def test_two_graphs_share_a_workspace_in_order():
+    """Two captured calls of different shapes on one workspace, replayed one after the other."""
+    c = [Paged("bf16", "e4m3", 2, 128, 64, ns, pasts, seed=20 + i).upload()
+         for i, (ns, pasts) in enumerate([([200, 1], [300, 40]), ([1, 1, 1], [500, 2, 90])])]
+    qs = [_q(x, 8) for x in c]
+    outs = [torch.zeros((x.total, 8, 128), dtype=torch.bfloat16, device="cuda") for x in c]
+    ws = host.workspace(max(x.workspace(8).numel() for x in c))
+    for x, q, o in zip(c, qs, outs):
+        x.attend(q[0], o, 8, 0, -1, ws=ws)
+    graphs = []
+    for x, q, o in zip(c, qs, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            x.attend(q[0], o, 8, 0, -1, ws=ws, stream=torch.cuda.current_stream())
+    for _ in range(5):
+        for o in outs:
+            o.zero_()
+        for g in graphs:
+            g.replay()
+        status_ok(ws)
+        for x, q, o in zip(c, qs, outs):
+            want, tol = x.attention(q[1], 8, 0, -1)
+            _check(f64(o), want, tol)
