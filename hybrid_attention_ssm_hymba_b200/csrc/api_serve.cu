@@ -89,7 +89,7 @@ hymba_status_t check_attention(const hymba_paged_kv_t* kv, int batch, int total_
 hymba_status_t check_w4(const void* w, const void* q4, const float* scales, int N, int K, int group,
                         hymba_dtype_t dtype) {
   if (!w || !q4 || !scales || N < 1 || K < 1 || group < 1 || !valid_dtype(dtype)) return HYMBA_ERR_INVALID_ARG;
-  if ((group != 32 && group != 64 && group != 128) || K % group || !aligned16(w) || !aligned16(q4) ||
+  if ((group != 32 && group != 64 && group != 128) || K % group || N > (1 << 30) || K > (1 << 30) || !aligned16(w) || !aligned16(q4) ||
       (reinterpret_cast<uintptr_t>(scales) & 3))
     return HYMBA_ERR_UNSUPPORTED;
   return HYMBA_OK;

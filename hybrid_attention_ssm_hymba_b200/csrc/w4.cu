@@ -135,12 +135,14 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// q of nibbles i and i + 4 of a word as a bf16 pair.
+// q of nibbles i and i + 4 of a word, times 2^-10, as a bf16 pair (exact).  The power of two,
+// taken out again at the end, lets a group's unscaled sum of the largest fp32 values stay finite.
+constexpr float kQUp = 1024.f;
 __device__ __forceinline__ uint32_t q_pair(uint32_t u, int i) {
   uint32_t v;
-  const uint32_t off = 0x43084308u;   // 136
   asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(v) : "r"(u >> (4 * i)));   // (u & mask) | 128.0: 128 + code
-  const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&off));
+  const __nv_bfloat162 q = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v), __float2bfloat162_rn(1.f / kQUp),
+                                   __float2bfloat162_rn(-136.f / kQUp));
   return *reinterpret_cast<const uint32_t*>(&q);
 }
 
@@ -231,7 +233,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_co
           if (kSplit == 3) {   // the leading 8 bits, the next 8, the rest
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float hi = __uint_as_float(__float_as_uint(f[e]) & 0xffff0000u), r = f[e] - hi;
+              const bool finite = fabsf(f[e]) < INFINITY;   // (an infinity or NaN is its leading part)
+              const float hi = finite ? __uint_as_float(__float_as_uint(f[e]) & 0xffff0000u) : f[e], r = finite ? f[e] - hi : 0.f;
               const float mid = __uint_as_float(__float_as_uint(r) & 0xffff0000u);
               f[e] = part == 0 ? hi : part == 1 ? mid : r - mid;
             }
@@ -297,14 +300,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_co
         if (!last || kSplit > 1) acc[tl * 16 * 8 * NT + i] = v;
         const int n = (tile0 + tl) * 16 + i / (8 * NT), m = i % (8 * NT);
         if (last && kSplit == 1 && n < p.N && m < p.M)
-          static_cast<T*>(p.c)[static_cast<long long>(m) * p.N + n] = from_f<T>(v);
+          static_cast<T*>(p.c)[static_cast<long long>(m) * p.N + n] = from_f<T>(v * kQUp);
       }
       meet();
       if (last && kSplit > 1)
         for (int i = threadIdx.x - grp * 32 * p.S; i < 16 * p.M; i += 32 * p.S) {
           const int r = i / p.M, m = i - r * p.M, n = (tile0 + tl) * 16 + r;
           const float* v = &acc[(tl * 16 + r) * 8 * NT + m * kSplit];
-          if (n < p.N) static_cast<T*>(p.c)[static_cast<long long>(m) * p.N + n] = from_f<T>((v[2] + v[1]) + v[0]);
+          if (n < p.N) static_cast<T*>(p.c)[static_cast<long long>(m) * p.N + n] = from_f<T>(((v[2] + v[1]) + v[0]) * kQUp);
         }
     }
   }

@@ -109,3 +109,15 @@ def test_gemm_w4_repeats_and_graph():
     size = a.double().abs() @ back.double().abs().t()
     tol = size * (2.0 ** -8 + 2052 * 2.0 ** -23) + (c.double().abs() + full.double().abs()) * 2.0 ** -8
     assert ((c.double() - full.double()).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gemm_w4_keeps_non_finite_rows_apart(dtype):
+    """An infinity or a NaN in one row of A reaches that row of C only; a large finite row stays finite."""
+    a = torch.randn(4, 256, dtype=TORCH[dtype], device="cuda")
+    a[1, 7], a[2, 9], a[3] = float("inf"), float("nan"), 3e37
+    q4 = torch.full((40, 128), 0x99, dtype=torch.uint8, device="cuda")      # every q = 1
+    sc = torch.full((40, 4), 1e-3, device="cuda")
+    c = torch.empty(4, 40, dtype=TORCH[dtype], device="cuda")
+    H.check(H.hymba_gemm_w4(a, q4, sc, c, 4, 40, 256, 64, DTYPE[dtype]))
+    assert torch.isfinite(c[0]).all() and torch.isposinf(c[1]).all() and torch.isnan(c[2]).all() and torch.isfinite(c[3]).all()
