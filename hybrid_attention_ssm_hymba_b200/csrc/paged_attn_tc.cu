@@ -8,7 +8,7 @@
 // packed into the rows of a tile, so every K/V row is read once for all of them; two row
 // groups of up to 128 rows (TQ tokens x G heads) share each 128-key block.  The work is one
 // line of key blocks, cut evenly over a persistent CTA per SM (paged_plan.cuh); parts of a cut
-// tile leave their unnormalised output, m and sum in scratch, and paged_join_kernel joins them.
+// tile leave their unnormalised output, m and sum in scratch, and paged_join_tc joins them.
 //
 //   warp 0      producer: Q of both groups by TMA; K and V block by block, one TMA per page
 //               piece and 64-column half, through the page table (two 2-deep rings)
@@ -716,7 +716,8 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
         __nv_bfloat16* orow = p.out + static_cast<long long>(ti.row0 + rtok) * p.out_ld +
                               (ti.kvh * p.g.G + r % p.g.G) * DH + kh * 64;
         const long long prow = (static_cast<long long>(blockIdx.x) * 2 + ti.part) * p.part_rows + x * 128 + r;
-        float* part = p.part + prow * DH + kh * 64;
+        // parts: [eight rows][four columns][row], which a warp writes in whole lines
+        uint4* part = reinterpret_cast<uint4*>(p.part) + (prow >> 3) * (2 * DH) + kh * 128 + (r & 7);
         if (!whole && kh == 0) p.part_ml[prow] = make_float2(FP8 ? m_used - kPUp : m_used, lsum);
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -729,9 +730,8 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
             for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
           }
           if (!whole) {
-            uint4* dst = reinterpret_cast<uint4*>(part + c * 16);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            for (int q = 0; q < 4; ++q) part[(4 * c + q) * 8] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           } else if (mine) {
             uint4* dst = reinterpret_cast<uint4*>(orow + c * 16);
 #pragma unroll
@@ -755,37 +755,48 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
   }
 }
 
-// Joins the parts of the tile that CTA i of the attention began and others finished: a warp a
-// row, gridDim.y CTAs a tile.  A row's parts are weighted by 2^(m - max).
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedAttnParams p) {
+// Joins the parts of the tile that CTA i of the attention began and others finished, weighted by
+// 2^(m - max): eight rows a CTA at a time, a warp 16 of their columns.
+__global__ void __launch_bounds__(256) paged_join_tc(const __grid_constant__ PagedAttnParams p) {
   pdl_trigger();
   pdl_wait();
   const int i = blockIdx.x;
   const CutRecord cut = p.cut[i];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group_rows = p.g.TQ * p.g.G;
-  for (int rr = blockIdx.y * 8 + warp; rr < cut.toks * p.g.G; rr += gridDim.y * 8) {
-    const int x = rr / group_rows, r = rr - x * group_rows, tok = x * p.g.TQ + r / p.g.G, rg = r % p.g.G;
-    // part c of the row lies at first[(2 c + (c == i)) * part_rows]: the first one is CTA i's own
-    const long long row = x * 128 + r;
-    float m = -INFINITY;
-    for (int c = i + lane; c <= cut.last; c += 32)
-      m = fmaxf(m, p.part_ml[(2LL * c + (c == i)) * p.part_rows + row].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const int c4 = (threadIdx.x >> 5) * 4 + ((threadIdx.x & 31) >> 3);   // column / 4
+  for (int row = blockIdx.y * 8 + (threadIdx.x & 7); row < p.part_rows; row += gridDim.y * 8) {
+    const int x = row >> 7, r = row & 127, tok = x * p.g.TQ + r / p.g.G, rg = r % p.g.G;
+    if (r >= p.g.TQ * p.g.G || tok >= cut.toks) continue;
+    float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int c = i; c <= cut.last; ++c) {
-      const long long at = (2LL * c + (c == i)) * p.part_rows + row;
-      const float2 ml = p.part_ml[at];
-      const float4 v = reinterpret_cast<const float4*>(p.part + at * DH)[lane];
-      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
-      l = fmaf(ml.y, f, l);
-      if (f != 0.f) acc = make_float4(fmaf(v.x, f, acc.x), fmaf(v.y, f, acc.y), fmaf(v.z, f, acc.z), fmaf(v.w, f, acc.w));
+    for (int c0 = i; c0 <= cut.last; c0 += 4) {   // CTA i's part is its second, the others' their first
+      float2 ml[4];
+      float4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        ml[u] = make_float2(-INFINITY, 0.f);
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c0 + u > cut.last) continue;
+        const long long at = (2LL * (c0 + u) + (c0 + u == i)) * p.part_rows + row;
+        ml[u] = p.part_ml[at];
+        v[u] = reinterpret_cast<const float4*>(p.part)[(at >> 3) * (2 * DH) + c4 * 8 + (row & 7)];
+      }
+      const float mn = fmaxf(fmaxf(m, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+      if (mn == -INFINITY) continue;
+      const float f0 = ex2_approx(m - mn);
+      m = mn;
+      l *= f0;
+      acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float f = ex2_approx(ml[u].x - mn);
+        if (f == 0.f) continue;
+        l = fmaf(ml[u].y, f, l);
+        acc = make_float4(fmaf(v[u].x, f, acc.x), fmaf(v[u].y, f, acc.y), fmaf(v[u].z, f, acc.z), fmaf(v[u].w, f, acc.w));
+      }
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;
     __nv_bfloat16* o = p.out + static_cast<long long>(cut.row0 + tok) * p.out_ld + (cut.kvh * p.g.G + rg) * DH;
-    reinterpret_cast<uint2*>(o)[lane] = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    reinterpret_cast<uint2*>(o)[c4] = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
   }
 }
 
@@ -817,11 +828,6 @@ bool encode(CUtensorMap* m, bool bytes, int rank, const void* base, const cuuint
 }
 
 }  // namespace
-
-cudaError_t launch_paged_join(const PagedAttnParams& p, int ctas, cudaStream_t st) {
-  if (ctas < 2) return cudaSuccess;
-  return launch(paged_join_kernel, dim3(ctas - 1, (p.part_rows + 31) / 32), dim3(256), 0, st, p);
-}
 
 // The scratch is sized for the B200's 148 SMs; a launch uses at most that many CTAs.
 constexpr int kMaxCtas = 148;
@@ -879,7 +885,7 @@ cudaError_t launch_paged_attention_tc(const PagedAttnDesc& a, cudaStream_t st) {
   if (cudaError_t e = fp8 ? launch(paged_attn_tc<true>, dim3(ctas), dim3(kThreadsFp8), smem_bytes<true>(), st, tq, tk, tv, p)
                           : launch(paged_attn_tc<false>, dim3(ctas), dim3(kThreads), smem_bytes<false>(), st, tq, tk, tv, p))
     return e;
-  return launch_paged_join(p, ctas, st);
+  return launch(paged_join_tc, dim3(ctas - 1, p.part_rows / 32), dim3(256), 0, st, p);
 }
 
 }  // namespace hy

@@ -509,6 +509,39 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) paged_decode_ker
   pdl_trigger();
 }
 
+// Joins the parts of the tile that CTA i of the attention began and others finished: a warp a
+// row, eight rows a CTA.  A row's parts are weighted by 2^(m - max).
+__global__ void __launch_bounds__(256) paged_join_rows(const __grid_constant__ PagedAttnParams p) {
+  pdl_trigger();
+  pdl_wait();
+  const int i = blockIdx.x;
+  const CutRecord cut = p.cut[i];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * 8 + warp, tok = row / p.g.G, rg = row % p.g.G;
+  if (tok < cut.toks) {
+    // part c of the row lies at first[(2 c + (c == i)) * part_rows]: the first one is CTA i's own
+    float m = -INFINITY;
+    for (int c = i + lane; c <= cut.last; c += 32)
+      m = fmaxf(m, p.part_ml[(2LL * c + (c == i)) * p.part_rows + row].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 4
+    for (int c = i; c <= cut.last; ++c) {
+      const long long at = (2LL * c + (c == i)) * p.part_rows + row;
+      const float2 ml = p.part_ml[at];
+      const float4 v = reinterpret_cast<const float4*>(p.part + at * DH)[lane];
+      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+      l = fmaf(ml.y, f, l);
+      if (f != 0.f) acc = make_float4(fmaf(v.x, f, acc.x), fmaf(v.y, f, acc.y), fmaf(v.z, f, acc.z), fmaf(v.w, f, acc.w));
+    }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    __nv_bfloat16* o = p.out + static_cast<long long>(cut.row0 + tok) * p.out_ld + (cut.kvh * p.g.G + rg) * DH;
+    reinterpret_cast<uint2*>(o)[lane] = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  }
+}
+
 // CTAs per SM that the registers allow, with one and with two tiles of queries.
 constexpr int kPerSm[2] = {3, 2};
 constexpr int kMaxSms = 148;   // the scratch is sized for the B200
@@ -556,7 +589,7 @@ cudaError_t launch_paged_decode(const PagedAttnDesc& a, cudaStream_t st) {
   const auto kernel = a.kv.type == CACHE_E4M3 ? (nt == 1 ? paged_decode_kernel<true, 1> : paged_decode_kernel<true, 2>)
                                               : (nt == 1 ? paged_decode_kernel<false, 1> : paged_decode_kernel<false, 2>);
   if (cudaError_t e = launch(kernel, dim3(ctas), dim3(32 * kWarps), 0, st, p)) return e;
-  return launch_paged_join(p, ctas, st);
+  return launch(paged_join_rows, dim3(ctas - 1, nt), dim3(256), 0, st, p);
 }
 
 }  // namespace hy

@@ -37,7 +37,8 @@ struct PagedAttnParams {
   long long q_ld;
   __nv_bfloat16* out;
   long long out_ld;
-  float* part;          // [CTA][2][part_rows][dh]: 0 = the CTA's first tile continued, 1 = its last tile begun
+  float* part;          // [CTA][2][part_rows][dh] (the rows' order is the kernel's own): 0 = the CTA's first
+                        // tile continued, 1 = its last tile begun
   float2* part_ml;      // [CTA][2][part_rows] (m in log2 units, sum)
   CutRecord* cut;       // [CTA]
   int part_rows;
@@ -65,8 +66,6 @@ inline PagedScratch paged_scratch_layout(int batch, int ctas, int part_rows, int
   s.total = o;
   return s;
 }
-// Joins the cut tiles of a launch of `ctas` CTAs (paged_attn_tc.cu).
-cudaError_t launch_paged_join(const PagedAttnParams& p, int ctas, cudaStream_t st);
 
 // One tile's visit: block x of [0, n) starts at key 128 * block(x).
 struct TileSpan {
