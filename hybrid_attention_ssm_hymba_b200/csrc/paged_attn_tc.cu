@@ -13,9 +13,9 @@
 //   warp 0      producer: Q of both groups by TMA; K and V block by block, one TMA per page
 //               piece and 64-column half, through the page table (two 2-deep rings)
 //   warp 1      UMMA issuer, per block: P_a V, S_a of the next block, P_b V, S_b of the next
-//   warps 2..9  softmax of group a, warps 10..17 of group b: two threads per row, each over 64
-//               of the block's keys and 64 of O's columns
-//   warps 18, 19 (e4m3 cache only) turn the 8-bit K and V of a block into the fp16 tiles the
+//   warps 2..9  softmax of group a, warps 10..17 of group b (e4m3 cache: two later): two threads
+//               per row, each over 64 of the block's keys and 64 of O's columns
+//   warps 2, 3  (e4m3 cache only) turn the 8-bit K and V of a block into the fp16 tiles the
 //               tensor core reads.  An e4m3 code is exact in fp16.  V: code times scale is rounded
 //               once to fp16's 11 bits (2^-12, where the output's own rounding is 2^-8).  K: a
 //               score of hundreds would lose too much that way, so K is the code times the power
@@ -110,13 +110,16 @@ __device__ __forceinline__ float row_max64(const uint32_t (&sv)[64]) {
     for (int i = 0; i < 8; ++i) m[i] = max3f(m[i], __uint_as_float(sv[e + i]), __uint_as_float(sv[e + 8 + i]));
   return max3f(max3f(m[0], m[1], m[2]), max3f(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
 }
-// 64 values times a shared vector, the same for every row.
+// 64 values times a shared vector, the same for every row; eight loads ahead (one: 1385 us against
+// 1328 for 4096 rows over 32K e4m3 keys), since shared memory is busy with the tensor core's operands.
 __device__ __forceinline__ void scale64(uint32_t (&sv)[64], uint32_t vec) {
-  float4 next = lds_f4(vec);   // one load ahead: shared memory is busy with the tensor core's operands
+  float4 ring[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) ring[q] = lds_f4(vec + 16 * q);
 #pragma unroll
   for (int q = 0; q < 16; ++q) {
-    const float4 k = next;
-    if (q < 15) next = lds_f4(vec + 16 * q + 16);
+    const float4 k = ring[q % 8];
+    if (q + 8 < 16) ring[q % 8] = lds_f4(vec + 16 * (q + 8));
     const float2 a = __fmul2_rn(make_float2(__uint_as_float(sv[4 * q]), __uint_as_float(sv[4 * q + 1])), make_float2(k.x, k.y));
     const float2 b = __fmul2_rn(make_float2(__uint_as_float(sv[4 * q + 2]), __uint_as_float(sv[4 * q + 3])), make_float2(k.z, k.w));
     sv[4 * q] = __float_as_uint(a.x);
@@ -158,6 +161,13 @@ __device__ __forceinline__ float row_exp64(uint32_t (&sv)[64], float scale_log2,
 }
 
 constexpr int kThreads = 576, kThreadsFp8 = 640;
+// 8-bit path: registers of a thread at launch, of the softmax warpgroups and of the warpgroup of the
+// other four warps.  (Ragged e4m3 chunks: 98 us, without the shift 105; the bf16 path, two idle
+// warps added for it: 1010 us for 4096 rows over 32K, without 970.)
+constexpr int kRegs = 96, kRegsSoft = 104, kRegsFew = 64;
+static_assert(512 * kRegsSoft + 128 * kRegsFew <= kThreadsFp8 * kRegs, "more registers than the launch has");
+template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
 template <bool FP8>
 __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
@@ -223,339 +233,347 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
     prefix = sm.prefix;
   }
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- producer (whole warp)
-    PieceWalk walk(p, prefix, lane == 0);
-    Piece pc;
-    const int npc = 128 / p.piece;   // K/V loads per block and half: lane i < npc issues piece i's
-    const int none = p.kv.n_pages * p.kv.page_size;   // a row beyond the map: zeros
-    uint32_t jb = 0, seg = 0;        // blocks and tiles so far
-    uint32_t k_iss = 0, v_iss = 0, k_par = 0, v_par = 0;
-    uint32_t raw = 0, scales_issued = 0;   // FP8: half tiles, and blocks whose scales are under way
-    bool ok = true;
-    for (;;) {
-      const bool more = walk.next(p, &pc, lane == 0);
-      const int groups = pc.ts.toks > p.g.TQ ? 2 : 1;   // row groups with tokens
-      ok = mbar_wait(&sm.q_empty, (seg & 1) ^ 1u, p.status, abort_flag) &&
-           mbar_wait(&sm.tile_empty[seg & (kTileSlots - 1)], ((seg / kTileSlots) & 1) ^ 1u, p.status, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (lane == 0) {
-        TileInfo& ti = sm.tile[seg & (kTileSlots - 1)];
-        ti.toks = more && ok ? pc.ts.toks : 0;
-        if (more) {
-          ti.p0 = pc.ts.p0;
-          ti.p1 = pc.ts.p1;
-          ti.n = pc.blk1 - pc.blk0;
-          ti.row0 = pc.row0;
-          ti.kvh = pc.kvh;
-          ti.part = pc.whole ? -1 : (pc.blk0 == 0 ? 1 : 0);
-          ti.groups = groups;
-        }
-        mbar_arrive(&sm.tile_full[seg & (kTileSlots - 1)]);
-      }
-      if (!more || !ok) break;
-      if (lane == 0) {
-        const int bytes = p.g.TQ * p.g.G * 128;
-        mbar_arrive_expect_tx(&sm.q_full, 2 * groups * bytes);
-        for (int x = 0; x < groups; ++x) {
-          tma_load_3d(sQ + x * TILE_BYTES, &tmQ, &sm.q_full, 0, pc.kvh * p.g.G, pc.row0 + x * p.g.TQ);
-          tma_load_3d(sQ + x * TILE_BYTES + HALF, &tmQ, &sm.q_full, 64, pc.kvh * p.g.G, pc.row0 + x * p.g.TQ);
-        }
-      }
-      ++seg;
-      __syncwarp();
-      const int lo = p.g.window < 0 ? 0 : pc.ts.p0 - p.g.window;   // first key of any query's window
-      for (int x = pc.blk0; x < pc.blk1; ++x, ++jb) {
-        const int k0 = pc.ts.block(x) * kKeyBlock, s = jb & 1;
-        const uint32_t par = (jb >> 1) & 1;
-        int row = none;
-        bool bad = false;
-        if (lane < npc) {
-          const int r0 = k0 + lane * p.piece, r1 = r0 + p.piece - 1;
-          if (r0 <= pc.ts.p1 && (r0 < p.g.n_meta || r1 >= lo)) {
-            const int page = page_of(p.kv, pc.b, r0);
-            bad = page < 0;
-            if (!bad) row = page * p.kv.page_size + r0 % p.kv.page_size;
-          }
-        }
-        const unsigned bads = __ballot_sync(0xffffffffu, bad);
-        if (bads && lane == 0) report_invalid(p.status);
-        BlockInfo& bi = sm.block[jb & (kBlockSlots - 1)];
-        if (lane < 4) {   // 32 rows per word
-          uint32_t m = 0xffffffffu;
-          if (bads)
-            for (int r = 0; r < 32; ++r)
-              if ((bads >> ((lane * 32 + r) / p.piece)) & 1u) m &= ~(1u << r);
-          bi.valid[lane] = m;
-        }
+  constexpr int kSoft = FP8 ? 4 : 2;   // first softmax warp
+  if (warp < kSoft) {
+    if constexpr (FP8) reg_dec<kRegsFew>();
+    if (warp == 0) {
+      // ---------------------------------------------------------------- producer (whole warp)
+      PieceWalk walk(p, prefix, lane == 0);
+      Piece pc;
+      const int npc = 128 / p.piece;   // K/V loads per block and half: lane i < npc issues piece i's
+      const int none = p.kv.n_pages * p.kv.page_size;   // a row beyond the map: zeros
+      uint32_t jb = 0, seg = 0;        // blocks and tiles so far
+      uint32_t k_iss = 0, v_iss = 0, k_par = 0, v_par = 0;
+      uint32_t raw = 0, scales_issued = 0;   // FP8: half tiles, and blocks whose scales are under way
+      bool ok = true;
+      for (;;) {
+        const bool more = walk.next(p, &pc, lane == 0);
+        const int groups = pc.ts.toks > p.g.TQ ? 2 : 1;   // row groups with tokens
+        ok = mbar_wait(&sm.q_empty, (seg & 1) ^ 1u, p.status, abort_flag) &&
+             mbar_wait(&sm.tile_empty[seg & (kTileSlots - 1)], ((seg / kTileSlots) & 1) ^ 1u, p.status, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
         if (lane == 0) {
-          uint32_t f = 0;
-          const int k1 = k0 + kKeyBlock - 1;
-          for (int gx = 0; gx < 2; ++gx) {   // places of the group's rows: pa .. pb
-            const int pa = pc.ts.p0 + gx * p.g.TQ, pb = min(pc.ts.p1, pa + p.g.TQ - 1);
-            if (bads || k1 > pa || (p.g.window >= 0 && pb - k0 > p.g.window && k1 >= p.g.n_meta)) f |= 1u << gx;
+          TileInfo& ti = sm.tile[seg & (kTileSlots - 1)];
+          ti.toks = more && ok ? pc.ts.toks : 0;
+          if (more) {
+            ti.p0 = pc.ts.p0;
+            ti.p1 = pc.ts.p1;
+            ti.n = pc.blk1 - pc.blk0;
+            ti.row0 = pc.row0;
+            ti.kvh = pc.kvh;
+            ti.part = pc.whole ? -1 : (pc.blk0 == 0 ? 1 : 0);
+            ti.groups = groups;
           }
-          if (k1 > pc.ts.p1 || max(k0, p.g.n_meta) < min(k0 + kKeyBlock, lo)) f |= kZeroV;
-          bi.k0 = k0;
-          bi.flags = f;
+          mbar_arrive(&sm.tile_full[seg & (kTileSlots - 1)]);
         }
-        __syncwarp();
-        if constexpr (FP8) {
-          // the scales of the pieces that are there, then K and V in half tiles
-          const int page = row / p.kv.page_size, at = row - page * p.kv.page_size;
-          const bool have = lane < npc && row != none;
-          const unsigned haves = __ballot_sync(0xffffffffu, have);
-          uint64_t* sf = &sm.scale_full[jb % kScaleSlots];
-          if (lane == 0) mbar_arrive_expect_tx(sf, 2 * __popc(haves) * p.piece * 4);
-          __syncwarp();
-          if (have) {
-#pragma unroll
-            for (int w = 0; w < 2; ++w)
-              bulk_load_1d(&sm.scale[jb % kScaleSlots][w][lane * p.piece], p.kv.scales + page_scale(p.kv, w, page, at, pc.kvh),
-                           p.piece * 4, sf);
+        if (!more || !ok) break;
+        if (lane == 0) {
+          const int bytes = p.g.TQ * p.g.G * 128;
+          mbar_arrive_expect_tx(&sm.q_full, 2 * groups * bytes);
+          for (int x = 0; x < groups; ++x) {
+            tma_load_3d(sQ + x * TILE_BYTES, &tmQ, &sm.q_full, 0, pc.kvh * p.g.G, pc.row0 + x * p.g.TQ);
+            tma_load_3d(sQ + x * TILE_BYTES + HALF, &tmQ, &sm.q_full, 64, pc.kvh * p.g.G, pc.row0 + x * p.g.TQ);
           }
-          scales_issued = jb + 1;
-#pragma unroll 1
-          for (int u = 0; ok && u < 4; ++u, ++raw) {   // K rows 0.., K rows 64.., V rows 0.., V rows 64..
-            const uint32_t rs = raw % kRawStages;
-            ok = __all_sync(0xffffffffu, mbar_wait(&sm.raw_empty[rs], ((raw / kRawStages) & 1) ^ 1u, p.status, abort_flag));
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[rs], kRawBytes);
-            __syncwarp();
-            const int r0 = lane * p.piece;
-            if (lane < npc && (r0 >> 6) == (u & 1))
-              tma_load_2d(sRaw + rs * kRawBytes + (r0 & 63) * DH, u < 2 ? &tmK : &tmV, &sm.raw_full[rs], pc.kvh * DH, row);
-          }
-          if (!ok) break;
-          continue;
         }
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.k_empty[s], par ^ 1u, p.status, abort_flag));
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[s], TILE_BYTES);
+        ++seg;
         __syncwarp();
-        if (lane < npc) {
-          uint8_t* dst = sK + s * TILE_BYTES + lane * p.piece * 128;
-          tma_load_2d(dst, &tmK, &sm.k_full[s], pc.kvh * DH, row);
-          tma_load_2d(dst + HALF, &tmK, &sm.k_full[s], pc.kvh * DH + 64, row);
-        }
-        k_iss |= 1u << s;
-        k_par = (k_par & ~(1u << s)) | (par << s);
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.v_empty[s], par ^ 1u, p.status, abort_flag));
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[s], TILE_BYTES);
-        __syncwarp();
-        if (lane < npc) {
-          uint8_t* dst = sV + s * TILE_BYTES + lane * p.piece * 128;
-          tma_load_2d(dst, &tmV, &sm.v_full[s], pc.kvh * DH, row);
-          tma_load_2d(dst + HALF, &tmV, &sm.v_full[s], pc.kvh * DH + 64, row);
-        }
-        v_iss |= 1u << s;
-        v_par = (v_par & ~(1u << s)) | (par << s);
-      }
-      if (!ok) break;   // the others leave by the abort flag
-    }
-    // every issued copy lands before the CTA may exit
-    int never = 0;
-    for (int s = 0; s < 2; ++s) {
-      if (k_iss & (1u << s)) mbar_wait(&sm.k_full[s], (k_par >> s) & 1u, nullptr, &never, 100000000ull);
-      if (v_iss & (1u << s)) mbar_wait(&sm.v_full[s], (v_par >> s) & 1u, nullptr, &never, 100000000ull);
-    }
-    if constexpr (FP8) {
-      for (uint32_t u = raw > kRawStages ? raw - kRawStages : 0; u < raw; ++u)
-        mbar_wait(&sm.raw_full[u % kRawStages], (u / kRawStages) & 1, nullptr, &never, 100000000ull);
-      for (uint32_t u = scales_issued > kScaleSlots ? scales_issued - kScaleSlots : 0; u < scales_issued; ++u)
-        mbar_wait(&sm.scale_full[u % kScaleSlots], (u / kScaleSlots) & 1, nullptr, &never, 100000000ull);
-    }
-    if (seg) mbar_wait(&sm.q_full, (seg - 1) & 1u, nullptr, &never, 100000000ull);
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- UMMA issuer (lane 0)
-    if (lane == 0) {
-      const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(sK), 16, 1024),
-                     dV = sdesc_sw128(smem_u32(sV), HALF, 1024);
-      auto issue_s = [&](int x, int s) {  // S_x = Q_x K^T into TMEM columns [128 x, 128 x + 128)
-        const uint64_t qd = sdesc_add(dQ, x * TILE_BYTES), kd = sdesc_add(dK, s * TILE_BYTES);
-#pragma unroll
-        for (int k = 0; k < DH / 16; ++k) {
-          const uint32_t off = (k >> 2) * HALF + (k & 3) * 32;
-          umma_bf16_ss(tmem_base + x * 128, sdesc_add(qd, off), sdesc_add(kd, off), IDESC_QK<FP8>, k != 0 ? 1u : 0u);
-        }
-        umma_commit(&sm.s_full[x]);
-      };
-      auto issue_pv = [&](int x, int s, bool acc) {  // O_x (+)= P_x V, P_x from TMEM over S_x
-        const uint64_t vd = sdesc_add(dV, s * TILE_BYTES);
-#pragma unroll
-        for (int k = 0; k < 128 / 16; ++k)
-          umma_bf16_ts(tmem_base + 256 + x * 128, tmem_base + x * 128 + k * 8, sdesc_add(vd, k * 16 * 128), IDESC_PV<FP8>,
-                       (acc || k != 0) ? 1u : 0u);
-        umma_commit(&sm.o_done[x]);
-      };
-      uint32_t jb = 0, cnt[2] = {0, 0};   // blocks so far: all, and per group
-      uint32_t tiles[2] = {0, 0};         // and tiles, per group
-      bool ok = true;
-      for (uint32_t seg = 0; ok; ++seg) {
-        const TileInfo& ti = sm.tile[seg & (kTileSlots - 1)];
-        ok = mbar_wait(&sm.tile_full[seg & (kTileSlots - 1)], (seg / kTileSlots) & 1, p.status, abort_flag);
-        if (!ok || ti.toks == 0) break;
-        const int n = ti.n, gr = ti.groups;
-        ok = mbar_wait(&sm.q_full, seg & 1, p.status, abort_flag) &&
-             mbar_wait(&sm.k_full[jb & 1], (jb >> 1) & 1, p.status, abort_flag);
-        if constexpr (FP8) {   // Q in fp16
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            if (ok && x < gr) ok = mbar_wait(&sm.q_ready[x], tiles[x]++ & 1, p.status, abort_flag);
-        }
-        // S_x goes over the TMEM columns that the last P V of the previous tile reads
-        for (int x = 0; ok && x < gr; ++x)
-          if (cnt[x] > 0) ok = mbar_wait(&sm.o_done[x], (cnt[x] - 1) & 1, p.status, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        for (int x = 0; x < gr; ++x) issue_s(x, jb & 1);
-        umma_commit(&sm.k_empty[jb & 1]);
-        if (n == 1) umma_commit(&sm.q_empty);
-        for (int j = 0; ok && j < n; ++j, ++jb) {
-          for (int x = 0; ok && x < gr; ++x) {
-            const uint32_t par = cnt[x] & 1;
-            if (!mbar_wait(&sm.p_full[x], par, p.status, abort_flag)) { ok = false; break; }
-            if (x == 0 && !mbar_wait(&sm.v_full[jb & 1], (jb >> 1) & 1, p.status, abort_flag)) { ok = false; break; }
-            tc_fence_after();
-            issue_pv(x, jb & 1, j > 0);
-            ++cnt[x];
-            if (x == gr - 1) umma_commit(&sm.v_empty[jb & 1]);
-            if (j + 1 < n) {
-              // S_x of the next block overwrites the TMEM columns this P V reads: wait for it
-              if (!mbar_wait(&sm.o_done[x], par, p.status, abort_flag)) { ok = false; break; }
-              if (x == 0 && !mbar_wait(&sm.k_full[(jb + 1) & 1], ((jb + 1) >> 1) & 1, p.status, abort_flag)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              issue_s(x, (jb + 1) & 1);
-              if (x == gr - 1) {
-                umma_commit(&sm.k_empty[(jb + 1) & 1]);
-                if (j + 2 == n) umma_commit(&sm.q_empty);
-              }
+        const int lo = p.g.window < 0 ? 0 : pc.ts.p0 - p.g.window;   // first key of any query's window
+        for (int x = pc.blk0; x < pc.blk1; ++x, ++jb) {
+          const int k0 = pc.ts.block(x) * kKeyBlock, s = jb & 1;
+          const uint32_t par = (jb >> 1) & 1;
+          int row = none;
+          bool bad = false;
+          if (lane < npc) {
+            const int r0 = k0 + lane * p.piece, r1 = r0 + p.piece - 1;
+            if (r0 <= pc.ts.p1 && (r0 < p.g.n_meta || r1 >= lo)) {
+              const int page = page_of(p.kv, pc.b, r0);
+              bad = page < 0;
+              if (!bad) row = page * p.kv.page_size + r0 % p.kv.page_size;
             }
           }
-        }
-      }
-      umma_commit(&sm.mma_done);
-      int never = 0;
-      mbar_wait(&sm.mma_done, 0, nullptr, &never, 100000000ull);
-    }
-  } else if (FP8 && warp >= 18) {
-    // ---------------------------------------------------------------- e4m3 -> fp16 (two warps)
-    if constexpr (FP8) {
-      const int t = threadIdx.x - 18 * 32;   // of 64
-      uint32_t jb = 0, raw = 0;
-      bool ok = true;
-      for (uint32_t seg = 0; ok; ++seg) {
-        const volatile TileInfo& ti = sm.tile[seg & (kTileSlots - 1)];
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.tile_full[seg & (kTileSlots - 1)], (seg / kTileSlots) & 1, p.status,
-                                               abort_flag));
-        if (!ok || ti.toks == 0) break;
-        const int n = ti.n, p1 = ti.p1, lo = p.g.window < 0 ? 0 : ti.p0 - p.g.window;
-        uint32_t most[2] = {0, 0};   // the largest of K's and of V's scales so far, as bits
-        for (int j = 0; ok && j < n; ++j, ++jb) {
-          const uint32_t s = jb & 1, par = (jb >> 1) & 1, slot = jb % kScaleSlots, slot_par = (jb / kScaleSlots) & 1;
+          const unsigned bads = __ballot_sync(0xffffffffu, bad);
+          if (bads && lane == 0) report_invalid(p.status);
           BlockInfo& bi = sm.block[jb & (kBlockSlots - 1)];
-          if (warp == 18) {
-            // the scales as the products use them (see Smem), 0 for rows that no query of the tile sees.
-            // Done before k_full, so that S of the block implies it.
-            ok = __all_sync(0xffffffffu, mbar_wait(&sm.scale_full[slot], slot_par, p.status, abort_flag));
-            if (!ok) break;
-            const uint32_t valid = bi.valid[lane >> 3] >> ((lane & 7) * 4);
-            const int key0 = bi.k0 + lane * 4;
-            uint32_t seen = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (((valid >> e) & 1u) && key0 + e <= p1 && (key0 + e >= lo || key0 + e < p.g.n_meta)) seen |= 1u << e;
-            float4& k4 = *reinterpret_cast<float4*>(&sm.scale[slot][0][lane * 4]);
-            float4& v4 = *reinterpret_cast<float4*>(&sm.scale[slot][1][lane * 4]);
-            float k[4] = {k4.x, k4.y, k4.z, k4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w}, up[2];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (!((seen >> e) & 1u)) k[e] = v[e] = 0.f;
-              most[0] = max(most[0], __float_as_uint(k[e]) & 0x7fffffffu);
-              most[1] = max(most[1], __float_as_uint(v[e]) & 0x7fffffffu);
-            }
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              most[w] = __reduce_max_sync(0xffffffffu, most[w]);
-              // every scale is below 2^ex
-              const int ex = max(static_cast<int>(most[w] >> 23) - 126, w ? kUp - 127 : kUp - kMostUp);
-              up[w] = pow2(kUp - ex);
-              if (lane == 0) (w ? bi.ev : bi.ek) = ex;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t kb = __float_as_uint(k[e]);
-              const __half2 h = __floats2half2_rn(v[e] * up[1], __uint_as_float(kb & 0x7f800000u) * up[0]);
-              v[e] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h));
-              k[e] = __uint_as_float((kb & 0x7fffffu) | 0x3f800000u);
-            }
-            k4 = make_float4(k[0], k[1], k[2], k[3]);
-            v4 = make_float4(v[0], v[1], v[2], v[3]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.scale_ready[slot]);
+          if (lane < 4) {   // 32 rows per word
+            uint32_t m = 0xffffffffu;
+            if (bads)
+              for (int r = 0; r < 32; ++r)
+                if ((bads >> ((lane * 32 + r) / p.piece)) & 1u) m &= ~(1u << r);
+            bi.valid[lane] = m;
           }
-          ok = __all_sync(0xffffffffu, mbar_wait(&sm.scale_ready[slot], slot_par, p.status, abort_flag));
+          if (lane == 0) {
+            uint32_t f = 0;
+            const int k1 = k0 + kKeyBlock - 1;
+            for (int gx = 0; gx < 2; ++gx) {   // places of the group's rows: pa .. pb
+              const int pa = pc.ts.p0 + gx * p.g.TQ, pb = min(pc.ts.p1, pa + p.g.TQ - 1);
+              if (bads || k1 > pa || (p.g.window >= 0 && pb - k0 > p.g.window && k1 >= p.g.n_meta)) f |= 1u << gx;
+            }
+            if (k1 > pc.ts.p1 || max(k0, p.g.n_meta) < min(k0 + kKeyBlock, lo)) f |= kZeroV;
+            bi.k0 = k0;
+            bi.flags = f;
+          }
+          __syncwarp();
+          if constexpr (FP8) {
+            // the scales of the pieces that are there, then K and V in half tiles
+            const int page = row / p.kv.page_size, at = row - page * p.kv.page_size;
+            const bool have = lane < npc && row != none;
+            const unsigned haves = __ballot_sync(0xffffffffu, have);
+            uint64_t* sf = &sm.scale_full[jb % kScaleSlots];
+            if (lane == 0) mbar_arrive_expect_tx(sf, 2 * __popc(haves) * p.piece * 4);
+            __syncwarp();
+            if (have) {
+#pragma unroll
+              for (int w = 0; w < 2; ++w)
+                bulk_load_1d(&sm.scale[jb % kScaleSlots][w][lane * p.piece], p.kv.scales + page_scale(p.kv, w, page, at, pc.kvh),
+                             p.piece * 4, sf);
+            }
+            scales_issued = jb + 1;
 #pragma unroll 1
-          for (int u = 0; ok && u < 4; ++u, ++raw) {
-            const uint32_t rs = raw % kRawStages;
-            if ((u & 1) == 0)
-              ok = __all_sync(0xffffffffu, mbar_wait(u ? &sm.v_empty[s] : &sm.k_empty[s], par ^ 1u, p.status, abort_flag));
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.raw_full[rs], (raw / kRawStages) & 1, p.status, abort_flag));
+            for (int u = 0; ok && u < 4; ++u, ++raw) {   // K rows 0.., K rows 64.., V rows 0.., V rows 64..
+              const uint32_t rs = raw % kRawStages;
+              ok = __all_sync(0xffffffffu, mbar_wait(&sm.raw_empty[rs], ((raw / kRawStages) & 1) ^ 1u, p.status, abort_flag));
+              if (!ok) break;
+              if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[rs], kRawBytes);
+              __syncwarp();
+              const int r0 = lane * p.piece;
+              if (lane < npc && (r0 >> 6) == (u & 1))
+                tma_load_2d(sRaw + rs * kRawBytes + (r0 & 63) * DH, u < 2 ? &tmK : &tmV, &sm.raw_full[rs], pc.kvh * DH, row);
+            }
             if (!ok) break;
-            // 16 codes (one of a row's eight chunks) at a time, to two 16-byte chunks of the swizzled
-            // tile.  The lanes of a row's upper half take the neighbouring row, so that eight lanes
-            // meet no bank twice in either tile.
-            const int up = (t >> 2) & 1, row0 = (t >> 3) ^ up, c = (t & 3) * 2;
-            const uint32_t src = smem_u32(sRaw + rs * kRawBytes) + row0 * DH + (t & 7) * 16;
-            const uint32_t dst = smem_u32((u < 2 ? sK : sV) + s * TILE_BYTES + up * HALF + ((u & 1) * 64 + row0) * 128);
-            const uint32_t fs = smem_u32(&sm.scale[slot][1][(u & 1) * 64 + row0]);
-            const uint32_t at0 = dst + ((c ^ row0) << 4), at1 = dst + (((c + 1) ^ row0) << 4);   // row & 7 = row0
-            const bool hide = u >= 2 && (bi.flags & kZeroV);
-            const int key0 = bi.k0 + (u & 1) * 64 + row0;
-            float4 r4[8];   // all in flight before the first is used
-            uint32_t f[8];
+            continue;
+          }
+          ok = __all_sync(0xffffffffu, mbar_wait(&sm.k_empty[s], par ^ 1u, p.status, abort_flag));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[s], TILE_BYTES);
+          __syncwarp();
+          if (lane < npc) {
+            uint8_t* dst = sK + s * TILE_BYTES + lane * p.piece * 128;
+            tma_load_2d(dst, &tmK, &sm.k_full[s], pc.kvh * DH, row);
+            tma_load_2d(dst + HALF, &tmK, &sm.k_full[s], pc.kvh * DH + 64, row);
+          }
+          k_iss |= 1u << s;
+          k_par = (k_par & ~(1u << s)) | (par << s);
+          ok = __all_sync(0xffffffffu, mbar_wait(&sm.v_empty[s], par ^ 1u, p.status, abort_flag));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[s], TILE_BYTES);
+          __syncwarp();
+          if (lane < npc) {
+            uint8_t* dst = sV + s * TILE_BYTES + lane * p.piece * 128;
+            tma_load_2d(dst, &tmV, &sm.v_full[s], pc.kvh * DH, row);
+            tma_load_2d(dst + HALF, &tmV, &sm.v_full[s], pc.kvh * DH + 64, row);
+          }
+          v_iss |= 1u << s;
+          v_par = (v_par & ~(1u << s)) | (par << s);
+        }
+        if (!ok) break;   // the others leave by the abort flag
+      }
+      // every issued copy lands before the CTA may exit
+      int never = 0;
+      for (int s = 0; s < 2; ++s) {
+        if (k_iss & (1u << s)) mbar_wait(&sm.k_full[s], (k_par >> s) & 1u, nullptr, &never, 100000000ull);
+        if (v_iss & (1u << s)) mbar_wait(&sm.v_full[s], (v_par >> s) & 1u, nullptr, &never, 100000000ull);
+      }
+      if constexpr (FP8) {
+        for (uint32_t u = raw > kRawStages ? raw - kRawStages : 0; u < raw; ++u)
+          mbar_wait(&sm.raw_full[u % kRawStages], (u / kRawStages) & 1, nullptr, &never, 100000000ull);
+        for (uint32_t u = scales_issued > kScaleSlots ? scales_issued - kScaleSlots : 0; u < scales_issued; ++u)
+          mbar_wait(&sm.scale_full[u % kScaleSlots], (u / kScaleSlots) & 1, nullptr, &never, 100000000ull);
+      }
+      if (seg) mbar_wait(&sm.q_full, (seg - 1) & 1u, nullptr, &never, 100000000ull);
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- UMMA issuer (lane 0)
+      if (lane == 0) {
+        const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(sK), 16, 1024),
+                       dV = sdesc_sw128(smem_u32(sV), HALF, 1024);
+        auto issue_s = [&](int x, int s) {  // S_x = Q_x K^T into TMEM columns [128 x, 128 x + 128)
+          const uint64_t qd = sdesc_add(dQ, x * TILE_BYTES), kd = sdesc_add(dK, s * TILE_BYTES);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) r4[i] = lds_f4(src + i * 1024);
+          for (int k = 0; k < DH / 16; ++k) {
+            const uint32_t off = (k >> 2) * HALF + (k & 3) * 32;
+            umma_bf16_ss(tmem_base + x * 128, sdesc_add(qd, off), sdesc_add(kd, off), IDESC_QK<FP8>, k != 0 ? 1u : 0u);
+          }
+          umma_commit(&sm.s_full[x]);
+        };
+        auto issue_pv = [&](int x, int s, bool acc) {  // O_x (+)= P_x V, P_x from TMEM over S_x
+          const uint64_t vd = sdesc_add(dV, s * TILE_BYTES);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = __byte_perm(lds_u32(fs + i * 32), 0u, u < 2 ? 0x3232 : 0x1010);
-            if (hide) {   // rows of V that no query of the tile sees (they may hold NaN codes)
+          for (int k = 0; k < 128 / 16; ++k)
+            umma_bf16_ts(tmem_base + 256 + x * 128, tmem_base + x * 128 + k * 8, sdesc_add(vd, k * 16 * 128), IDESC_PV<FP8>,
+                         (acc || k != 0) ? 1u : 0u);
+          umma_commit(&sm.o_done[x]);
+        };
+        uint32_t jb = 0, cnt[2] = {0, 0};   // blocks so far: all, and per group
+        uint32_t tiles[2] = {0, 0};         // and tiles, per group
+        bool ok = true;
+        for (uint32_t seg = 0; ok; ++seg) {
+          const TileInfo& ti = sm.tile[seg & (kTileSlots - 1)];
+          ok = mbar_wait(&sm.tile_full[seg & (kTileSlots - 1)], (seg / kTileSlots) & 1, p.status, abort_flag);
+          if (!ok || ti.toks == 0) break;
+          const int n = ti.n, gr = ti.groups;
+          ok = mbar_wait(&sm.q_full, seg & 1, p.status, abort_flag) &&
+               mbar_wait(&sm.k_full[jb & 1], (jb >> 1) & 1, p.status, abort_flag);
+          if constexpr (FP8) {   // Q in fp16
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int key = key0 + i * 8;
-                if (key > p1 || (key < lo && key >= p.g.n_meta)) r4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int x = 0; x < 2; ++x)
+              if (ok && x < gr) ok = mbar_wait(&sm.q_ready[x], tiles[x]++ & 1, p.status, abort_flag);
+          }
+          // S_x goes over the TMEM columns that the last P V of the previous tile reads
+          for (int x = 0; ok && x < gr; ++x)
+            if (cnt[x] > 0) ok = mbar_wait(&sm.o_done[x], (cnt[x] - 1) & 1, p.status, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          for (int x = 0; x < gr; ++x) issue_s(x, jb & 1);
+          umma_commit(&sm.k_empty[jb & 1]);
+          if (n == 1) umma_commit(&sm.q_empty);
+          for (int j = 0; ok && j < n; ++j, ++jb) {
+            for (int x = 0; ok && x < gr; ++x) {
+              const uint32_t par = cnt[x] & 1;
+              if (!mbar_wait(&sm.p_full[x], par, p.status, abort_flag)) { ok = false; break; }
+              if (x == 0 && !mbar_wait(&sm.v_full[jb & 1], (jb >> 1) & 1, p.status, abort_flag)) { ok = false; break; }
+              tc_fence_after();
+              issue_pv(x, jb & 1, j > 0);
+              ++cnt[x];
+              if (x == gr - 1) umma_commit(&sm.v_empty[jb & 1]);
+              if (j + 1 < n) {
+                // S_x of the next block overwrites the TMEM columns this P V reads: wait for it
+                if (!mbar_wait(&sm.o_done[x], par, p.status, abort_flag)) { ok = false; break; }
+                if (x == 0 && !mbar_wait(&sm.k_full[(jb + 1) & 1], ((jb + 1) >> 1) & 1, p.status, abort_flag)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+                issue_s(x, (jb + 1) & 1);
+                if (x == gr - 1) {
+                  umma_commit(&sm.k_empty[(jb + 1) & 1]);
+                  if (j + 2 == n) umma_commit(&sm.q_empty);
+                }
               }
             }
+          }
+        }
+        umma_commit(&sm.mma_done);
+        int never = 0;
+        mbar_wait(&sm.mma_done, 0, nullptr, &never, 100000000ull);
+      }
+    } else {
+      // ---------------------------------------------------------------- e4m3 -> fp16 (two warps)
+      if constexpr (FP8) {
+        const int t = threadIdx.x - 2 * 32;   // of 64
+        uint32_t jb = 0, raw = 0;
+        bool ok = true;
+        for (uint32_t seg = 0; ok; ++seg) {
+          const volatile TileInfo& ti = sm.tile[seg & (kTileSlots - 1)];
+          ok = __all_sync(0xffffffffu, mbar_wait(&sm.tile_full[seg & (kTileSlots - 1)], (seg / kTileSlots) & 1, p.status,
+                                                 abort_flag));
+          if (!ok || ti.toks == 0) break;
+          const int n = ti.n, p1 = ti.p1, lo = p.g.window < 0 ? 0 : ti.p0 - p.g.window;
+          uint32_t most[2] = {0, 0};   // the largest of K's and of V's scales so far, as bits
+          for (int j = 0; ok && j < n; ++j, ++jb) {
+            const uint32_t s = jb & 1, par = (jb >> 1) & 1, slot = jb % kScaleSlots, slot_par = (jb / kScaleSlots) & 1;
+            BlockInfo& bi = sm.block[jb & (kBlockSlots - 1)];
+            if (warp == 2) {
+              // the scales as the products use them (see Smem), 0 for rows that no query of the tile sees.
+              // Done before k_full, so that S of the block implies it.
+              ok = __all_sync(0xffffffffu, mbar_wait(&sm.scale_full[slot], slot_par, p.status, abort_flag));
+              if (!ok) break;
+              const uint32_t valid = bi.valid[lane >> 3] >> ((lane & 7) * 4);
+              const int key0 = bi.k0 + lane * 4;
+              uint32_t seen = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t w[4] = {__float_as_uint(r4[i].x), __float_as_uint(r4[i].y), __float_as_uint(r4[i].z),
-                                     __float_as_uint(r4[i].w)};
-              uint32_t h[8];
+              for (int e = 0; e < 4; ++e)
+                if (((valid >> e) & 1u) && key0 + e <= p1 && (key0 + e >= lo || key0 + e < p.g.n_meta)) seen |= 1u << e;
+              float4& k4 = *reinterpret_cast<float4*>(&sm.scale[slot][0][lane * 4]);
+              float4& v4 = *reinterpret_cast<float4*>(&sm.scale[slot][1][lane * 4]);
+              float k[4] = {k4.x, k4.y, k4.z, k4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w}, up[2];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const uint32_t x = f16_of_e4m3(w[e >> 1], e & 1);
-                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&f[i]));
-                h[e] = *reinterpret_cast<const uint32_t*>(&y);
+              for (int e = 0; e < 4; ++e) {
+                if (!((seen >> e) & 1u)) k[e] = v[e] = 0.f;
+                most[0] = max(most[0], __float_as_uint(k[e]) & 0x7fffffffu);
+                most[1] = max(most[1], __float_as_uint(v[e]) & 0x7fffffffu);
               }
-              sts_u32x4(at0 + i * 1024, h[0], h[1], h[2], h[3]);
-              sts_u32x4(at1 + i * 1024, h[4], h[5], h[6], h[7]);
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                most[w] = __reduce_max_sync(0xffffffffu, most[w]);
+                // every scale is below 2^ex
+                const int ex = max(static_cast<int>(most[w] >> 23) - 126, w ? kUp - 127 : kUp - kMostUp);
+                up[w] = pow2(kUp - ex);
+                if (lane == 0) (w ? bi.ev : bi.ek) = ex;
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t kb = __float_as_uint(k[e]);
+                const __half2 h = __floats2half2_rn(v[e] * up[1], __uint_as_float(kb & 0x7f800000u) * up[0]);
+                v[e] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h));
+                k[e] = __uint_as_float((kb & 0x7fffffu) | 0x3f800000u);
+              }
+              k4 = make_float4(k[0], k[1], k[2], k[3]);
+              v4 = make_float4(v[0], v[1], v[2], v[3]);
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sm.scale_ready[slot]);
             }
-            fence_proxy_async_smem();
-            // only now: an arrival right behind the loads can overtake them, and the next copy would
-            // land in what they still read
-            mbar_arrive(&sm.raw_empty[rs]);
-            mbar_arrive(u < 2 ? &sm.k_full[s] : &sm.v_full[s]);
+            ok = __all_sync(0xffffffffu, mbar_wait(&sm.scale_ready[slot], slot_par, p.status, abort_flag));
+#pragma unroll 1
+            for (int u = 0; ok && u < 4; ++u, ++raw) {
+              const uint32_t rs = raw % kRawStages;
+              if ((u & 1) == 0)
+                ok = __all_sync(0xffffffffu, mbar_wait(u ? &sm.v_empty[s] : &sm.k_empty[s], par ^ 1u, p.status, abort_flag));
+              ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.raw_full[rs], (raw / kRawStages) & 1, p.status, abort_flag));
+              if (!ok) break;
+              // 16 codes (one of a row's eight chunks) at a time, to two 16-byte chunks of the swizzled
+              // tile.  The lanes of a row's upper half take the neighbouring row, so that eight lanes
+              // meet no bank twice in either tile.
+              const int up = (t >> 2) & 1, row0 = (t >> 3) ^ up, c = (t & 3) * 2;
+              const uint32_t src = smem_u32(sRaw + rs * kRawBytes) + row0 * DH + (t & 7) * 16;
+              const uint32_t dst = smem_u32((u < 2 ? sK : sV) + s * TILE_BYTES + up * HALF + ((u & 1) * 64 + row0) * 128);
+              const uint32_t fs = smem_u32(&sm.scale[slot][1][(u & 1) * 64 + row0]);
+              const uint32_t at0 = dst + ((c ^ row0) << 4), at1 = dst + (((c + 1) ^ row0) << 4);   // row & 7 = row0
+              const bool hide = u >= 2 && (bi.flags & kZeroV);
+              const int key0 = bi.k0 + (u & 1) * 64 + row0;
+#pragma unroll 1
+              for (int i0 = 0; i0 < 8; i0 += 4) {   // (eight at a time: 98 us against 93, see kRegs)
+                float4 r4[4];   // in flight before the first is used
+                uint32_t f[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r4[i] = lds_f4(src + (i0 + i) * 1024);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = __byte_perm(lds_u32(fs + (i0 + i) * 32), 0u, u < 2 ? 0x3232 : 0x1010);
+                if (hide) {   // rows of V that no query of the tile sees (they may hold NaN codes)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const int key = key0 + (i0 + i) * 8;
+                    if (key > p1 || (key < lo && key >= p.g.n_meta)) r4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                  }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const uint32_t w[4] = {__float_as_uint(r4[i].x), __float_as_uint(r4[i].y), __float_as_uint(r4[i].z),
+                                         __float_as_uint(r4[i].w)};
+                  uint32_t h[8];
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) {
+                    const uint32_t x = f16_of_e4m3(w[e >> 1], e & 1);
+                    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&f[i]));
+                    h[e] = *reinterpret_cast<const uint32_t*>(&y);
+                  }
+                  sts_u32x4(at0 + (i0 + i) * 1024, h[0], h[1], h[2], h[3]);
+                  sts_u32x4(at1 + (i0 + i) * 1024, h[4], h[5], h[6], h[7]);
+                }
+              }
+              fence_proxy_async_smem();
+              // only now: an arrival right behind the loads can overtake them, and the next copy would
+              // land in what they still read
+              mbar_arrive(&sm.raw_empty[rs]);
+              mbar_arrive(u < 2 ? &sm.k_full[s] : &sm.v_full[s]);
+            }
           }
         }
       }
     }
   } else {
+    if constexpr (FP8) reg_inc<kRegsSoft>();
     // ------------------------------------------------------------------ softmax (two groups of 8 warps)
-    const int x = (warp - 2) >> 3;         // row group
-    const int kh = ((warp - 2) >> 2) & 1;  // half of the keys and of O's columns
+    const int x = (warp - kSoft) >> 3;         // row group
+    const int kh = ((warp - kSoft) >> 2) & 1;  // half of the keys and of O's columns
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tSx = tmem_base + x * 128 + lane_off, tOx = tmem_base + 256 + x * 128 + lane_off + kh * 64;
@@ -682,7 +700,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
           if (!FP8 && (flags & kZeroV)) {
             // rows of V that no query of the tile sees: [a0, a1) between the meta rows and the
             // window, [b0, 128) behind the last query
-            const int k0 = bi.k0, tid = (warp - 2 - 8 * x) * 32 + lane;
+            const int k0 = bi.k0, tid = (warp - kSoft - 8 * x) * 32 + lane;
             const int a0 = max(0, p.g.n_meta - k0);
             const int a1 = min(kKeyBlock, p.g.window < 0 ? 0 : ti.p0 - p.g.window - k0), b0 = max(0, ti.p1 + 1 - k0);
             ok = __all_sync(0xffffffffu, mbar_wait(&sm.v_full[jb & 1], (jb >> 1) & 1, p.status, abort_flag));
@@ -846,6 +864,13 @@ cudaError_t launch_paged_attention_tc(const PagedAttnDesc& a, cudaStream_t st) {
   if (cudaError_t e = fp8 ? smem_attr_once(paged_attn_tc<true>, smem_bytes<true>(), attr8_done)
                           : smem_attr_once(paged_attn_tc<false>, smem_bytes<false>(), attr_done))
     return e;
+  if (fp8) {   // the registers that the softmax warps ask for have to be there: the others would wait for good
+    static const bool have = [] {
+      cudaFuncAttributes at;
+      return cudaFuncGetAttributes(&at, paged_attn_tc<true>) == cudaSuccess && at.numRegs >= kRegs;
+    }();
+    if (!have) return cudaErrorInvalidConfiguration;
+  }
   const int ctas = num_sms() < kMaxCtas ? num_sms() : kMaxCtas;
   PagedAttnParams p{};
   p.kv = a.kv;
