@@ -1,11 +1,12 @@
 // api_serve.cu -- the serving part of the C ABI (include/hymba.h): argument checks of the
 // paged K/V cache, its attention and the 4-bit weight products, and their launches.
-#include "hy_kernels.h"
+#include "hy_serve.h"
 #include "hymba.h"
 
 namespace {
 
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+inline bool aligned_to(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+inline bool aligned16(const void* p) { return aligned_to(p, 16); }
 inline int esize(hymba_dtype_t t) { return t == HYMBA_BF16 ? 2 : 4; }
 inline bool valid_dtype(hymba_dtype_t t) { return t == HYMBA_BF16 || t == HYMBA_F32; }
 
@@ -42,13 +43,14 @@ hymba_status_t check_cache(const hymba_paged_kv_t* kv, hymba_dtype_t dtype) {
       static_cast<long long>(kv->table_ld) * ps > (1ll << 30) ||
       static_cast<long long>(kv->n_kv_heads) * kv->head_dim > (1 << 16))
     return HYMBA_ERR_UNSUPPORTED;
-  if (!aligned16(kv->pages) || (kv->cache_type == HYMBA_CACHE_E4M3 && !aligned16(kv->scales)))
+  if (!aligned16(kv->pages) || !aligned_to(kv->page_table, 4) || (kv->cache_type == HYMBA_CACHE_E4M3 && !aligned16(kv->scales)))
     return HYMBA_ERR_UNSUPPORTED;
   return HYMBA_OK;
 }
 
 hymba_status_t check_batch(int batch, const int* q_start, const int* kv_len, int total_rows) {
-  return batch < 1 || !q_start || !kv_len || total_rows < 0 ? HYMBA_ERR_INVALID_ARG : HYMBA_OK;
+  if (batch < 1 || !q_start || !kv_len || total_rows < 0) return HYMBA_ERR_INVALID_ARG;
+  return aligned_to(q_start, 4) && aligned_to(kv_len, 4) ? HYMBA_OK : HYMBA_ERR_UNSUPPORTED;
 }
 
 hymba_status_t check_workspace(const void* workspace, size_t ws_bytes, size_t need) {
@@ -90,7 +92,7 @@ hymba_status_t check_w4(const void* w, const void* q4, const float* scales, int 
                         hymba_dtype_t dtype) {
   if (!w || !q4 || !scales || N < 1 || K < 1 || group < 1 || !valid_dtype(dtype)) return HYMBA_ERR_INVALID_ARG;
   if ((group != 32 && group != 64 && group != 128) || K % group || N > (1 << 30) || K > (1 << 30) || !aligned16(w) || !aligned16(q4) ||
-      (reinterpret_cast<uintptr_t>(scales) & 3))
+      !aligned_to(scales, 4))
     return HYMBA_ERR_UNSUPPORTED;
   return HYMBA_OK;
 }
@@ -181,7 +183,7 @@ hymba_status_t hymba_gemm_w4(const void* a, const void* w_q4, const float* scale
   hymba_status_t s = check_w4(a, w_q4, scales, N, K, group, dtype);
   if (s != HYMBA_OK) return s;
   if (!c || M < 1) return HYMBA_ERR_INVALID_ARG;
-  if (M > 16) return HYMBA_ERR_UNSUPPORTED;
+  if (M > 16 || !aligned_to(c, esize(dtype))) return HYMBA_ERR_UNSUPPORTED;
   if ((s = check_device(w_q4)) != HYMBA_OK) return s;
   return cuda_status(hy::launch_gemm_w4(a, w_q4, scales, c, M, N, K, group, dtype == HYMBA_BF16,
                                         static_cast<cudaStream_t>(stream)));

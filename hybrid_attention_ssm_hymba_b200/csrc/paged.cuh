@@ -6,7 +6,7 @@
 #include <cuda_fp8.h>
 
 #include "hy_common.cuh"
-#include "hy_kernels.h"
+#include "hy_serve.h"
 
 namespace hy {
 

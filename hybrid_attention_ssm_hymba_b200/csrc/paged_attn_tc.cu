@@ -26,6 +26,15 @@
 //               and more below its largest value.
 // TMEM (512 columns): S_a | S_b | O_a | O_b; P in 16 bits over the consumed S columns.
 //
+// Bound by the round of a group: S (tensor core), softmax, P V, one after another, with the other
+// group's round half a turn behind.  4096 rows of 16 heads over 32K bf16 rows: 970 us, 1066 TFLOP/s,
+// 64 % of the measured bf16 rate; of a round's 4100 cycles the softmax takes 1900 and the tensor core
+// 2050 for both groups.  e4m3 rows: 1306 us; reading K's scales and converting share the shared
+// memory with the products.  Nine ragged sequences of up to 1604 e4m3 rows in a window of 1024 (16
+// blocks a CTA): 93 us, of which 16 blocks take 51; starting up, and per tile Q's conversion, the
+// first S and the output take the rest.  A third group per CTA has no TMEM left, and one group with
+// twice the keys would read every K/V row twice as often.
+//
 // Rows of V that no query of the tile sees (behind the sequence, between the meta rows and
 // the window) may hold NaN, and 0 x NaN would reach every output: page pieces of such rows
 // are loaded from beyond the tensor map (zeros), and in a partly visible piece the softmax
@@ -64,7 +73,9 @@ struct BlockInfo {
 };
 constexpr uint32_t kZeroV = 4u;
 
-constexpr int kPlanBatch = 64;   // batches up to this are planned by every CTA itself
+// Batches up to this are planned by every CTA itself (4 sequences of 40 rows in a window of 1024: 24 us,
+// with the plan kernel 32; 64 of 17 rows 61 and 70); the 8-bit path's tiles leave no room for many more.
+constexpr int kPlanBatch = 64;
 template <bool FP8> struct Smem;
 template <> struct Smem<true>;   // with the scales and barriers of the 8-bit path, below
 template <> struct Smem<false> {   // behind the six tiles
@@ -881,7 +892,6 @@ cudaError_t launch_paged_attention_tc(const PagedAttnDesc& a, cudaStream_t st) {
   p.g.n_meta = a.n_meta;
   p.g.window = a.window;
   p.part_rows = tc_part_rows(a.rb, p.g.G);
-  p.min_blocks = 2;
   const PagedScratch L = paged_scratch_layout(a.rb.batch, kMaxCtas, p.part_rows, DH);
   uint8_t* sc = static_cast<uint8_t*>(a.scratch);
   p.prefix = reinterpret_cast<long long*>(sc + L.prefix);

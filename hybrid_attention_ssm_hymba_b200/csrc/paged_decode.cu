@@ -18,7 +18,10 @@
 //          by one byte permutation, and P's 8 x 8 pieces are transposed between the lanes.
 // A CTA of four warps takes 32 keys of each 128-key block per warp and walks its part of the
 // line of blocks (paged_plan.cuh).  K of the next step is loaded as soon as K Q^T has read this
-// one's, V as soon as V^T P^T has, page numbers two steps and scales one step earlier.
+// one's, V as soon as V^T P^T has, page numbers two steps and scales one step earlier.  16 long e4m3
+// histories (348 MB): 69 us, 5.0 TB/s, 77 % of the measured copy rate, three CTAs an SM with 27 million
+// warp instructions in 40 % of the issue slots.  4 rows in a window of 1024: 11.8 us, of which the bytes
+// are 1.4; the rest is two launches, the plan, a page number's, a row's and the join's way from memory.
 //
 // e4m3 codes are exact in fp16, one conversion for two of them, so the 8-bit products run in
 // fp16 with their ranges kept by powers of two: a row of Q is scaled to at most 2^8 (its bf16
@@ -30,7 +33,9 @@ namespace hy {
 namespace {
 
 constexpr int DH = 128, kWarps = 4, kRows = 16;
-constexpr int kPlanBatch = 1024;   // batches up to this are planned by every CTA itself
+// Batches up to this are planned by every CTA itself (4 rows in a window of 1024: 11.8 us, with the
+// plan kernel 18.8; 1000 of them 372 and 396).
+constexpr int kPlanBatch = 1024;
 constexpr float kLazy = 7.f;       // a maximum moves when it is exceeded by 2^7: n_j stays below 2^15
 constexpr float kLazySum = 60.f;   // the same for a sum in fp32
 constexpr float kUp = 8.f;         // the exponent added to n_j
@@ -542,14 +547,16 @@ __global__ void __launch_bounds__(256) paged_join_rows(const __grid_constant__ P
   }
 }
 
-// CTAs per SM that the registers allow, with one and with two tiles of queries.
+// CTAs per SM that the registers allow, with one and with two tiles of queries.  One where it holds
+// the rows: 16 long e4m3 histories 69 us, with two tiles 88.
 constexpr int kPerSm[2] = {3, 2};
 constexpr int kMaxSms = 148;   // the scratch is sized for the B200
 int query_tiles(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads) { return rb.max_rows * (n_q_heads / kv.hkv) <= 8 ? 1 : 2; }
 
 }  // namespace
 
-// Whether this kernel takes the call: the rows of one K/V head fit one product's 16.
+// Whether this kernel takes the call: the rows of one K/V head fit two products' 16 columns (4 rows
+// in a window of 1024: 11.8 us, on the tensor-core kernel 16.0; 16 long e4m3 histories 69 and 205).
 bool paged_decode_takes(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads) {
   return static_cast<long long>(rb.max_rows) * (n_q_heads / kv.hkv) <= kRows;
 }
@@ -569,7 +576,6 @@ cudaError_t launch_paged_decode(const PagedAttnDesc& a, cudaStream_t st) {
   p.g.window = a.window;
   const int nt = query_tiles(a.kv, a.rb, a.n_q_heads);
   p.part_rows = 8 * nt;
-  p.min_blocks = 1;
   p.page_shift = page_shift(a.kv.page_size);
   const PagedScratch L = paged_scratch_layout(a.rb.batch, kPerSm[nt - 1] * kMaxSms, p.part_rows, DH);
   uint8_t* sc = static_cast<uint8_t*>(a.scratch);

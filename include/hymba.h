@@ -424,8 +424,10 @@ HYMBA_API hymba_status_t hymba_rmsnorm(const void* x, void* y, int rows, int d, 
  * HYMBA_CACHE_E4M3 holds, per (row, K/V head), e4m3 codes and one fp32 scale over the head's
  * dh elements:
  *   scale = max(amax / 448, 2^-126);  code = e4m3(x * (1 / scale)), nearest even;  value = code * scale
- * (a row with a NaN or an infinity has a NaN or infinite scale and reads back as NaN throughout;
- * codes written by other means hold no NaN code, 0x7f or 0xff).
+ * (a row with a NaN or an infinity has a NaN or infinite scale and reads back as NaN throughout; a
+ * NaN code, 0x7f or 0xff, written by other means is a NaN; scales are not negative).
+ * Limits: n_pages * page_size < 2^31, table_ld * page_size <= 2^30, Hkv*dh <= 2^16, Hq*dh <= 2^19,
+ * total_rows * Hq < 2^31.
  */
 typedef enum { HYMBA_CACHE_F32 = 0, HYMBA_CACHE_BF16 = 1, HYMBA_CACHE_E4M3 = 2 } hymba_cache_type_t;
 
@@ -493,7 +495,8 @@ HYMBA_API hymba_status_t hymba_paged_attention(const void* q, int q_ld, const hy
  * consecutive k, with q in [-8, 7]:  w[n, k] = q[n, k] * scales[n, k / group].
  *   w_q4    [N, K/2] bytes: byte i of a row holds q[2i] + 8 in its low, q[2i + 1] + 8 in its high nibble
  *   scales  [N, K/group] fp32
- * K a multiple of group; w, a and w_q4 16-byte aligned.
+ * K a multiple of group, N and K at most 2^30; w, a and w_q4 16-byte aligned, scales and c to their
+ * elements.
  * hymba_quantize_w4:   scale = max(amax / 7, 2^-126), q = 7 w / amax to the nearest integer (ties to
  *                      even); a group's weights must be finite
  * hymba_dequantize_w4: w = q * scale rounded to dtype (the weights of a product with many rows)

@@ -96,6 +96,17 @@ def test_bad_w4_rows():
         assert H.hymba_gemm_w4(P, P, P, c, m, 16, 128, 64, H.HYMBA_BF16, stream=0) == status
 
 
+def test_pointers_off_their_elements():
+    """A load or store of an element at such an address would fault."""
+    assert H.hymba_paged_kv_read(_kv(page_table=P + 2), P, P, 256, 2, P, P, 5, H.HYMBA_BF16, P, 256, stream=0) == UNSUPPORTED
+    for q_start, kv_len in ((P + 2, P), (P, P + 1)):
+        assert H.hymba_paged_kv_append(_kv(), P, P, 256, 2, q_start, kv_len, 5, H.HYMBA_BF16, P, 256, stream=0) == UNSUPPORTED
+        assert H.hymba_paged_attention(P, 512, _kv(), P, 512, 2, q_start, kv_len, 5, 3, 4, 8, 64, H.HYMBA_BF16, P, 1 << 40,
+                                       stream=0) == UNSUPPORTED
+    for c, dtype in ((P + 1, H.HYMBA_BF16), (P + 2, H.HYMBA_F32)):
+        assert H.hymba_gemm_w4(P, P, P, c, 4, 16, 128, 64, dtype, stream=0) == UNSUPPORTED
+
+
 def test_workspace_sizes_are_bounded():
     """The scratch does not grow with the histories, and covers one-row and long chunks."""
     for most, total in ((1, 64), (40, 400), (8192, 20000)):
