@@ -125,15 +125,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 def _ptr(t) -> Optional[int]:
-    if t is None:
-        return None
-    if isinstance(t, int):
+    try:
+        return t.data_ptr()
+    except AttributeError:   # None or an address
         return t
-    return t.data_ptr()
 
 
 def _nbytes(t) -> int:
-    return t.numel() * t.element_size()
+    return t.nbytes
 
 
 _current_stream = None   # () -> the handle of torch's current stream, once CUDA is there
@@ -146,7 +145,8 @@ def _stream(stream) -> Optional[int]:
             import torch
             if not torch.cuda.is_available():
                 return None
-            raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
             # the handle alone: building a torch.cuda.Stream around it takes 3 us of every call
             _current_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
         return _current_stream()

@@ -423,17 +423,17 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
           const int n = ti.n, gr = ti.groups;
           ok = mbar_wait(&sm.q_full, seg & 1, p.status, abort_flag) &&
                mbar_wait(&sm.k_full[jb & 1], (jb >> 1) & 1, p.status, abort_flag);
-          if constexpr (FP8) {   // Q in fp16
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-              if (ok && x < gr) ok = mbar_wait(&sm.q_ready[x], tiles[x]++ & 1, p.status, abort_flag);
+          // one group after the other, so that the first begins while the second still has its last tile's
+          // output to write: S_x needs Q_x (FP8: in fp16), and the last P V of the previous tile, which
+          // reads the TMEM columns that S_x goes over, done
+          for (int x = 0; ok && x < gr; ++x) {
+            if constexpr (FP8) ok = mbar_wait(&sm.q_ready[x], tiles[x]++ & 1, p.status, abort_flag);
+            if (ok && cnt[x] > 0) ok = mbar_wait(&sm.o_done[x], (cnt[x] - 1) & 1, p.status, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(x, jb & 1);
           }
-          // S_x goes over the TMEM columns that the last P V of the previous tile reads
-          for (int x = 0; ok && x < gr; ++x)
-            if (cnt[x] > 0) ok = mbar_wait(&sm.o_done[x], (cnt[x] - 1) & 1, p.status, abort_flag);
           if (!ok) break;
-          tc_fence_after();
-          for (int x = 0; x < gr; ++x) issue_s(x, jb & 1);
           umma_commit(&sm.k_empty[jb & 1]);
           if (n == 1) umma_commit(&sm.q_empty);
           for (int j = 0; ok && j < n; ++j, ++jb) {
