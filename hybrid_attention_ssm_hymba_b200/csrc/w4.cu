@@ -97,12 +97,14 @@ __global__ void __launch_bounds__(256) dequantize_w4_kernel(const uint32_t* __re
 // split into three bf16 columns (8 + 8 + 8 of the 24 bits), which are summed at the end.
 //
 // A CTA of 16 warps owns a range of 16-row tiles and takes K in slabs whose columns of A fit
-// shared memory, already in the order of the products.  The S warps of a group share a tile:
-// each streams chunks of 256 k (16 rows x 128 bytes) through a ring of its own by cp.async, and
-// their sums meet in shared memory at the tile's end.  Eight rows against 16384 x 8192: 24.6 us
-// (3.1 TB/s, 47 % of the measured copy rate); the stream alone takes 14 us, taking the nibbles apart
-// and the products alone 20, at four warps an SM quarter that issue in half of the cycles.  One row
-// against 2048 x 5632: 5.9 us, a launch and one chunk's way.
+// shared memory, already in the order of the products.  The chunks of 256 k (16 rows x 128 bytes) of
+// all its tiles are shared out evenly: each warp streams its own through a ring of its own by cp.async,
+// and the parts of a tile meet in shared memory at the slab's end, in the warps' order.  Eight rows
+// against 16384 x 8192: 26.9 us (2.8 TB/s, 43 % of the measured copy rate), 23.8 with the weights in
+// L2.  (Each tile shared by two warps, the best fixed number there: 26.3 and 24.6; but four rows against
+// 11264 x 5632 then took 18.9 us against 15.4, for every CTA had a whole number of rounds.)  The stream
+// alone takes 14 us, taking the nibbles apart and the products alone 20, at four warps an SM quarter
+// that issue in half of the cycles.  One row against 2048 x 5632: 5.6 us, a launch and a chunk's way.
 //
 // The 32 k of 16 bytes of a row are one or part of one group; lane (g, t) takes 4 of them
 // (8 k) of rows g and g + 8.  A word's nibbles i and i + 4 make one bf16 pair: (word >> 4 i)
@@ -114,15 +116,17 @@ struct GemmW4Params {
   const uint8_t* q4;
   const float* scales;
   void* c;
-  int M, N, K, tiles, slab, S;   // slab: k of one pass; S: warps that share a tile
+  int M, N, K, tiles, slab;   // slab: k of one pass
 };
 
 template <int NT> struct W4Shape {
   static constexpr int ring = NT <= 2 ? 3 : 2;
   static constexpr int slab = NT == 1 ? 4096 : NT == 2 ? 2048 : NT == 3 ? 1024 : 512;
   static constexpr int x_bytes = slab / 32 * NT * 8 * 64;
-  static constexpr int stage = 16 * kRowPitch + 16 * 8 * 4;      // codes, then scales [row][8]
-  static constexpr int red_bytes = kWarps * 16 * 8 * NT * 4;
+  static constexpr int part = 16 * 8 * NT;                       // a tile's sums
+  static constexpr int chunk_bytes = 16 * kRowPitch + 16 * 8 * 4;   // codes, then scales [row][8]
+  static constexpr int stage = chunk_bytes > part * 4 ? chunk_bytes : part * 4;
+  static constexpr int red_bytes = kWarps * part * 4;
   static constexpr int acc_bytes = kTileRowsMax * 8 * NT * 4;
   static constexpr int smem = x_bytes + kWarps * ring * stage + red_bytes + acc_bytes;
 };
@@ -164,26 +168,24 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_co
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int tile0 = static_cast<int>(static_cast<long long>(blockIdx.x) * p.tiles / gridDim.x),
             tile1 = static_cast<int>(static_cast<long long>(blockIdx.x + 1) * p.tiles / gridDim.x);
-  const int grp = warp / p.S, ws = warp - grp * p.S, groups = kWarps / p.S;
-  const int my_tiles = (tile1 - tile0 - grp + groups - 1) / groups;   // tiles tile0 + grp, + groups, ...
+  const int tiles = tile1 - tile0;                                    // at most eight
   constexpr int per_chunk = kChunk >> GS, kLog = 8 - GS;              // scales of a row and chunk
   const long long row_bytes = p.K / 2, row_scales = p.K >> GS;
-  // the warps of a tile (a barrier of theirs: at most eight groups of two or more)
-  auto meet = [&] {
-    if (p.S == 1) __syncwarp();
-    else bar_sync_n(1 + grp, 32 * p.S);
-  };
   const uint32_t my_ring = smem_u32(ring + warp * W::ring * W::stage);
   pdl_trigger();
   pdl_wait();
   for (int k0 = 0; k0 < p.K; k0 += p.slab) {
     const int ks = min(p.slab, p.K - k0), chunks = (ks + kChunk - 1) / kChunk;
-    const int cpw = ws < chunks ? (chunks - ws + p.S - 1) / p.S : 0;   // chunks of this warp per tile
-    // the next chunk to fetch: its tile (of this group), its number in the tile, its slot
-    int ft = 0, fc = 0, fs = 0;
+    // the CTA's chunks, tile by tile, in equal shares; a share is no longer than a tile (eight tiles and
+    // sixteen warps), so it is the end of one tile and the beginning of the next at most
+    const int all = tiles * chunks, share = (all + kWarps - 1) / kWarps;
+    const int begin = min(warp * share, all), end = min(begin + share, all);
+    // the next chunk to fetch: its tile, its number in the tile, its slot
+    int fi = begin, ft = begin / chunks, fc = begin - ft * chunks, fs = 0;
+    int chunk = fc;   // and to compute
     auto fetch = [&]() {
-      if (ft < my_tiles && cpw > 0) {
-        const int kc = (ws + fc * p.S) * kChunk + k0, n0 = (tile0 + grp + ft * groups) * 16;
+      if (fi < end) {
+        const int kc = fc * kChunk + k0, n0 = (tile0 + ft) * 16;
         const uint32_t dst = my_ring + fs * W::stage, dq = dst + (lane >> 3) * kRowPitch + (lane & 7) * 16;
         const int k = kc + (lane & 7) * 32;
         if (n0 + 16 <= p.N && kc + kChunk <= p.K) {   // eight lanes: the 128 bytes of a row
@@ -206,7 +208,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_co
                       have);
           }
         }
-        if (++fc == cpw) {
+        ++fi;
+        if (++fc == chunks) {
           fc = 0;
           ++ft;
         }
@@ -217,7 +220,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_co
 #pragma unroll
     for (int i = 0; i + 1 < W::ring; ++i) fetch();
     // the slab's columns of A, in the products' order: x0 x4 x1 x5 x2 x6 x3 x7 of each eight
-    __syncthreads();   // (the previous slab's are no longer read)
+    __syncthreads();   // (the previous slab's, and its parts, are no longer read)
     constexpr int kColWarps = NT * 8 >= kWarps ? 1 : 2;   // warps that share a column
     for (int col = warp / kColWarps; col < NT * 8; col += kWarps / kColWarps) {
       const int m = col / kSplit, part = col - m * kSplit;
@@ -250,70 +253,86 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_co
       }
     }
     __syncthreads();
+    constexpr int kPart = W::part;
     int slot = 0;
-    for (int ti = 0; ti < my_tiles; ++ti) {
-      float sum[NT][4], part[NT][4];
+    float sum[NT][4], part[NT][4];
+    auto clear = [&] {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[n][e] = 0.f;
-      for (int c = 0; c < cpw; ++c) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(W::ring - 2) : "memory");
-        __syncwarp();   // every lane's pieces of this chunk are there, and the next slot is free
-        fetch();
-        const uint32_t st = my_ring + slot * W::stage, codes = st + g * kRowPitch + t * 4;
-        const uint32_t sc = st + 16 * kRowPitch + g * 32;
-        slot = slot + 1 == W::ring ? 0 : slot + 1;
-        const uint32_t xk = smem_u32(sx) + (((ws + c * p.S) * (kChunk / 32) * NT * 8 + g) * 4 + t) * 16;
-#pragma unroll
-        for (int q = 0; q < kChunk / 32; ++q) {
-          const uint32_t u0 = lds_u32(codes + q * 16), u1 = lds_u32(codes + 8 * kRowPitch + q * 16);
-          const uint32_t a0[4] = {q_pair(u0, 0), q_pair(u1, 0), q_pair(u0, 1), q_pair(u1, 1)};
-          const uint32_t a1[4] = {q_pair(u0, 2), q_pair(u1, 2), q_pair(u0, 3), q_pair(u1, 3)};
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const float4 x = lds_f4(xk + (q * NT + n) * 512);
-            if ((q * 32) % (1 << GS) == 0) {   // a group begins
-#pragma unroll
-              for (int e = 0; e < 4; ++e) part[n][e] = 0.f;
-            }
-            mma_bf16(part[n], a0, __float_as_uint(x.x), __float_as_uint(x.y));
-            mma_bf16(part[n], a1, __float_as_uint(x.z), __float_as_uint(x.w));
-          }
-          if ((q * 32 + 32) % (1 << GS) == 0) {   // the group is complete
-            const float s0 = lds_f32(sc + (q * 32 >> GS) * 4), s1 = lds_f32(sc + 8 * 32 + (q * 32 >> GS) * 4);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) sum[n][e] = fmaf(part[n][e], e < 2 ? s0 : s1, sum[n][e]);
-          }
-        }
-      }
-      // the warps of the tile
+    };
+    auto put = [&](float* dst) {   // [row][column]
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<float2*>(&red[(warp * 16 + g + 8 * h) * 8 * NT + n * 8 + 2 * t]) =
-              make_float2(sum[n][2 * h], sum[n][2 * h + 1]);
-      meet();
-      const int tl = grp + ti * groups;   // tile of the CTA
-      const bool first = k0 == 0, last = k0 + p.slab >= p.K;
-      for (int i = threadIdx.x - grp * 32 * p.S; i < 16 * 8 * NT; i += 32 * p.S) {
-        float v = first ? 0.f : acc[tl * 16 * 8 * NT + i];
-        for (int w = 0; w < p.S; ++w) v += red[(grp * p.S + w) * 16 * 8 * NT + i];
-        if (!last || kSplit > 1) acc[tl * 16 * 8 * NT + i] = v;
-        const int n = (tile0 + tl) * 16 + i / (8 * NT), m = i % (8 * NT);
-        if (last && kSplit == 1 && n < p.N && m < p.M)
-          static_cast<T*>(p.c)[static_cast<long long>(m) * p.N + n] = from_f<T>(v * kQUp);
-      }
-      meet();
-      if (last && kSplit > 1)
-        for (int i = threadIdx.x - grp * 32 * p.S; i < 16 * p.M; i += 32 * p.S) {
-          const int r = i / p.M, m = i - r * p.M, n = (tile0 + tl) * 16 + r;
-          const float* v = &acc[(tl * 16 + r) * 8 * NT + m * kSplit];
-          if (n < p.N) static_cast<T*>(p.c)[static_cast<long long>(m) * p.N + n] = from_f<T>(((v[2] + v[1]) + v[0]) * kQUp);
+          *reinterpret_cast<float2*>(&dst[(g + 8 * h) * 8 * NT + n * 8 + 2 * t]) = make_float2(sum[n][2 * h], sum[n][2 * h + 1]);
+    };
+    clear();
+    for (int i = begin; i < end; ++i) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(W::ring - 2) : "memory");
+      __syncwarp();   // every lane's pieces of this chunk are there, and the next slot is free
+      fetch();
+      const uint32_t st = my_ring + slot * W::stage, codes = st + g * kRowPitch + t * 4;
+      const uint32_t sc = st + 16 * kRowPitch + g * 32;
+      slot = slot + 1 == W::ring ? 0 : slot + 1;
+      const uint32_t xk = smem_u32(sx) + ((chunk * (kChunk / 32) * NT * 8 + g) * 4 + t) * 16;
+#pragma unroll
+      for (int q = 0; q < kChunk / 32; ++q) {
+        const uint32_t u0 = lds_u32(codes + q * 16), u1 = lds_u32(codes + 8 * kRowPitch + q * 16);
+        const uint32_t a0[4] = {q_pair(u0, 0), q_pair(u1, 0), q_pair(u0, 1), q_pair(u1, 1)};
+        const uint32_t a1[4] = {q_pair(u0, 2), q_pair(u1, 2), q_pair(u0, 3), q_pair(u1, 3)};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float4 x = lds_f4(xk + (q * NT + n) * 512);
+          if ((q * 32) % (1 << GS) == 0) {   // a group begins
+#pragma unroll
+            for (int e = 0; e < 4; ++e) part[n][e] = 0.f;
+          }
+          mma_bf16(part[n], a0, __float_as_uint(x.x), __float_as_uint(x.y));
+          mma_bf16(part[n], a1, __float_as_uint(x.z), __float_as_uint(x.w));
         }
+        if ((q * 32 + 32) % (1 << GS) == 0) {   // the group is complete
+          const float s0 = lds_f32(sc + (q * 32 >> GS) * 4), s1 = lds_f32(sc + 8 * 32 + (q * 32 >> GS) * 4);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[n][e] = fmaf(part[n][e], e < 2 ? s0 : s1, sum[n][e]);
+        }
+      }
+      if (++chunk == chunks && i + 1 < end) {   // on to the next tile
+        put(red + warp * kPart);
+        clear();
+        chunk = 0;
+      }
+    }
+    // the tiles' sums, over their warps in order; a warp's last part lies in the last stage of its ring, whose
+    // chunks have been read and whose other stages the next slab's fill before that part is read
+    auto last_part = [&](int w) { return reinterpret_cast<float*>(ring + ((w + 1) * W::ring - 1) * W::stage); };
+    __syncwarp();
+    if (end > begin) put(last_part(warp));
+    __syncthreads();
+    const bool first = k0 == 0, last = k0 + p.slab >= p.K;
+    for (int i = threadIdx.x; i < tiles * kPart; i += 32 * kWarps) {
+      const int tl = i / kPart, e = i - tl * kPart, c0 = tl * chunks, c1 = c0 + chunks;
+      const int w1 = (c1 - 1) / share;   // the only one that may go on to the next tile
+      float v = first ? 0.f : acc[i];
+#pragma unroll 4
+      for (int w = c0 / share; w < w1; ++w) v += last_part(w)[e];
+      v += min((w1 + 1) * share, all) <= c1 ? last_part(w1)[e] : red[w1 * kPart + e];
+      if (!last || kSplit > 1) acc[i] = v;
+      const int n = (tile0 + tl) * 16 + e / (8 * NT), m = e % (8 * NT);
+      if (last && kSplit == 1 && n < p.N && m < p.M)
+        static_cast<T*>(p.c)[static_cast<long long>(m) * p.N + n] = from_f<T>(v * kQUp);
+    }
+    if (last && kSplit > 1) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < tiles * 16 * p.M; i += 32 * kWarps) {
+        const int r = i / p.M, m = i - r * p.M, n = tile0 * 16 + r;
+        const float* v = &acc[r * 8 * NT + m * kSplit];
+        if (n < p.N) static_cast<T*>(p.c)[static_cast<long long>(m) * p.N + n] = from_f<T>(((v[2] + v[1]) + v[0]) * kQUp);
+      }
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -328,24 +347,10 @@ cudaError_t launch_gemm_w4_t(GemmW4Params p, int group, cudaStream_t st) {
   const auto kernel = gs == 0 ? gemm_w4_kernel<T, NT, 5> : gs == 1 ? gemm_w4_kernel<T, NT, 6> : gemm_w4_kernel<T, NT, 7>;
   if (cudaError_t e = smem_attr_once(kernel, W::smem, done[gs])) return e;
   p.slab = W::slab;
-  const int chunks = ((p.K < p.slab ? p.K : p.slab) + kChunk - 1) / kChunk;
   p.tiles = (p.N + 15) / 16;
-  const int sms = num_sms(), least = (p.tiles + kTileRowsMax / 16 - 1) / (kTileRowsMax / 16);   // CTAs: the sums' room
-  // S: a warp's chunks of a tile and, as one more, the meeting of a tile's warps, times the tiles
-  // one after another (8 rows against 16384 x 8192: S = 1, 2, 4, 16 take 26.4, 24.6, 23.5, 29.6 us, and
-  // 2 is taken; one row against 2048 x 5632: S = 1, 4, 16 take 17.6, 10.8, 5.9, and 16 is)
-  int best = 1 << 30, grid = 1;
-  for (int S = 1; S <= kWarps && S <= chunks; S *= 2) {
-    const int per_cta = kWarps / S, want = (p.tiles + per_cta - 1) / per_cta;
-    const int ctas = least > sms ? least : (want < sms ? (want > least ? want : least) : sms);
-    const int rounds = ((p.tiles + ctas - 1) / ctas + per_cta - 1) / per_cta;
-    const int cost = rounds * ((chunks + S - 1) / S + 1);
-    if (cost < best) {
-      best = cost;
-      p.S = S;
-      grid = ctas;
-    }
-  }
+  // a CTA per SM, or more where eight tiles each are all that their sums have room for
+  const int sms = num_sms(), least = (p.tiles + kTileRowsMax / 16 - 1) / (kTileRowsMax / 16);
+  const int grid = least > sms ? least : p.tiles < sms ? p.tiles : sms;
   return launch(kernel, dim3(grid), dim3(32 * kWarps), W::smem, st, p);
 }
 
@@ -377,9 +382,9 @@ cudaError_t launch_dequantize_w4(const void* q4, const float* scales, void* w, i
 
 cudaError_t launch_gemm_w4(const void* a, const void* q4, const float* scales, void* c, int M, int N, int K, int group,
                            bool bf16, cudaStream_t st) {
-  GemmW4Params p{a, static_cast<const uint8_t*>(q4), scales, c, M, N, K, 0, 0, 0};
-  // the fewest tiles of eight columns that hold the rows (8 bf16 rows against 16384 x 8192: one tile 24.6
-  // us, two 36.9; fp32: 5 rows 46 in two tiles, 70 in three; 8 rows 72 in three, 166 in six)
+  GemmW4Params p{a, static_cast<const uint8_t*>(q4), scales, c, M, N, K, 0, 0};
+  // the fewest tiles of eight columns that hold the rows (against 16384 x 8192 in L2: 8 bf16 rows in one tile
+  // 23.8 us, in two 34.9; 5 fp32 rows in two 45, in three 73; 8 fp32 rows in three 74, in six 175)
   if (bf16) return M <= 8 ? launch_gemm_w4_t<__nv_bfloat16, 1>(p, group, st) : launch_gemm_w4_t<__nv_bfloat16, 2>(p, group, st);
   // three columns a row
   if (M <= 2) return launch_gemm_w4_t<float, 1>(p, group, st);
