@@ -100,10 +100,10 @@ __global__ void __launch_bounds__(256) dequantize_w4_kernel(const uint32_t* __re
 // shared memory, already in the order of the products.  The chunks of 256 k (16 rows x 128 bytes) of
 // all its tiles are shared out evenly: each warp streams its own through a ring of its own by cp.async,
 // and the parts of a tile meet in shared memory at the slab's end, in the warps' order.  Eight rows
-// against 16384 x 8192: 26.9 us (2.8 TB/s, 43 % of the measured copy rate), 23.8 with the weights in
-// L2.  (Each tile shared by two warps, the best fixed number there: 26.3 and 24.6; but four rows against
-// 11264 x 5632 then took 18.9 us against 15.4, for every CTA had a whole number of rounds.)  The stream
-// alone takes 14 us, taking the nibbles apart and the products alone 20, at four warps an SM quarter
+// against 16384 x 8192: 25.4 us (3.0 TB/s, 46 % of the measured copy rate); four against 11264 x 5632:
+// 14.6.  (Each tile shared by a fixed number of warps, so that a CTA takes whole rounds: 26.3 and 18.9;
+// the next slab's first chunks not under way while the parts meet: 27.0 and 15.5.)  The stream alone
+// takes 14 us, taking the nibbles apart and the products alone 20, at four warps an SM quarter
 // that issue in half of the cycles.  One row against 2048 x 5632: 5.6 us, a launch and a chunk's way.
 //
 // The 32 k of 16 bytes of a row are one or part of one group; lane (g, t) takes 4 of them
@@ -174,51 +174,61 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_co
   const uint32_t my_ring = smem_u32(ring + warp * W::ring * W::stage);
   pdl_trigger();
   pdl_wait();
-  for (int k0 = 0; k0 < p.K; k0 += p.slab) {
-    const int ks = min(p.slab, p.K - k0), chunks = (ks + kChunk - 1) / kChunk;
-    // the CTA's chunks, tile by tile, in equal shares; a share is no longer than a tile (eight tiles and
-    // sixteen warps), so it is the end of one tile and the beginning of the next at most
-    const int all = tiles * chunks, share = (all + kWarps - 1) / kWarps;
-    const int begin = min(warp * share, all), end = min(begin + share, all);
-    // the next chunk to fetch: its tile, its number in the tile, its slot
-    int fi = begin, ft = begin / chunks, fc = begin - ft * chunks, fs = 0;
-    int chunk = fc;   // and to compute
-    auto fetch = [&]() {
-      if (fi < end) {
-        const int kc = fc * kChunk + k0, n0 = (tile0 + ft) * 16;
-        const uint32_t dst = my_ring + fs * W::stage, dq = dst + (lane >> 3) * kRowPitch + (lane & 7) * 16;
-        const int k = kc + (lane & 7) * 32;
-        if (n0 + 16 <= p.N && kc + kChunk <= p.K) {   // eight lanes: the 128 bytes of a row
-          const uint8_t* src = p.q4 + (n0 + (lane >> 3)) * row_bytes + (k >> 1);
+  // A slab of K.  The CTA's chunks, tile by tile, go to the warps in equal shares; a share is no longer than
+  // a tile (eight tiles and sixteen warps), so it is the end of one tile and the beginning of the next at most.
+  int k0, chunks, all, share, begin, end, chunk;   // chunk: the next one to compute, in its tile
+  int fi, ft, fc, fs;   // the next chunk to fetch: its number, its tile, its number in the tile, its slot
+  auto fetch = [&]() {
+    if (fi < end) {
+      const int kc = fc * kChunk + k0, n0 = (tile0 + ft) * 16;
+      const uint32_t dst = my_ring + fs * W::stage, dq = dst + (lane >> 3) * kRowPitch + (lane & 7) * 16;
+      const int k = kc + (lane & 7) * 32;
+      if (n0 + 16 <= p.N && kc + kChunk <= p.K) {   // eight lanes: the 128 bytes of a row
+        const uint8_t* src = p.q4 + (n0 + (lane >> 3)) * row_bytes + (k >> 1);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) cp_async16(dq + i * 4 * kRowPitch, src + i * 4 * row_bytes, true);
+        for (int i = 0; i < 4; ++i) cp_async16(dq + i * 4 * kRowPitch, src + i * 4 * row_bytes, true);
 #pragma unroll
-          for (int i = lane; i < 16 * per_chunk; i += 32)
-            cp_async4(dst + 16 * kRowPitch + ((i >> kLog) * 8 + (i & (per_chunk - 1))) * 4,
-                      p.scales + (n0 + (i >> kLog)) * row_scales + (kc >> GS) + (i & (per_chunk - 1)), true);
-        } else {   // rows behind the last read it again, k behind the last count as zeros
-          const bool ok = k < p.K;
+        for (int i = lane; i < 16 * per_chunk; i += 32)
+          cp_async4(dst + 16 * kRowPitch + ((i >> kLog) * 8 + (i & (per_chunk - 1))) * 4,
+                    p.scales + (n0 + (i >> kLog)) * row_scales + (kc >> GS) + (i & (per_chunk - 1)), true);
+      } else {   // rows behind the last read it again, k behind the last count as zeros
+        const bool ok = k < p.K;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            cp_async16(dq + i * 4 * kRowPitch, p.q4 + min(n0 + i * 4 + (lane >> 3), p.N - 1) * row_bytes + (ok ? k >> 1 : 0), ok);
-          for (int i = lane; i < 16 * per_chunk; i += 32) {
-            const int row = i >> kLog, q = i & (per_chunk - 1), gi = (kc >> GS) + q;
-            const bool have = gi < row_scales;
-            cp_async4(dst + 16 * kRowPitch + (row * 8 + q) * 4, p.scales + min(n0 + row, p.N - 1) * row_scales + (have ? gi : 0),
-                      have);
-          }
+        for (int i = 0; i < 4; ++i)
+          cp_async16(dq + i * 4 * kRowPitch, p.q4 + min(n0 + i * 4 + (lane >> 3), p.N - 1) * row_bytes + (ok ? k >> 1 : 0), ok);
+        for (int i = lane; i < 16 * per_chunk; i += 32) {
+          const int row = i >> kLog, q = i & (per_chunk - 1), gi = (kc >> GS) + q;
+          const bool have = gi < row_scales;
+          cp_async4(dst + 16 * kRowPitch + (row * 8 + q) * 4, p.scales + min(n0 + row, p.N - 1) * row_scales + (have ? gi : 0),
+                    have);
         }
-        ++fi;
-        if (++fc == chunks) {
-          fc = 0;
-          ++ft;
-        }
-        fs = fs + 1 == W::ring ? 0 : fs + 1;
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
+      ++fi;
+      if (++fc == chunks) {
+        fc = 0;
+        ++ft;
+      }
+      fs = fs + 1 == W::ring ? 0 : fs + 1;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto enter = [&](int k) {
+    k0 = k;
+    chunks = (min(p.slab, p.K - k0) + kChunk - 1) / kChunk;
+    all = tiles * chunks;
+    share = (all + kWarps - 1) / kWarps;
+    begin = min(warp * share, all);
+    end = min(begin + share, all);
+    fi = begin;
+    ft = begin / chunks;
+    chunk = fc = begin - ft * chunks;
+    fs = 0;
 #pragma unroll
     for (int i = 0; i + 1 < W::ring; ++i) fetch();
+  };
+  enter(0);
+  for (bool last = false; !last;) {
+    const int ks = min(p.slab, p.K - k0);
     // the slab's columns of A, in the products' order: x0 x4 x1 x5 x2 x6 x3 x7 of each eight
     __syncthreads();   // (the previous slab's, and its parts, are no longer read)
     constexpr int kColWarps = NT * 8 >= kWarps ? 1 : 2;   // warps that share a column
@@ -308,19 +318,22 @@ __global__ void __launch_bounds__(32 * kWarps, 1) gemm_w4_kernel(const __grid_co
       }
     }
     // the tiles' sums, over their warps in order; a warp's last part lies in the last stage of its ring, whose
-    // chunks have been read and whose other stages the next slab's fill before that part is read
+    // chunks have been read; the next slab's begin to fill the other stages meanwhile
     auto last_part = [&](int w) { return reinterpret_cast<float*>(ring + ((w + 1) * W::ring - 1) * W::stage); };
     __syncwarp();
     if (end > begin) put(last_part(warp));
+    const int n_chunks = chunks, n_all = all, n_share = share;
+    const bool first = k0 == 0;
+    last = k0 + p.slab >= p.K;
+    if (!last) enter(k0 + p.slab);
     __syncthreads();
-    const bool first = k0 == 0, last = k0 + p.slab >= p.K;
     for (int i = threadIdx.x; i < tiles * kPart; i += 32 * kWarps) {
-      const int tl = i / kPart, e = i - tl * kPart, c0 = tl * chunks, c1 = c0 + chunks;
-      const int w1 = (c1 - 1) / share;   // the only one that may go on to the next tile
+      const int tl = i / kPart, e = i - tl * kPart, c0 = tl * n_chunks, c1 = c0 + n_chunks;
+      const int w1 = (c1 - 1) / n_share;   // the only one that may go on to the next tile
       float v = first ? 0.f : acc[i];
 #pragma unroll 4
-      for (int w = c0 / share; w < w1; ++w) v += last_part(w)[e];
-      v += min((w1 + 1) * share, all) <= c1 ? last_part(w1)[e] : red[w1 * kPart + e];
+      for (int w = c0 / n_share; w < w1; ++w) v += last_part(w)[e];
+      v += min((w1 + 1) * n_share, n_all) <= c1 ? last_part(w1)[e] : red[w1 * kPart + e];
       if (!last || kSplit > 1) acc[i] = v;
       const int n = (tile0 + tl) * 16 + e / (8 * NT), m = e % (8 * NT);
       if (last && kSplit == 1 && n < p.N && m < p.M)
