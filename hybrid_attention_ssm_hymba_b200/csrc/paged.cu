@@ -45,8 +45,8 @@ template <typename C, bool WRITE> HY_DEV constexpr int lane_vectors() { return W
 // WRITE: x (the batch's rows) -> cache; else cache -> x.  T: element type of x, C: of the cache.
 // Bound by HBM when there are many rows; what competes are the instructions around each vector,
 // so a thread keeps its place in a row (K or V, head, elements) and walks the rows.  33280 rows of
-// 4 x 128 from bf16 into e4m3: 21.7 us, 4.8 TB/s (73 % of the measured copy rate); back: 17.6 us,
-// 5.7 TB/s (87 %).
+// 4 x 128 from bf16 into e4m3: 24.1 us, 4.3 TB/s (65 % of the measured copy rate); back: 21.7 us,
+// 4.7 TB/s (71 %); 21.7 and 17.6 where the inputs are in L2.
 template <typename T, typename C, bool WRITE, int ROWS>
 __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const PagedKv kv, const RaggedBatch rb, T* xk, T* xv,
                                                                   long long ld, int lpu, unsigned* status) {
@@ -155,8 +155,8 @@ cudaError_t launch_copy_t(const PagedKv& kv, const RaggedBatch& rb, void* k, voi
   int lpu = 1;
   while (lpu * per_lane < kv.dh) lpu *= 2;
   // many rows: enough vectors a thread that finding the rows' pages does not show; few: many CTAs.
-  // (CTAs of 32 rows or of 4: 33280 rows of 4 x 128 into e4m3 21.7 us, 40.1; back 17.6, 33.6; four rows
-  // 5.0, 3.3.  From 16 rows for each of four CTAs
+  // (CTAs of 32 rows or of 4, from L2: 33280 rows of 4 x 128 into e4m3 21.7 us, 40.1; back 17.6, 33.6;
+  // four rows 5.0, 3.3.  From 16 rows for each of four CTAs
   // per SM on, CTAs of 32 leave no SM without work.)
   const auto go = [&](auto kernel, int rows) {
     return launch(kernel, dim3((rb.total_rows + rows - 1) / rows), dim3(kCopyThreads), 0, st, kv, rb, static_cast<T*>(k),

@@ -31,7 +31,7 @@
 // 64 % of the measured bf16 rate; of a round's 4100 cycles the softmax takes 1900 and the tensor core
 // 2050 for both groups.  e4m3 rows: 1306 us; reading K's scales and converting share the shared
 // memory with the products.  Nine ragged sequences of up to 1604 e4m3 rows in a window of 1024 (16
-// blocks a CTA): 93 us, of which 16 blocks take 51; starting up, and per tile Q's conversion, the
+// blocks a CTA): 90 us, of which 16 blocks take 51; starting up, and per tile Q's conversion, the
 // first S and the output take the rest.  A third group per CTA has no TMEM left, and one group with
 // twice the keys would read every K/V row twice as often.
 //

@@ -397,7 +397,7 @@ cudaError_t launch_gemm_w4(const void* a, const void* q4, const float* scales, v
                            bool bf16, cudaStream_t st) {
   GemmW4Params p{a, static_cast<const uint8_t*>(q4), scales, c, M, N, K, 0, 0};
   // the fewest tiles of eight columns that hold the rows (against 16384 x 8192 in L2: 8 bf16 rows in one tile
-  // 23.8 us, in two 34.9; 5 fp32 rows in two 45, in three 73; 8 fp32 rows in three 74, in six 175)
+  // 23 us, in two 35; 5 fp32 rows in two 45, in three 73; 8 fp32 rows in three 74, in six 175)
   if (bf16) return M <= 8 ? launch_gemm_w4_t<__nv_bfloat16, 1>(p, group, st) : launch_gemm_w4_t<__nv_bfloat16, 2>(p, group, st);
   // three columns a row
   if (M <= 2) return launch_gemm_w4_t<float, 1>(p, group, st);

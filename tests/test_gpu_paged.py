@@ -442,6 +442,13 @@ def test_attention_scales_far_apart(cache, n):
 
 
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 40, 300])
+def test_attention_many_parts(cache, n):
+    """A tile or a few over a long history: every CTA has a part or two of one."""
+    _attend(Paged("bf16", cache, 1, 128, 64, [n], [30000], seed=19), 2, 8, -1)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
 @pytest.mark.parametrize("batch,n", [(70, 33), (1100, 1)])
 def test_attention_large_batches(cache, batch, n):
     """Batches beyond what a CTA plans itself, some sequences empty."""

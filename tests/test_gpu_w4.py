@@ -81,6 +81,13 @@ def test_gemm_w4_wide(dtype):
     _product(5, 11264, 2048, 64, dtype)
 
 
+@pytest.mark.parametrize("dtype,m", [("bf16", 8), ("bf16", 16), ("f32", 2), ("f32", 8)])
+@pytest.mark.parametrize("n,k,group", [(7109, 768, 64), (7109, 2560, 32), (19000, 4352, 128)])
+def test_gemm_w4_shares(n, k, group, dtype, m):
+    """Several tiles of rows a CTA, whose chunks its warps share across tiles and slabs."""
+    _product(m, n, k, group, dtype)
+
+
 def test_gemm_w4_repeats_and_graph():
     a = torch.randn(8, 2048, device="cuda").bfloat16()
     w = (torch.randn(512, 2048, device="cuda") * 0.02).bfloat16()
