@@ -36,9 +36,10 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const T* __restrict__ 
     // the quotient 7 w / most, within an ulp and then corrected by its remainder (Markstein's
     // theorem: rounded to nearest, so a half that is exact stays one), and 1.5 * 2^23 added, which
     // rounds it to the nearest even integer in the sum's low bits.  bf16: 7 w is exact.  fp32: it
-    // is not, and next to a half 64 bits decide, as where the remainder is subnormal.
+    // is not, and next to a half 64 bits decide, as where the remainder is subnormal or 7 w of the
+    // largest weight would leave fp32's range (FLT_MAX / 7 = 4.86e37).
     uint32_t u = 0;
-    bool near = most < 1e-30f;
+    bool near = !(most >= 1e-30f && most <= 4.8e37f);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float w7 = 7.f * f[e], t0 = w7 * y, t = fmaf(fmaf(-t0, most, w7), y, t0), s = t + 12582912.f;
