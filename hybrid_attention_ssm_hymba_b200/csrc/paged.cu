@@ -271,9 +271,10 @@ __global__ void __launch_bounds__(32 * kSimtWarps) paged_attn_simt(const PagedAt
       float mx = v;
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-      const float mn = fmaxf(m[g], mx);
-      if (mn == -INFINITY) continue;   // no key so far
-      const float corr = exp2f(m[g] - mn), e = exp2f(v - mn);
+      // no number yet: no key so far, or scores that are all NaN, which the maximum passes over and
+      // the sum keeps
+      const float mn = fmaxf(m[g], mx), mr = mn == -INFINITY ? 0.f : mn;
+      const float corr = exp2f(m[g] - mr), e = exp2f(v - mr);
       float sum = e;
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);

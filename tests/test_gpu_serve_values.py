@@ -1,11 +1,12 @@
-"""Values the serving calls have to keep: weights next to the largest number."""
+"""Values the serving calls have to keep: weights next to the largest number; NaN in Q and in
+visible rows of the cache."""
 import numpy as np
 import pytest
 import torch
 
 import hybrid_attention_ssm_hymba_b200 as H
-from gpu_util import requires_cuda
-from serve_util import DTYPE, TINY, TORCH
+from gpu_util import requires_cuda, status_ok
+from serve_util import DTYPE, TINY, TORCH, Paged, f64
 
 pytestmark = [pytest.mark.gpu, requires_cuda]
 
@@ -36,3 +37,93 @@ def test_quantise_w4_of_the_largest_weights(dtype, group):
     got = q4.cpu().numpy()
     assert np.array_equal((got & 15) - 8.0, q[:, 0::2]) and np.array_equal((got >> 4) - 8.0, q[:, 1::2])
     assert np.array_equal(sc.cpu().numpy(), scale)
+
+
+# --------------------------------------------------------------------------- not finite
+
+def _q(c, hq, seed=5):
+    q = np.random.default_rng(seed).standard_normal((c.total, hq, c.dh)).astype(np.float32)
+    return torch.from_numpy(q).to(TORCH[c.dtype])
+
+
+def _row_tolerance(c, q, hq, meta, window):
+    """(out, tolerance) in 64 bits as in Paged.attention, with each row's own scores in its
+    tolerance (one row's huge scores say nothing about another's), and what 8-bit rows add: P is
+    held in 16 bits with a common power of two a row, 2^-25 at least, the largest p_j amax_j / 448
+    of the row at 2^8 or more: L 2^-33 max_j p_j amax_j in all, and as much again for its lag."""
+    want, _ = c.attention(q, hq, meta, window)
+    tol = np.full_like(want, np.nan)
+    g = hq // c.hkv
+    for b in range(c.batch):
+        at = slice(c.first[b], c.first[b + 1])
+        see = c.visible(b, meta, window)
+        k, v = np.nan_to_num(c.rows(0, b, 0, c.lens[b])), np.nan_to_num(c.rows(1, b, 0, c.lens[b]))
+        for h in range(hq):
+            qq, kk, vv = q[at, h], k[:, h // g], np.abs(v[:, h // g])
+            s = np.where(see, qq @ kk.T / np.sqrt(c.dh), -np.inf)
+            p = np.exp(s - s.max(1, keepdims=True))
+            p /= p.sum(1, keepdims=True)
+            size = np.where(see, np.abs(qq) @ np.abs(kk).T, 0) / np.sqrt(c.dh) * (c.dh + 2) * 2.0 ** -24
+            # a score's error matters by its key's weight: 2 ds, and never more than the whole row
+            a = p @ vv
+            ds = np.minimum(2 * size.max(1, keepdims=True), 1.0)
+            t = a * (ds + (c.lens[b] + 16) * 2.0 ** -23) + np.abs(want[at, h]) * 2.0 ** -8 + a * 2.0 ** -8
+            tol[at, h] = t + c.lens[b] * 2.0 ** -32 * (p * vv.max(1)[None]).max(1, keepdims=True)
+    return want, tol
+
+
+def _close(got, want, tol, rows=None):
+    rows = np.arange(len(want)) if rows is None else np.asarray(rows)
+    g, w, t = got[rows], want[rows], tol[rows]
+    assert np.isfinite(g).all(), f"{int((~np.isfinite(g)).sum())} values that are not finite"
+    bad = np.abs(g - w) - t
+    assert (bad <= 0).all(), f"{int((bad > 0).sum())} values beyond the tolerance; worst {np.nanmax(np.abs(g - w) / t):.3e} of it"
+
+
+FORMS = [("f32", "f32"), ("f32", "e4m3")]
+
+# one block a tile; tiles of several blocks, which few tiles in a call cut into parts; a row's
+# last key alone in its block, or in its piece of the keys
+SHAPES = [([1, 1], [32, 0]), ([1, 3], [128, 40]), ([1], [4000]), ([60, 40], [0, 10]), ([20, 129], [237, 128]),
+          ([200, 3], [313, 5])]
+
+
+@pytest.mark.parametrize("dtype,cache", FORMS)
+@pytest.mark.parametrize("ns,pasts", SHAPES)
+def test_a_nan_query_row_is_a_nan_output_row(ns, pasts, dtype, cache):
+    c = Paged(dtype, cache, 2, 128, 64, ns, pasts, seed=31).upload()
+    hq = 4
+    q = _q(c, hq)
+    want, tol = _row_tolerance(c, q.double().numpy(), hq, 0, -1)
+    bad = sorted({0, int(c.first[1]) - 1})
+    q[bad, 1] = float("nan")
+    out = torch.zeros((c.total, hq, 128), dtype=TORCH[dtype], device="cuda")
+    status_ok(c.attend(q.cuda(), out, hq, 0, -1))
+    got = f64(out)
+    assert np.isnan(got[bad, 1]).all(), "a NaN row of Q gave numbers"
+    got[bad, 1] = want[bad, 1]
+    _close(got[:c.first[-1]], want[:c.first[-1]], tol[:c.first[-1]])
+
+
+@pytest.mark.parametrize("dtype,cache", FORMS)
+@pytest.mark.parametrize("ns,pasts", SHAPES)
+@pytest.mark.parametrize("which", [0, 1])
+def test_a_nan_token_reaches_its_own_row(which, ns, pasts, dtype, cache):
+    """The newest K or V row of a sequence is NaN (as an append of a NaN leaves it): the last row's
+    output is NaN for the heads that read it, whole tile or cut; other sequences are as they were."""
+    c = Paged(dtype, cache, 2, 128, 64, ns, pasts, seed=32)
+    hq = 4
+    q = _q(c, hq)
+    want, tol = _row_tolerance(c, q.double().numpy(), hq, 0, -1)
+    x = np.random.default_rng(3).standard_normal((1, 2, 128)).astype(np.float32)
+    x[0, 1] = np.nan
+    c.put(which, 0, c.lens[0] - 1, x)
+    c.upload()
+    out = torch.zeros((c.total, hq, 128), dtype=TORCH[dtype], device="cuda")
+    status_ok(c.attend(q.cuda(), out, hq, 0, -1))
+    got, last = f64(out), int(c.first[1]) - 1
+    assert np.isnan(got[last, 2:]).all(), "the row that sees a NaN gave numbers"
+    assert np.isfinite(got[last, :2]).all()
+    rest = np.arange(c.first[1], c.first[-1])
+    if len(rest):
+        _close(got, want, tol, rest)
