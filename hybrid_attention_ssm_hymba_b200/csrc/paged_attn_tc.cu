@@ -809,16 +809,16 @@ __global__ void __launch_bounds__(256) paged_join_tc(const __grid_constant__ Pag
         ml[u] = p.part_ml[at];
         v[u] = reinterpret_cast<const float4*>(p.part)[(at >> 3) * (2 * DH) + c4 * 8 + (row & 7)];
       }
-      const float mn = fmaxf(fmaxf(m, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
-      if (mn == -INFINITY) continue;
-      const float f0 = ex2_approx(m - mn);
+      const float mn = fmaxf(fmaxf(m, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x)), mr = mn == -INFINITY ? 0.f : mn;
+      const float f0 = ex2_approx(m - mr);
       m = mn;
       l *= f0;
       acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const float f = ex2_approx(ml[u].x - mn);
-        if (f == 0.f) continue;
+        // a part that saw no key; one whose scores are all NaN has a NaN for its sum, and counts
+        if (ml[u].y == 0.f) continue;
+        const float f = ex2_approx(ml[u].x - mr);
         l = fmaf(ml[u].y, f, l);
         acc = make_float4(fmaf(v[u].x, f, acc.x), fmaf(v[u].y, f, acc.y), fmaf(v[u].z, f, acc.z), fmaf(v[u].w, f, acc.w));
       }

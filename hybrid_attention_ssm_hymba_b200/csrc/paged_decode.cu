@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(256) paged_join_rows(const __grid_constant__ P
       const float4 v = reinterpret_cast<const float4*>(p.part + at * DH)[lane];
       const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
       l = fmaf(ml.y, f, l);
-      if (f != 0.f) acc = make_float4(fmaf(v.x, f, acc.x), fmaf(v.y, f, acc.y), fmaf(v.z, f, acc.z), fmaf(v.w, f, acc.w));
+      if (ml.y != 0.f) acc = make_float4(fmaf(v.x, f, acc.x), fmaf(v.y, f, acc.y), fmaf(v.z, f, acc.z), fmaf(v.w, f, acc.w));
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;
     __nv_bfloat16* o = p.out + static_cast<long long>(cut.row0 + tok) * p.out_ld + (cut.kvh * p.g.G + rg) * DH;

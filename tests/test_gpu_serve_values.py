@@ -80,7 +80,7 @@ def _close(got, want, tol, rows=None):
     assert (bad <= 0).all(), f"{int((bad > 0).sum())} values beyond the tolerance; worst {np.nanmax(np.abs(g - w) / t):.3e} of it"
 
 
-FORMS = [("f32", "f32"), ("f32", "e4m3")]
+FORMS = [("f32", "f32"), ("f32", "e4m3"), ("bf16", "bf16"), ("bf16", "e4m3")]
 
 # one block a tile; tiles of several blocks, which few tiles in a call cut into parts; a row's
 # last key alone in its block, or in its piece of the keys
@@ -127,3 +127,22 @@ def test_a_nan_token_reaches_its_own_row(which, ns, pasts, dtype, cache):
     rest = np.arange(c.first[1], c.first[-1])
     if len(rest):
         _close(got, want, tol, rest)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("ns,pasts", SHAPES)
+def test_an_infinite_value_of_no_weight(ns, pasts, cache):
+    """A visible V row of infinities (NaN in an e4m3 cache) whose weight is too small for fp32: 0 times
+    it is NaN, whole tile or cut."""
+    c = Paged("bf16", cache, 2, 128, 64, ns, pasts, seed=37)
+    x = np.zeros((1, 2, 128), np.float32)
+    c.put(1, 0, 0, np.where(np.arange(2)[:, None] == 1, np.inf, x).astype(np.float32))
+    x[:, :, 0] = -400
+    c.put(0, 0, 0, x)
+    c.upload()
+    q = _q(c, 4)
+    q[:, :, 0] = 16
+    out = torch.zeros((c.total, 4, 128), dtype=torch.bfloat16, device="cuda")
+    status_ok(c.attend(q.cuda(), out, 4, 0, -1))
+    got, last = f64(out), int(c.first[1]) - 1
+    assert np.isnan(got[last, 2:]).all() and np.isfinite(got[last, :2]).all()
