@@ -18,10 +18,10 @@
 //   warps 2, 3  (e4m3 cache only) turn the 8-bit K and V of a block into the fp16 tiles the
 //               tensor core reads.  An e4m3 code is exact in fp16.  V: code times scale is rounded
 //               once to fp16's 11 bits (2^-12, where the output's own rounding is 2^-8).  K: a
-//               score of hundreds would lose too much that way, so K is the code times the power
-//               of two in its scale, exactly, and the softmax threads multiply S's columns by the
-//               scale's mantissa.  Powers of two, the same for all rows of a tile, keep fp16's
-//               range: scales are held below 2^7 of the largest that the tile has met, a row of Q
+//               score of hundreds would lose too much that way, so K is the code alone and the
+//               softmax threads multiply S's columns by its scale in fp32: rows of any magnitude
+//               stand side by side.  Powers of two, the same for all rows of a tile, keep fp16's
+//               range: V's scales are held below 2^7 of the largest that the tile has met, a row of Q
 //               is scaled to at most 2^8, and P to at most 2^15; each keeps 11 bits down to 2^-25
 //               and more below its largest value.
 // TMEM (512 columns): S_a | S_b | O_a | O_b; P in 16 bits over the consumed S columns.
@@ -49,11 +49,11 @@ constexpr int DH = 128, TILE_BYTES = 128 * DH * 2, HALF = 128 * 64 * 2;
 constexpr uint32_t kFmtBits = (1u << 7) | (1u << 10);
 template <bool FP8> constexpr uint32_t IDESC_QK = idesc_bf16(128, 128, false, false) & ~(FP8 ? kFmtBits : 0u);
 template <bool FP8> constexpr uint32_t IDESC_PV = idesc_bf16(128, DH, false, true) & ~(FP8 ? kFmtBits : 0u);
-constexpr int kUp = 7;         // FP8: K's and V's scales are held below 2^kUp, code times scale below 2^16
+constexpr int kUp = 7;         // FP8: V's scales are held below 2^kUp, code times scale below 2^16
 constexpr float kPUp = 11.f;   // FP8: P is 2^(s - m + kPUp)
-// FP8: Q and K are scaled up by at most 2^kMostUp each, so that the factor from their product to
-// log2 units stays a normal number (0 times a hidden score's -inf would be no number).
-constexpr int kMostUp = 60;
+// FP8: a row of Q is scaled up by at most 2^kMostUp, so that the factor from S to log2 units stays
+// a normal number (0 times a hidden score's -inf would be no number).
+constexpr int kMostUp = 120;
 
 // What the producer tells the softmax threads of each tile (they give the slot back) and of
 // each key block (it is at most four blocks ahead of them: a ring of 8 needs no giving back).
@@ -68,7 +68,7 @@ struct TileInfo {
 struct BlockInfo {
   int k0;
   uint32_t flags;     // bit x: group x masks; bit 2: some rows of V are to be zeroed
-  int ek, ev;         // FP8: K's and V's scales are held times 2^(kUp - ek), 2^(kUp - ev)
+  int ev;             // FP8: V's scales are held times 2^(kUp - ev)
   uint32_t valid[4];  // rows whose page number is valid, one bit each
 };
 constexpr uint32_t kZeroV = 4u;
@@ -94,8 +94,8 @@ template <> struct Smem<false> {   // behind the six tiles
 constexpr int kRawStages = 3, kRawBytes = 64 * DH, kScaleSlots = 4;
 template <> struct Smem<true> : Smem<false> {
   uint64_t raw_full[kRawStages], raw_empty[kRawStages], scale_full[kScaleSlots], scale_ready[kScaleSlots], q_ready[2];
-  // As copied: K's and V's scales [slot][K, V][row].  As used: the mantissa of K's scale in [1, 2),
-  // and (fp16 pair) V's scale and the power of two of K's, in fp16's range.
+  // As copied: K's and V's scales [slot][K, V][row].  As used: K's scale, and V's in fp16's range (in the
+  // low half of its word).
   alignas(16) float scale[kScaleSlots][2][128];
 };
 template <bool FP8> constexpr int smem_bytes() {
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
                                                  abort_flag));
           if (!ok || ti.toks == 0) break;
           const int n = ti.n, p1 = ti.p1, lo = p.g.window < 0 ? 0 : ti.p0 - p.g.window;
-          uint32_t most[2] = {0, 0};   // the largest of K's and of V's scales so far, as bits
+          uint32_t most = 0;   // the largest of V's scales so far, as bits
           for (int j = 0; ok && j < n; ++j, ++jb) {
             const uint32_t s = jb & 1, par = (jb >> 1) & 1, slot = jb % kScaleSlots, slot_par = (jb / kScaleSlots) & 1;
             BlockInfo& bi = sm.block[jb & (kBlockSlots - 1)];
@@ -495,27 +495,20 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
                 if (((valid >> e) & 1u) && key0 + e <= p1 && (key0 + e >= lo || key0 + e < p.g.n_meta)) seen |= 1u << e;
               float4& k4 = *reinterpret_cast<float4*>(&sm.scale[slot][0][lane * 4]);
               float4& v4 = *reinterpret_cast<float4*>(&sm.scale[slot][1][lane * 4]);
-              float k[4] = {k4.x, k4.y, k4.z, k4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w}, up[2];
+              float k[4] = {k4.x, k4.y, k4.z, k4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 if (!((seen >> e) & 1u)) k[e] = v[e] = 0.f;
-                most[0] = max(most[0], __float_as_uint(k[e]) & 0x7fffffffu);
-                most[1] = max(most[1], __float_as_uint(v[e]) & 0x7fffffffu);
+                most = max(most, __float_as_uint(v[e]) & 0x7fffffffu);
               }
-#pragma unroll
-              for (int w = 0; w < 2; ++w) {
-                most[w] = __reduce_max_sync(0xffffffffu, most[w]);
-                // every scale is below 2^ex
-                const int ex = max(static_cast<int>(most[w] >> 23) - 126, w ? kUp - 127 : kUp - kMostUp);
-                up[w] = pow2(kUp - ex);
-                if (lane == 0) (w ? bi.ev : bi.ek) = ex;
-              }
+              most = __reduce_max_sync(0xffffffffu, most);
+              const int ex = max(static_cast<int>(most >> 23) - 126, kUp - 127);   // every scale is below 2^ex
+              const float up = pow2(kUp - ex);
+              if (lane == 0) bi.ev = ex;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const uint32_t kb = __float_as_uint(k[e]);
-                const __half2 h = __floats2half2_rn(v[e] * up[1], __uint_as_float(kb & 0x7f800000u) * up[0]);
+                const __half2 h = __floats2half2_rn(v[e] * up, 0.f);
                 v[e] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h));
-                k[e] = __uint_as_float((kb & 0x7fffffu) | 0x3f800000u);
               }
               k4 = make_float4(k[0], k[1], k[2], k[3]);
               v4 = make_float4(v[0], v[1], v[2], v[3]);
@@ -547,7 +540,8 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) r4[i] = lds_f4(src + (i0 + i) * 1024);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = __byte_perm(lds_u32(fs + (i0 + i) * 32), 0u, u < 2 ? 0x3232 : 0x1010);
+                for (int i = 0; i < 4; ++i)   // K: times 1
+                  f[i] = u < 2 ? 0x3c003c00u : __byte_perm(lds_u32(fs + (i0 + i) * 32), 0u, 0x1010);
                 if (hide) {   // rows of V that no query of the tile sees (they may hold NaN codes)
 #pragma unroll
                   for (int i = 0; i < 4; ++i) {
@@ -646,10 +640,9 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
       for (int j = 0; j < n; ++j, ++jb, ++cnt) {
         ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.s_full[x], cnt & 1, p.status, abort_flag));
         uint32_t sv[64];
-        float m_half = -INFINITY, to_block = to_log2;   // from this block's S to log2 units
+        float m_half = -INFINITY;
         const volatile BlockInfo& bi = sm.block[jb & (kBlockSlots - 1)];
         const uint32_t flags = bi.flags;
-        if constexpr (FP8) to_block *= pow2(bi.ek - kUp);
         if (ok) {
           tc_fence_after();
           tmem_ld32(tSx + kh * 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
@@ -668,7 +661,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
                 if (!(see & (1u << e))) sv[32 * w + e] = __float_as_uint(-INFINITY);
             }
           }
-          m_half = row_max64(sv) * to_block;
+          m_half = row_max64(sv) * to_log2;
         }
         // the row maximum over both halves; the barrier also orders this half's reads of
         // S before the other half's P stores (P of keys 64..127 lands in S columns 32..63)
@@ -685,7 +678,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
             m_used = m_cand;
           }
           const float m_ref = (m_used == -INFINITY) ? 0.f : (FP8 ? m_used - kPUp : m_used);
-          const float sum = row_exp64<FP8>(sv, to_block, m_ref);
+          const float sum = row_exp64<FP8>(sv, to_log2, m_ref);
           float alpha_o = alpha;
           bool moved = need;
           if constexpr (FP8) {

@@ -1,5 +1,5 @@
 """Values the serving calls have to keep: weights next to the largest number; NaN in Q and in
-visible rows of the cache."""
+visible rows of the cache; rows of K and V whose magnitudes lie far apart."""
 import numpy as np
 import pytest
 import torch
@@ -146,3 +146,38 @@ def test_an_infinite_value_of_no_weight(ns, pasts, cache):
     status_ok(c.attend(q.cuda(), out, 4, 0, -1))
     got, last = f64(out), int(c.first[1]) - 1
     assert np.isnan(got[last, 2:]).all() and np.isfinite(got[last, :2]).all()
+
+
+# --------------------------------------------------------------------------- far apart
+
+def _largest_score(c, q, hq, b, window):
+    """Of each new row of sequence b, over its heads and the keys that it sees."""
+    k, g = np.nan_to_num(c.rows(0, b, 0, c.lens[b])), hq // c.hkv
+    see = c.visible(b, 0, window)
+    qb = q[c.first[b]:c.first[b + 1]]
+    return np.max([np.where(see, np.abs(qb[:, h] @ k[:, h // g].T), 0).max(1) for h in range(hq)], 0) / np.sqrt(c.dh)
+
+
+@pytest.mark.parametrize("up", [24, 30, 45, 60])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 40, 300])
+def test_a_large_k_row_that_a_query_does_not_see(n, cache, up):
+    """A row of K 2^up times the others, in the window of some queries of a tile and not of the
+    rest: those are as exact as without it.  (Rows that see a score beyond 2^20 are outside the
+    call's range.)"""
+    c = Paged("bf16", cache, 2, 128, 64, [n, n], [400, 300], seed=33)
+    window, hq = 64, 8
+    for b in range(2):
+        lo = c.lens[b] - c.ns[b]
+        for j in (lo - window, lo + n // 2):     # the first query's last key; one that appears halfway
+            if j < c.lens[b] - 1:
+                c.put(0, b, j, (2.0 ** up * c.rng.standard_normal((1, 2, 128))).astype(np.float32))
+    c.upload()
+    q = _q(c, hq)
+    want, tol = _row_tolerance(c, q.double().numpy(), hq, 0, window)
+    out = torch.zeros((c.total, hq, 128), dtype=torch.bfloat16, device="cuda")
+    status_ok(c.attend(q.cuda(), out, hq, 0, window))
+    rows = np.arange(c.first[-1])
+    mine = np.concatenate([_largest_score(c, q.double().numpy(), hq, b, window) for b in range(2)]) < 2.0 ** 20
+    assert mine.sum() > len(rows) // 3 or n == 1
+    _close(f64(out), want, tol, rows[mine])
