@@ -16,14 +16,17 @@
 //   warps 2..9  softmax of group a, warps 10..17 of group b (e4m3 cache: two later): two threads
 //               per row, each over 64 of the block's keys and 64 of O's columns
 //   warps 2, 3  (e4m3 cache only) turn the 8-bit K and V of a block into the fp16 tiles the
-//               tensor core reads.  An e4m3 code is exact in fp16.  V: code times scale is rounded
-//               once to fp16's 11 bits (2^-12, where the output's own rounding is 2^-8).  K: a
-//               score of hundreds would lose too much that way, so K is the code alone and the
-//               softmax threads multiply S's columns by its scale in fp32: rows of any magnitude
-//               stand side by side.  Powers of two, the same for all rows of a tile, keep fp16's
-//               range: V's scales are held below 2^7 of the largest that the tile has met, a row of Q
-//               is scaled to at most 2^8, and P to at most 2^15; each keeps 11 bits down to 2^-25
-//               and more below its largest value.
+//               tensor core reads.  An e4m3 code is exact in fp16.  V: its scale and the code
+//               times it are each rounded to fp16's 11 bits (2^-11 in all, where the output's own
+//               rounding is 2^-8).  K: a score of hundreds would lose too much that way, so K is
+//               the code alone and the softmax threads multiply S's columns by its scale in fp32:
+//               rows of any magnitude stand side by side.  Powers of two keep fp16's range: V's
+//               scales are held below 2^7 with the largest that the tile has met, a row of Q is
+//               scaled to at most 2^8, and P to at most 2^15.  V's scales keep their 11 bits down
+//               to 2^-21 of the largest.  From the first block with scales further apart
+//               (kSpread) on, V is the code times its scale's mantissa, and the scale's power of
+//               two goes into P, relative to the largest of the row's own keys: a large V row
+//               costs no bits of the rows that do not see it.
 // TMEM (512 columns): S_a | S_b | O_a | O_b; P in 16 bits over the consumed S columns.
 //
 // Bound by the round of a group: S (tensor core), softmax, P V, one after another, with the other
@@ -51,6 +54,11 @@ template <bool FP8> constexpr uint32_t IDESC_QK = idesc_bf16(128, 128, false, fa
 template <bool FP8> constexpr uint32_t IDESC_PV = idesc_bf16(128, DH, false, true) & ~(FP8 ? kFmtBits : 0u);
 constexpr int kUp = 7;         // FP8: V's scales are held below 2^kUp, code times scale below 2^16
 constexpr float kPUp = 11.f;   // FP8: P is 2^(s - m + kPUp)
+// FP8: V's scales of a tile stand in V as they are while their exponents differ by at most this.  Beyond,
+// a block takes a second exponential: scales of 2^+-15 in random order, 4096 rows over 32K keys 2110 us
+// against 1295, ragged chunks 132 against 97.  (Always so, the usual scales would pay it too.)
+constexpr int kSpread = 20;
+constexpr int kApart = 1 << 20;   // BlockInfo::ev of such a block
 // FP8: a row of Q is scaled up by at most 2^kMostUp, so that the factor from S to log2 units stays
 // a normal number (0 times a hidden score's -inf would be no number).
 constexpr int kMostUp = 120;
@@ -68,7 +76,7 @@ struct TileInfo {
 struct BlockInfo {
   int k0;
   uint32_t flags;     // bit x: group x masks; bit 2: some rows of V are to be zeroed
-  int ev;             // FP8: V's scales are held times 2^(kUp - ev)
+  int ev;             // FP8: V's scales are held times 2^(kUp - ev); kApart: without their powers of two
   uint32_t valid[4];  // rows whose page number is valid, one bit each
 };
 constexpr uint32_t kZeroV = 4u;
@@ -94,8 +102,8 @@ template <> struct Smem<false> {   // behind the six tiles
 constexpr int kRawStages = 3, kRawBytes = 64 * DH, kScaleSlots = 4;
 template <> struct Smem<true> : Smem<false> {
   uint64_t raw_full[kRawStages], raw_empty[kRawStages], scale_full[kScaleSlots], scale_ready[kScaleSlots], q_ready[2];
-  // As copied: K's and V's scales [slot][K, V][row].  As used: K's scale, and V's in fp16's range (in the
-  // low half of its word).
+  // As copied: K's and V's scales [slot][K, V][row].  As used: K's scale, and for V a word with the factor
+  // of its codes in fp16 (low half) and (kApart) the scale's exponent in bf16 (high half).
   alignas(16) float scale[kScaleSlots][2][128];
 };
 template <bool FP8> constexpr int smem_bytes() {
@@ -145,6 +153,41 @@ __device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t u, int half) {
   if (half) asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, hi;}" : "=r"(v) : "r"(u));
   else asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, lo;}" : "=r"(v) : "r"(u));
   return v;
+}
+// FP8, a kApart block: the exponent of V's scale from its word.
+__device__ __forceinline__ float v_exponent(float word) { return __uint_as_float(__float_as_uint(word) & 0xffff0000u); }
+// The largest of s sc + e, e the exponent of V's scale: what the terms of P V reach.
+__device__ __forceinline__ float row_reach64(const uint32_t (&sv)[64], uint32_t vec, float sc) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    const float4 w = lds_f4(vec + 16 * q);
+    m = max3f(m, fmaf(__uint_as_float(sv[4 * q]), sc, v_exponent(w.x)), fmaf(__uint_as_float(sv[4 * q + 1]), sc, v_exponent(w.y)));
+    m = max3f(m, fmaf(__uint_as_float(sv[4 * q + 2]), sc, v_exponent(w.z)), fmaf(__uint_as_float(sv[4 * q + 3]), sc, v_exponent(w.w)));
+  }
+  return m;
+}
+// P = 2^(s sc - m + e + up) in place as pairs of fp16; returns the sum of the 2^(s sc - m + kPUp).
+__device__ __forceinline__ float row_exp64_apart(uint32_t (&sv)[64], uint32_t vec, float sc, float m, float up) {
+  float sum = 0.f;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    const float4 w = lds_f4(vec + 16 * q);
+    const float e[4] = {v_exponent(w.x), v_exponent(w.y), v_exponent(w.z), v_exponent(w.w)};
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = fmaf(__uint_as_float(sv[4 * q + i]), sc, -m);
+      sum += ex2_approx(x + kPUp);
+      y[i] = ex2_approx(x + (e[i] + up));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const __half2 r = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+      sv[2 * q + i] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+  }
+  return sum;
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
 // P = 2^(S scale - m_ref), packed in place as pairs of bf16 or fp16 (sv[q] <- p[2q], p[2q + 1]);
@@ -478,7 +521,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
                                                  abort_flag));
           if (!ok || ti.toks == 0) break;
           const int n = ti.n, p1 = ti.p1, lo = p.g.window < 0 ? 0 : ti.p0 - p.g.window;
-          uint32_t most = 0;   // the largest of V's scales so far, as bits
+          uint32_t most = 0, least = 0x7f7fffffu;   // the largest and the least of V's scales so far, as bits
           for (int j = 0; ok && j < n; ++j, ++jb) {
             const uint32_t s = jb & 1, par = (jb >> 1) & 1, slot = jb % kScaleSlots, slot_par = (jb / kScaleSlots) & 1;
             BlockInfo& bi = sm.block[jb & (kBlockSlots - 1)];
@@ -499,16 +542,31 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 if (!((seen >> e) & 1u)) k[e] = v[e] = 0.f;
-                most = max(most, __float_as_uint(v[e]) & 0x7fffffffu);
+                const uint32_t bits = __float_as_uint(v[e]) & 0x7fffffffu;   // (an infinity or NaN: kApart)
+                most = max(most, bits);
+                if ((seen >> e) & 1u) least = min(least, bits);
               }
               most = __reduce_max_sync(0xffffffffu, most);
               const int ex = max(static_cast<int>(most >> 23) - 126, kUp - 127);   // every scale is below 2^ex
-              const float up = pow2(kUp - ex);
-              if (lane == 0) bi.ev = ex;
+              const bool apart = __any_sync(0xffffffffu, (most >> 23) > (least >> 23) + kSpread);
+              if (lane == 0) bi.ev = apart ? kApart : ex;
+              if (!apart) {
+                const float up = pow2(kUp - ex);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __half2 h = __floats2half2_rn(v[e] * up, 0.f);
-                v[e] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h));
+                for (int e = 0; e < 4; ++e) {
+                  const __half2 h = __floats2half2_rn(v[e] * up, 0.f);
+                  v[e] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h));
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t bits = __float_as_uint(v[e]);
+                  const int x = static_cast<int>(bits >> 23) & 0xff;
+                  const float exponent = x == 255 ? 0.f : static_cast<float>(max(x, 1) - 127);
+                  const __half2 h = __floats2half2_rn(
+                      x == 255 ? v[e] : x == 0 ? v[e] * pow2(126) : __uint_as_float((bits & 0x807fffffu) | 0x3f800000u), 0.f);
+                  v[e] = __uint_as_float((__float_as_uint(exponent) & 0xffff0000u) | *reinterpret_cast<const uint32_t*>(&h));
+                }
               }
               k4 = make_float4(k[0], k[1], k[2], k[3]);
               v4 = make_float4(v[0], v[1], v[2], v[3]);
@@ -602,7 +660,8 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
         continue;
       }
       float m_used = -INFINITY, l = 0.f, to_log2 = p.scale_log2;
-      int e_used = 0;   // FP8: the exponent of V's scales that O is held with
+      // FP8: O is held times 2^(kPUp - m_used + kUp - e_used); e_used is ev, or the row's own (kApart)
+      float e_used = 0.f;
       if constexpr (FP8) {
         // this half of the row of Q from bf16 to fp16, its largest value in [2^7, 2^8)
         ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.q_full, seg & 1, p.status, abort_flag));
@@ -663,6 +722,10 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
           }
           m_half = row_max64(sv) * to_log2;
         }
+        if constexpr (FP8) {   // (the other parity is free: S of this block came after the last block's reads of it)
+          if (__builtin_expect(bi.ev == kApart, 0))
+            sm.smax[(cnt + 1) & 1][x][kh][r] = row_reach64(sv, smem_u32(&sm.scale[jb % kScaleSlots][1][kh * 64]), to_log2);
+        }
         // the row maximum over both halves; the barrier also orders this half's reads of
         // S before the other half's P stores (P of keys 64..127 lands in S columns 32..63)
         sm.smax[cnt & 1][x][kh][r] = m_half;
@@ -672,20 +735,39 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
         const float m_cand = fmaxf(m_half, sm.smax[cnt & 1][x][kh ^ 1][r]);
         if (ok) {
           const bool need = m_cand > m_used + kRescaleLog2;
-          float alpha = 1.f;
+          float alpha = 1.f, down = 0.f;
           if (need) {
-            alpha = ex2_approx(m_used - m_cand);  // 0 when m_used is -inf
+            down = m_used - m_cand;
+            alpha = ex2_approx(down);  // 0 when m_used is -inf
             m_used = m_cand;
           }
           const float m_ref = (m_used == -INFINITY) ? 0.f : (FP8 ? m_used - kPUp : m_used);
-          const float sum = row_exp64<FP8>(sv, to_log2, m_ref);
-          float alpha_o = alpha;
+          float alpha_o = alpha, sum;
           bool moved = need;
           if constexpr (FP8) {
-            const int e = bi.ev;
-            moved |= e != e_used;
-            alpha_o *= pow2(e_used - e);
-            e_used = e;
+            const int ev = bi.ev;
+            if (__builtin_expect(ev == kApart, 0)) {
+              // e_used for the maximum as it is now (-inf: O holds nothing yet), then what this block's
+              // reach asks for.  The first such block may also lower it, by what O's range allows: the
+              // rows' scales were within 2^kSpread so far, so it ends at or below the row's own reach.
+              const bool first = sm.block[(jb - 1) & (kBlockSlots - 1)].ev != kApart;
+              const float m0 = m_used == -INFINITY ? 0.f : m_used;
+              const float e_was = j == 0 || m_used == -INFINITY || down == -INFINITY ? -INFINITY : e_used + down;
+              const volatile float(&reach)[2][128] = sm.smax[(cnt + 1) & 1][x];
+              const float cand = fmaxf(reach[0][r], reach[1][r]) - m0 + kUp;
+              e_used = first ? fmaxf(cand, e_was - 40.f) : cand > e_was + kRescaleLog2 ? cand : e_was;
+              if (e_used == -INFINITY) e_used = 0.f;
+              alpha_o = ex2_approx(e_was - e_used);
+              moved |= e_was != e_used;
+              sum = row_exp64_apart(sv, smem_u32(&sm.scale[jb % kScaleSlots][1][kh * 64]), to_log2, m0, kPUp + kUp - e_used);
+            } else {
+              sum = row_exp64<FP8>(sv, to_log2, m_ref);
+              moved |= ev != static_cast<int>(e_used);
+              alpha_o *= ex2_approx(e_used - ev);
+              e_used = ev;
+            }
+          } else {
+            sum = row_exp64<FP8>(sv, to_log2, m_ref);
           }
           tmem_st32(tSx + kh * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
           if (j > 0 && __any_sync(0xffffffffu, moved)) {
@@ -733,8 +815,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
       if (ok) {
         tc_fence_after();
         const bool mine = rtok < (x + 1) * p.g.TQ && rtok < ti.toks, whole = ti.part < 0;
-        // FP8: O is held times 2^(kUp - e_used), taken out in two steps that stay normal numbers
-        const float down = FP8 ? pow2(e_used) : 1.f, inv = (lsum != 0.f ? 1.f / lsum : 0.f) * (FP8 ? pow2(-kUp) : 1.f);
+        const float down = FP8 ? ex2_approx(e_used - kUp) : 1.f, inv = lsum != 0.f ? 1.f / lsum : 0.f;
         __nv_bfloat16* orow = p.out + static_cast<long long>(ti.row0 + rtok) * p.out_ld +
                               (ti.kvh * p.g.G + r % p.g.G) * DH + kh * 64;
         const long long prow = (static_cast<long long>(blockIdx.x) * 2 + ti.part) * p.part_rows + x * 128 + r;
@@ -747,9 +828,8 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
           tmem_ld16(tOx + c * 16, o);
           tmem_wait_ld();
           if constexpr (FP8) {
-            const float f = whole ? down : down * pow2(-kUp);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * down);
           }
           if (!whole) {
 #pragma unroll

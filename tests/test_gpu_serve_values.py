@@ -181,3 +181,43 @@ def test_a_large_k_row_that_a_query_does_not_see(n, cache, up):
     mine = np.concatenate([_largest_score(c, q.double().numpy(), hq, b, window) for b in range(2)]) < 2.0 ** 20
     assert mine.sum() > len(rows) // 3 or n == 1
     _close(f64(out), want, tol, rows[mine])
+
+
+@pytest.mark.parametrize("up", [12, 21, 24, 30, 45, 80])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,past", [(1, 400), (40, 400), (300, 300), (20, 2000)])
+def test_a_large_v_row_that_a_query_does_not_see(n, past, cache, up):
+    """The same for V: large rows at the window's far end and halfway through the new rows, and
+    small ones between; also with the roles of large and small exchanged."""
+    for sign in (1, -1):
+        c = Paged("bf16", cache, 2, 128, 64, [n, n], [past, past - 100], seed=34)
+        window, hq = 200, 8
+        for b in range(2):
+            lo = c.lens[b] - c.ns[b]
+            for j in (lo - window, lo - window + 1, lo + n // 2):
+                if 0 <= j < c.lens[b]:
+                    c.put(1, b, j, (2.0 ** (sign * up) * c.rng.standard_normal((1, 2, 128))).astype(np.float32))
+        c.upload()
+        q = _q(c, hq)
+        want, tol = _row_tolerance(c, q.double().numpy(), hq, 0, window)
+        out = torch.zeros((c.total, hq, 128), dtype=torch.bfloat16, device="cuda")
+        status_ok(c.attend(q.cuda(), out, hq, 0, window))
+        _close(f64(out), want, tol, np.arange(c.first[-1]))
+
+
+@pytest.mark.parametrize("n,past", [(1, 700), (90, 700), (300, 2000)])
+def test_v_scales_of_every_magnitude(n, past):
+    """V rows over 2^+-50 in random order, zero rows among them (their scale is the least one), in a
+    window and in all keys: each output row is exact beside its own largest terms."""
+    for window in (-1, 300):
+        c = Paged("bf16", "e4m3", 2, 128, 32, [n, 5], [past, 90], seed=35)
+        for b in range(2):
+            x = c.rng.standard_normal((c.lens[b], 2, 128)) * 2.0 ** c.rng.integers(-50, 50, (c.lens[b], 2, 1))
+            x[:: 7] = 0
+            c.put(1, b, 0, x.astype(np.float32))
+        c.upload()
+        q = _q(c, 8)
+        want, tol = _row_tolerance(c, q.double().numpy(), 8, 16, window)
+        out = torch.zeros((c.total, 8, 128), dtype=torch.bfloat16, device="cuda")
+        status_ok(c.attend(q.cuda(), out, 8, 16, window))
+        _close(f64(out), want, tol, np.arange(c.first[-1]))
