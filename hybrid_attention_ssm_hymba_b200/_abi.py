@@ -127,8 +127,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
 def _ptr(t) -> Optional[int]:
     try:
         return t.data_ptr()
-    except AttributeError:   # None or an address
-        return t
+    except AttributeError:
+        if t is None or isinstance(t, int):   # an address
+            return t
+        raise   # (ctypes would take bytes and str for pointers)
 
 
 def _nbytes(t) -> int:
