@@ -187,12 +187,27 @@ def make_paged_kv(pages, page_table, page_size: int, n_kv_heads: int, head_dim: 
                   scales=None) -> hymba_paged_kv_t:
     """hymba_paged_kv_t over device tensors: `pages` holds [2, n_pages, page_size, Hkv*dh]
     (any shape of that many elements), `page_table` [batch, table_ld] int32, `scales`
-    [2, n_pages, Hkv, page_size] fp32 for HYMBA_CACHE_E4M3.  The caller keeps the tensors."""
+    [2, n_pages, Hkv, page_size] fp32 for HYMBA_CACHE_E4M3.  The caller keeps the tensors.
+    Raises ValueError for tensors whose layout is not that one: the pitches come from the shapes."""
+    import torch
+    row = page_size * n_kv_heads * head_dim
+    size = {HYMBA_CACHE_F32: 4, HYMBA_CACHE_BF16: 2, HYMBA_CACHE_E4M3: 1}.get(cache_type)
+    n_pages = pages.numel() // (2 * row) if row > 0 else 0
+    for what, t in (("pages", pages), ("page_table", page_table), ("scales", scales)):
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"make_paged_kv: {what} is not contiguous")
+    if page_table.dtype != torch.int32:
+        raise ValueError(f"make_paged_kv: page_table is {page_table.dtype}, not int32")
+    if size is not None and pages.element_size() != size:
+        raise ValueError(f"make_paged_kv: pages of {pages.dtype} for a cache type of {size} bytes")
+    if row > 0 and pages.numel() != 2 * n_pages * row:
+        raise ValueError(f"make_paged_kv: {pages.numel()} elements are no whole number of K and V pages of {row}")
+    if scales is not None and (scales.dtype != torch.float32 or scales.numel() != 2 * n_pages * n_kv_heads * page_size):
+        raise ValueError(f"make_paged_kv: scales are not fp32 [2, {n_pages}, {n_kv_heads}, {page_size}]")
     kv = hymba_paged_kv_t()
     kv.pages, kv.scales, kv.page_table = _ptr(pages), _ptr(scales), _ptr(page_table)
     kv.page_size, kv.n_kv_heads, kv.head_dim, kv.cache_type = page_size, n_kv_heads, head_dim, cache_type
-    row = page_size * n_kv_heads * head_dim
-    kv.n_pages = pages.numel() // (2 * row) if row > 0 else 0
+    kv.n_pages = n_pages
     kv.table_ld = page_table.shape[-1]
     return kv
 

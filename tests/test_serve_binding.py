@@ -1,6 +1,7 @@
 """What the binding of the serving calls takes for a tensor (no GPU needed)."""
 import numpy as np
 import pytest
+import torch
 
 import hybrid_attention_ssm_hymba_b200 as H
 
@@ -16,3 +17,38 @@ def test_only_tensors_and_addresses_are_pointers(thing):
         H.hymba_quantize_w4(P, thing, P, 16, 128, 64, H.HYMBA_BF16, stream=0)
     with pytest.raises(AttributeError):
         H.hymba_workspace_status(thing, stream=0)
+
+
+def _pool(cache=torch.bfloat16, **kw):
+    a = dict(pages=torch.zeros(2, 6, 16, 2, 32, dtype=cache), page_table=torch.zeros(3, 4, dtype=torch.int32), page_size=16,
+             n_kv_heads=2, head_dim=32, cache_type=H.HYMBA_CACHE_BF16)
+    a.update(kw)
+    return a
+
+
+def test_paged_kv_of_dense_tensors():
+    kv = H.make_paged_kv(**_pool())
+    assert (kv.n_pages, kv.table_ld, kv.scales) == (6, 4, None)
+    kv = H.make_paged_kv(**_pool(torch.float8_e4m3fn, cache_type=H.HYMBA_CACHE_E4M3, scales=torch.zeros(2, 6, 2, 16)))
+    assert kv.n_pages == 6 and kv.scales
+    assert H.make_paged_kv(**_pool(pages=torch.zeros(2 * 6 * 16, 64, dtype=torch.bfloat16))).n_pages == 6
+    assert H.make_paged_kv(**_pool(page_table=torch.zeros(3, 9, dtype=torch.int32)[1:])).table_ld == 9   # rows of a table
+
+
+@pytest.mark.parametrize("bad", [
+    dict(page_table=torch.zeros(3, 9, dtype=torch.int32)[:, :4]),                # its rows are 9 apart, not 4
+    dict(page_table=torch.zeros(4, 3, dtype=torch.int32).t()), dict(page_table=torch.zeros(3, 4, dtype=torch.int64)),
+    dict(page_table=torch.zeros(3, 4)), dict(pages=torch.zeros(2, 6, 16, 2, 64, dtype=torch.bfloat16)[..., :32]),
+    dict(pages=torch.zeros(6, 2, 16, 2, 32, dtype=torch.bfloat16).transpose(0, 1)),
+    dict(pages=torch.zeros(2, 6, 16, 2, 32)), dict(pages=torch.zeros(2 * 6 * 16 * 64 + 8, dtype=torch.bfloat16)),
+    dict(pages=torch.zeros(2, 6, 16, 2, 32, dtype=torch.uint8), cache_type=H.HYMBA_CACHE_E4M3,
+         scales=torch.zeros(2, 6, 2, 32)[..., :16]),
+    dict(pages=torch.zeros(2, 6, 16, 2, 32, dtype=torch.uint8), cache_type=H.HYMBA_CACHE_E4M3,
+         scales=torch.zeros(2, 6, 2, 16, dtype=torch.bfloat16)),
+    dict(pages=torch.zeros(2, 6, 16, 2, 32, dtype=torch.uint8), cache_type=H.HYMBA_CACHE_E4M3, scales=torch.zeros(2, 5, 2, 16)),
+])
+def test_paged_kv_refuses_what_it_would_misread(bad):
+    """The descriptor's pitches come from the shapes: strided tensors, or elements of another size, would
+    be read as other rows without an error."""
+    with pytest.raises(ValueError):
+        H.make_paged_kv(**_pool(**bad))
