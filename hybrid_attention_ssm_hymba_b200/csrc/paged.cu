@@ -367,12 +367,18 @@ __global__ void __launch_bounds__(128) paged_join_simt(const PagedAttnDesc p, in
 // CTAs over which the keys of a row are split: four CTAs per SM of the B200 in all, and no piece
 // shorter than 128 keys of the longest sequence that the table holds (one token over 4000 rows: 27 us,
 // unsplit 425).
-int simt_splits(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads) {
-  const long long ctas = static_cast<long long>(rb.total_rows) * kv.hkv * ((n_q_heads / kv.hkv + kSimtHeads - 1) / kSimtHeads);
+constexpr long long kSimtCtas = 4 * 148;
+long long simt_row_ctas(const PagedKv& kv, int n_q_heads) {   // without a split
+  return static_cast<long long>(kv.hkv) * ((n_q_heads / kv.hkv + kSimtHeads - 1) / kSimtHeads);
+}
+long long simt_most_splits(const PagedKv& kv) {
   const long long most = (static_cast<long long>(kv.table_ld) * kv.page_size + 127) / 128;
-  long long s = ctas > 0 ? 4 * 148 / ctas : 1;
-  s = s < most ? s : most;
-  return s < 1 ? 1 : s > 64 ? 64 : static_cast<int>(s);
+  return most < 64 ? most : 64;
+}
+int simt_splits(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads) {
+  const long long ctas = rb.total_rows * simt_row_ctas(kv, n_q_heads), most = simt_most_splits(kv);
+  const long long s = ctas > 0 ? kSimtCtas / ctas : 1;
+  return s < 1 ? 1 : static_cast<int>(s < most ? s : most);
 }
 
 }  // namespace
@@ -396,8 +402,10 @@ cudaError_t launch_paged_attention_tc(const PagedAttnDesc& a, cudaStream_t st);
 
 size_t paged_attention_scratch(const PagedKv& kv, const RaggedBatch& rb, int n_q_heads, bool bf16) {
   if (!bf16) {
-    const int s = simt_splits(kv, rb, n_q_heads);
-    return s == 1 ? 0 : static_cast<size_t>(rb.total_rows) * n_q_heads * s * (kv.dh + 2) * 4;
+    // rows x splits: fewer rows are split further, so that what holds the most rows' parts holds any
+    // smaller call's (a server's one workspace)
+    const long long any = kSimtCtas / simt_row_ctas(kv, n_q_heads), most = simt_most_splits(kv), all = rb.total_rows * most;
+    return any < 2 || most < 2 ? 0 : static_cast<size_t>(any < all ? any : all) * n_q_heads * (kv.dh + 2) * 4;
   }
   return paged_decode_takes(kv, rb, n_q_heads) ? paged_decode_scratch(kv, rb, n_q_heads) : paged_attention_tc_scratch(kv, rb, n_q_heads);
 }

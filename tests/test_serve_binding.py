@@ -52,3 +52,21 @@ def test_paged_kv_refuses_what_it_would_misread(bad):
     be read as other rows without an error."""
     with pytest.raises(ValueError):
         H.make_paged_kv(**_pool(**bad))
+
+
+@pytest.mark.parametrize("dtype,cache", [(H.HYMBA_F32, H.HYMBA_CACHE_F32), (H.HYMBA_F32, H.HYMBA_CACHE_E4M3),
+                                         (H.HYMBA_BF16, H.HYMBA_CACHE_BF16), (H.HYMBA_BF16, H.HYMBA_CACHE_E4M3)])
+@pytest.mark.parametrize("hq,hkv,table_ld", [(16, 4, 512), (1, 1, 3), (48, 1, 40), (4, 4, 1), (64, 64, 2048)])
+def test_a_workspace_for_the_largest_call_serves_smaller_ones(hq, hkv, table_ld, dtype, cache):
+    """Sizes do not shrink as batch, rows or the longest chunk grow."""
+    kv = H.hymba_paged_kv_t()
+    for name, v in dict(pages=P, scales=P, page_table=P, n_pages=1000, page_size=64, table_ld=table_ld, n_kv_heads=hkv,
+                        head_dim=128, cache_type=cache).items():
+        setattr(kv, name, v)
+
+    def size(batch, total, most):
+        return H.hymba_paged_attention_workspace_size(kv, batch, total, most, hq, dtype)
+
+    for sizes in ([size(8, total, 8) for total in range(0, 700)], [size(8, 700, most) for most in range(1, 700)],
+                  [size(batch, 700, 8) for batch in range(1, 2000, 7)]):
+        assert min(sizes) >= 256 and sizes == sorted(sizes)
