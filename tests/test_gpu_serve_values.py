@@ -221,3 +221,24 @@ def test_v_scales_of_every_magnitude(n, past):
         out = torch.zeros((c.total, 8, 128), dtype=torch.bfloat16, device="cuda")
         status_ok(c.attend(q.cuda(), out, 8, 16, window))
         _close(f64(out), want, tol, np.arange(c.first[-1]))
+
+
+@pytest.mark.parametrize("n,batch", [(1, 200), (90, 3)])
+@pytest.mark.parametrize("up", [0, 60, 75])
+def test_rising_scores_with_large_values(n, batch, up):
+    """Scores that rise by 50 powers of two after the first keys, over V rows of 2^up, in enough
+    sequences that a CTA takes several blocks of one: sums that are held relative to an early
+    maximum stay finite."""
+    c = Paged("bf16", "e4m3", 1, 128, 64, [n] * batch, [600] * batch, seed=36)
+    k = np.zeros((c.lens[0], 1, 128), np.float32)
+    k[128:, 0, 0] = 50 / (8 * 1.4426950408889634 / np.sqrt(128))
+    for b in range(batch):
+        c.put(0, b, 0, k)
+        c.put(1, b, 0, (2.0 ** up * (2 + c.rng.random((c.lens[b], 1, 128)))).astype(np.float32))
+    c.upload()
+    q = torch.zeros(c.total, 4, 128, dtype=torch.bfloat16)
+    q[:, :, 0] = 8
+    want, tol = _row_tolerance(c, q.double().numpy(), 4, 0, -1)
+    out = torch.zeros((c.total, 4, 128), dtype=torch.bfloat16, device="cuda")
+    status_ok(c.attend(q.cuda(), out, 4, 0, -1))
+    _close(f64(out), want, tol, np.arange(c.first[-1]))
