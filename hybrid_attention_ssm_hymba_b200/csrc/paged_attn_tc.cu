@@ -702,6 +702,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
         float m_half = -INFINITY;
         const volatile BlockInfo& bi = sm.block[jb & (kBlockSlots - 1)];
         const uint32_t flags = bi.flags;
+        const int ev = FP8 ? bi.ev : 0;
         if (ok) {
           tc_fence_after();
           tmem_ld32(tSx + kh * 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
@@ -723,7 +724,7 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
           m_half = row_max64(sv) * to_log2;
         }
         if constexpr (FP8) {   // (the other parity is free: S of this block came after the last block's reads of it)
-          if (__builtin_expect(bi.ev == kApart, 0))
+          if (__builtin_expect(ev == kApart, 0))
             sm.smax[(cnt + 1) & 1][x][kh][r] = row_reach64(sv, smem_u32(&sm.scale[jb % kScaleSlots][1][kh * 64]), to_log2);
         }
         // the row maximum over both halves; the barrier also orders this half's reads of
@@ -745,7 +746,6 @@ __global__ void __launch_bounds__(FP8 ? kThreadsFp8 : kThreads, 1)
           float alpha_o = alpha, sum;
           bool moved = need;
           if constexpr (FP8) {
-            const int ev = bi.ev;
             if (__builtin_expect(ev == kApart, 0)) {
               // e_used for the maximum as it is now (-inf: O holds nothing yet), then what this block's
               // reach asks for.  The first such block may also lower it, by what O's range allows: the
