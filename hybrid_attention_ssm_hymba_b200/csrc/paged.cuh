@@ -65,6 +65,14 @@ HY_DEV long long page_scale(const PagedKv& kv, int which, int page, int row, int
   return ((static_cast<long long>(which) * kv.n_pages + page) * kv.hkv + head) * kv.page_size + row;
 }
 
+// Two e4m3 codes (the low or the high half of u) as fp16.
+HY_DEV uint32_t f16_of_e4m3(uint32_t u, int half) {
+  uint32_t v;
+  if (half) asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, hi;}" : "=r"(v) : "r"(u));
+  else asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, lo;}" : "=r"(v) : "r"(u));
+  return v;
+}
+
 // ------------------------------------------------------------------ eight elements as fp32
 template <typename T> struct Vec8;  // how a lane moves eight consecutive elements
 template <> struct Vec8<float> {

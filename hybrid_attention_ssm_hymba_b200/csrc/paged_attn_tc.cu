@@ -147,13 +147,6 @@ __device__ __forceinline__ void scale64(uint32_t (&sv)[64], uint32_t vec) {
     sv[4 * q + 3] = __float_as_uint(b.y);
   }
 }
-// Two e4m3 codes (the low or the high half of u) as fp16.
-__device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t u, int half) {
-  uint32_t v;
-  if (half) asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, hi;}" : "=r"(v) : "r"(u));
-  else asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, lo;}" : "=r"(v) : "r"(u));
-  return v;
-}
 // FP8, a kApart block: the exponent of V's scale from its word.
 __device__ __forceinline__ float v_exponent(float word) { return __uint_as_float(__float_as_uint(word) & 0xffff0000u); }
 // The largest of s sc + e, e the exponent of V's scale: what the terms of P V reach.

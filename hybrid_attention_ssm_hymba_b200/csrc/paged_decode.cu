@@ -63,13 +63,6 @@ __device__ __forceinline__ uint4 ldg_once(const void* p) {
   return v;
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-// Two e4m3 codes (the low or the high half of u) as fp16.
-__device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t u, int half) {
-  uint32_t v;
-  if (half) asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, hi;}" : "=r"(v) : "r"(u));
-  else asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, lo;}" : "=r"(v) : "r"(u));
-  return v;
-}
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
