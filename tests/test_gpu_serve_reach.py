@@ -108,3 +108,26 @@ def test_one_workspace_for_calls_of_every_size():
         status_ok(ws)
         want, tol = c.attention(qd, 4, 0, -1)
         _check(f64(out), want, tol)
+
+
+@pytest.mark.parametrize("dtype,cache,ns", [("bf16", "bf16", [1, 1]), ("bf16", "e4m3", [90, 300]), ("f32", "f32", [2, 1])])
+def test_two_streams_at_once(dtype, cache, ns):
+    """Two streams over one cache, each with its workspace: the bits of a call alone."""
+    c = Paged(dtype, cache, 2, 128, 64, ns, [700, 500], seed=47).upload()
+    q, _ = _q(c, 8)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [c.workspace(8) for _ in range(2)]
+    outs = [torch.zeros((c.total, 8, 128), dtype=TORCH[dtype], device="cuda") for _ in range(2)]
+    ref = torch.zeros_like(outs[0])
+    c.attend(q, ref, 8, 16, 300, ws=ws[0])
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for o, w, s in zip(outs, ws, streams):
+            with torch.cuda.stream(s):
+                o.zero_()
+                for _ in range(5):
+                    c.attend(q, o, 8, 16, 300, ws=w, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], ref) and torch.equal(outs[1], ref)
+    for w in ws:
+        status_ok(w)
