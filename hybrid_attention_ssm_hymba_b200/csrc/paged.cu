@@ -43,10 +43,11 @@ HY_DEV float div448(float m) {
 template <typename C, bool WRITE> HY_DEV constexpr int lane_vectors() { return WRITE && sizeof(C) == 1 ? 2 : 1; }
 
 // WRITE: x (the batch's rows) -> cache; else cache -> x.  T: element type of x, C: of the cache.
-// Bound by HBM when there are many rows; what competes are the instructions around each vector,
-// so a thread keeps its place in a row (K or V, head, elements) and walks the rows.  33280 rows of
-// 4 x 128 from bf16 into e4m3: 24.1 us, 4.3 TB/s (65 % of the measured copy rate); back: 21.7 us,
-// 4.7 TB/s (71 %); 21.7 and 17.6 where the inputs are in L2.
+// Many rows: HBM sets the floor; most stalls are waits for the loads, at 7 CTAs of work an SM of which
+// five fit at a time, and the scheduler issues in 54 % (into e4m3) and 61 % (back) of its cycles.  A
+// thread keeps its place in a row (K or V, head, elements) and walks the rows, to keep what it does
+// around each vector small.  33280 rows of 4 x 128 from bf16 into e4m3: 24.1 us, 4.3 TB/s (65 % of
+// the measured copy rate); back: 21.7 us, 4.7 TB/s (71 %); 21.8 and 17.8 one behind another.
 template <typename T, typename C, bool WRITE, int ROWS>
 __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const PagedKv kv, const RaggedBatch rb, T* xk, T* xv,
                                                                   long long ld, int lpu, unsigned* status) {
@@ -180,10 +181,11 @@ cudaError_t launch_copy(const PagedKv& kv, const RaggedBatch& rb, void* k, void*
 // its query heads).  A warp takes 32 of the visible keys (meta rows below the window, then the
 // window up to the row itself) at a time: lane = key for the scores (its K row against the queries
 // in shared memory), lane = dims for P V (whole V rows, eight in flight); online softmax, the warps
-// joined at the end.  Fp32 products have no tensor-core form that keeps their 24 bits; what bounds
-// this kernel is its FMAs and the re-reading of K and V by every row (L2); 1100 rows of 16 x 128 over
-// up to 1000 each take 660 us.  With few rows the keys
-// of a row are split over `splits` CTAs, each leaving its unnormalised output, m and sum per head
+// joined at the end.  What bounds this kernel is the re-reading of K and V by every row (L2, where a
+// lane's K row is not its neighbour's: L1 is busy in 65 % of the cycles, the scheduler in 34 %);
+// 4 x 275 rows of 16 x 128 over 275 to 1000 keys each take 766 us.  (The products could run on the
+// tensor cores with each fp32 operand in three bf16 parts, as in w4.cu; this kernel does not.)  With
+// few rows the keys of a row are split over `splits` CTAs, each leaving its unnormalised output, m and sum per head
 // in part[(row * Hq + head) * splits + split][dh + 2]; paged_join_simt joins them.
 constexpr int kSimtWarps = 4, kSimtHeads = 8, kSimtDh = 128;
 

@@ -32,10 +32,10 @@
 // Bound by the round of a group: S (tensor core), softmax, P V, one after another, with the other
 // group's round half a turn behind.  4096 rows of 16 heads over 32K bf16 rows: 970 us, 1066 TFLOP/s,
 // 64 % of the measured bf16 rate; of a round's 4100 cycles the softmax takes 1900 and the tensor core
-// 2050 for both groups.  e4m3 rows: 1306 us; reading K's scales and converting share the shared
+// 2050 for both groups.  e4m3 rows: 1290 us; reading K's scales and converting share the shared
 // memory with the products.  Nine ragged sequences of up to 1604 e4m3 rows in a window of 1024 (16
-// blocks a CTA): 90 us, of which 16 blocks take 51; starting up, and per tile Q's conversion, the
-// first S and the output take the rest.  A third group per CTA has no TMEM left, and one group with
+// blocks a CTA): 94 us, of which 16 blocks take about 51; starting up, and per tile Q's conversion,
+// the first S and the output take the rest.  A third group per CTA has no TMEM left, and one group with
 // twice the keys would read every K/V row twice as often.
 //
 // Rows of V that no query of the tile sees (behind the sequence, between the meta rows and
@@ -56,7 +56,7 @@ constexpr int kUp = 7;         // FP8: V's scales are held below 2^kUp, code tim
 constexpr float kPUp = 11.f;   // FP8: P is 2^(s - m + kPUp)
 // FP8: V's scales of a tile stand in V as they are while their exponents differ by at most this.  Beyond,
 // a block takes a second exponential: scales of 2^+-15 in random order, 4096 rows over 32K keys 2110 us
-// against 1295, ragged chunks 132 against 97.  (Always so, the usual scales would pay it too.)
+// against 1290, ragged chunks 132 against 96.  (Always so, the usual scales would pay it too.)
 constexpr int kSpread = 20;
 constexpr int kApart = 1 << 20;   // BlockInfo::ev of such a block
 // FP8: a row of Q is scaled up by at most 2^kMostUp, so that the factor from S to log2 units stays

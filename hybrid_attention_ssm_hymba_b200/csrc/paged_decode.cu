@@ -25,7 +25,7 @@
 //
 // e4m3 codes are exact in fp16, one conversion for two of them, so the 8-bit products run in
 // fp16 with their ranges kept by powers of two: a row of Q is scaled to at most 2^8 (its bf16
-// values stay exact down to 2^-32 of the largest), and P V sums n_j = 2^(s_j + log2 sv_j - m' + 8)
+// values stay exact down to 2^-25 of the largest), and P V sums n_j = 2^(s_j + log2 sv_j - m' + 8)
 // times the codes, with a running maximum m' of its own, while sum_j 2^(s_j - m) is kept apart.
 #include "paged_plan.cuh"
 

@@ -6,8 +6,10 @@ namespace hy {
 namespace {
 
 // Eight weights per lane and two (fp32) or four (bf16) such vectors in flight; the group / 8 lanes of a group share
-// its maximum by shuffles.  HBM bound: 2 or 4 bytes in and half a byte out per weight; 11264 x 2048
-// from bf16 and back 25.9 us (4.0 TB/s, 61 % of the measured copy rate).  In flight, there and back:
+// its maximum by shuffles.  HBM sets the floor: 2 or 4 bytes in and half a byte out per weight; 11264 x
+// 2048 from bf16 and back 25.9 us (4.0 TB/s, 61 % of the measured copy rate).  What bounds it: quantising
+// from bf16, two thirds of that time, issues in 78 % of the cycles (the nearest-even quotients); going back
+// waits for its loads and for L1 (71 % busy).  In flight, there and back:
 // bf16 2, 4, 8 vectors 26.4, 25.6, 28.3 us; fp32 (2048 x 2048) 2, 4: 11.9, 17.7.
 template <typename T> constexpr int kQuantAhead = sizeof(T) == 4 ? 2 : 4;
 
@@ -102,10 +104,14 @@ __global__ void __launch_bounds__(256) dequantize_w4_kernel(const uint32_t* __re
 // all its tiles are shared out evenly: each warp streams its own through a ring of its own by cp.async,
 // and the parts of a tile meet in shared memory at the slab's end, in the warps' order.  Eight rows
 // against 16384 x 8192: 25.4 us (3.0 TB/s, 46 % of the measured copy rate); four against 11264 x 5632:
-// 14.6.  (Each tile shared by a fixed number of warps, so that a CTA takes whole rounds: 26.3 and 18.9;
-// the next slab's first chunks not under way while the parts meet: 27.0 and 15.5.)  The stream alone
+// 14.6.  One change at a time: each tile shared by a fixed number of warps, a CTA in whole rounds, 26.3 and
+// 18.9; chunks in even shares 26.9 and 15.4 (uneven rounds cost the four rows most, and the eight nothing);
+// the next slab's first chunks under way while the parts meet 25.4 and 14.6.  The stream alone
 // takes 14 us, taking the nibbles apart and the products alone 20, at four warps an SM quarter
-// that issue in half of the cycles.  One row against 2048 x 5632: 5.6 us, a launch and a chunk's way.
+// that issue in half of the cycles.  One row against 2048 x 5632: 5.7 us, a launch and two slabs (A is
+// laid out for eight columns whatever the rows, so that 4096 k fill shared memory).  Sixteen rows against
+// 16384 x 8192: 36 us; fp32 rows, three columns each: eight 75, sixteen 194 (six tiles of columns leave
+// slabs of 512 k and a ring of two, whose parts meet every two chunks).
 //
 // The 32 k of 16 bytes of a row are one or part of one group; lane (g, t) takes 4 of them
 // (8 k) of rows g and g + 8.  A word's nibbles i and i + 4 make one bf16 pair: (word >> 4 i)

@@ -476,12 +476,20 @@ HYMBA_API hymba_status_t hymba_paged_kv_read(const hymba_paged_kv_t* kv, void* k
  *   max_rows  bounds every n_b (1: a generation step)
  *   bf16: dh 128 and at most 128 query heads per K/V head; f32: dh a multiple of 16 up to
  *   128; pointers 16-byte aligned, row strides a multiple of 16 bytes
- * Cache rows no query of the call sees may hold anything, NaN included.  A visible K or V
- * that is not finite reaches the rows that see it and, where several queries are handled
- * together, may reach others of the same sequence.  A row that sees no key (every page
- * number it needs was invalid) gives 0.
- * Workspace: hymba_paged_attention_workspace_size bytes, 256-byte aligned.  Calls that share
- * one (also through captured graphs) must be ordered.
+ * Cache rows no query of the call sees may hold anything, NaN included.  A NaN in a row of q,
+ * or a visible K or V that is not finite, reaches the rows that see it and, for K and V, where
+ * several queries are handled together, may reach others of the same sequence.  A row that sees
+ * no key (every page number it needs was invalid), or whose scores are all -infinity, gives 0.
+ * Maxima, sums and outputs are held in fp32.  bf16 calls round each softmax numerator once to 16
+ * bits (bf16, or fp16 over an e4m3 cache), as hymba_attention does, and take exponentials to about
+ * 2^-22; over an e4m3 cache a tile of many rows also holds code times scale of V in fp16's 11 bits.
+ * K and V rows of any magnitude may stand side by side: over an e4m3 cache a row keeps its terms
+ * p v down to 2^-33 of its own largest (V scales more than 2^20 apart within a tile take longer).  Range of the bf16 calls: scores q.k / sqrt(dh) up to 2^20 in
+ * magnitude (a row with larger ones may give anything, also NaN; other rows keep theirs), v up
+ * to 2^90.
+ * Workspace: hymba_paged_attention_workspace_size bytes, 256-byte aligned; the size does not
+ * shrink as batch, total_rows and max_rows grow, so that the largest call's serves the others.
+ * Calls that share one (also through captured graphs) must be ordered.
  */
 HYMBA_API size_t hymba_paged_attention_workspace_size(const hymba_paged_kv_t* kv, int batch, int total_rows,
                                                       int max_rows, int n_q_heads, hymba_dtype_t dtype);
