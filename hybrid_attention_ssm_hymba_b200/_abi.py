@@ -193,8 +193,9 @@ def make_paged_kv(pages, page_table, page_size: int, n_kv_heads: int, head_dim: 
     row = page_size * n_kv_heads * head_dim
     size = {HYMBA_CACHE_F32: 4, HYMBA_CACHE_BF16: 2, HYMBA_CACHE_E4M3: 1}.get(cache_type)
     n_pages = pages.numel() // (2 * row) if row > 0 else 0
-    for what, t in (("pages", pages), ("page_table", page_table), ("scales", scales)):
-        if t is not None and not t.is_contiguous():
+    quantised = cache_type == HYMBA_CACHE_E4M3 and scales is not None
+    for what, t in (("pages", pages), ("page_table", page_table)) + ((("scales", scales),) if quantised else ()):
+        if not t.is_contiguous():
             raise ValueError(f"make_paged_kv: {what} is not contiguous")
     if page_table.dtype != torch.int32:
         raise ValueError(f"make_paged_kv: page_table is {page_table.dtype}, not int32")
@@ -202,7 +203,7 @@ def make_paged_kv(pages, page_table, page_size: int, n_kv_heads: int, head_dim: 
         raise ValueError(f"make_paged_kv: pages of {pages.dtype} for a cache type of {size} bytes")
     if row > 0 and pages.numel() != 2 * n_pages * row:
         raise ValueError(f"make_paged_kv: {pages.numel()} elements are no whole number of K and V pages of {row}")
-    if scales is not None and (scales.dtype != torch.float32 or scales.numel() != 2 * n_pages * n_kv_heads * page_size):
+    if quantised and (scales.dtype != torch.float32 or scales.numel() != 2 * n_pages * n_kv_heads * page_size):
         raise ValueError(f"make_paged_kv: scales are not fp32 [2, {n_pages}, {n_kv_heads}, {page_size}]")
     kv = hymba_paged_kv_t()
     kv.pages, kv.scales, kv.page_table = _ptr(pages), _ptr(scales), _ptr(page_table)

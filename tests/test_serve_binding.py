@@ -32,6 +32,7 @@ def test_paged_kv_of_dense_tensors():
     kv = H.make_paged_kv(**_pool(torch.float8_e4m3fn, cache_type=H.HYMBA_CACHE_E4M3, scales=torch.zeros(2, 6, 2, 16)))
     assert kv.n_pages == 6 and kv.scales
     assert H.make_paged_kv(**_pool(pages=torch.zeros(2 * 6 * 16, 64, dtype=torch.bfloat16))).n_pages == 6
+    H.make_paged_kv(**_pool(scales=torch.zeros(1)))   # (a cache that has no scales does not look at them)
     assert H.make_paged_kv(**_pool(page_table=torch.zeros(3, 9, dtype=torch.int32)[1:])).table_ld == 9   # rows of a table
 
 
